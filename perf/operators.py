@@ -251,9 +251,9 @@ def work(case):
 # ---------------------------------------------------------------------- exact
 def _e4m3_64(v):
     """Nearest E4M3 value (ties to even) of |v| <= 448, in 64 bits."""
-    _, e = torch.frexp(v)
-    step = torch.ldexp(torch.ones_like(v), (e - 1).clamp(min=-6) - 3)
-    return torch.round(v / step) * step
+    m, _ = torch.frexp(v)  # |m| in [1/2, 1): four bits of it stay
+    normal = torch.round(m * 16) / 16 * (v / torch.where(m == 0, torch.ones_like(m), m))
+    return torch.where(v.abs() < 2.0 ** -6, torch.round(v * 512) / 512, normal)
 
 
 def _linear_64(x, st):
@@ -262,7 +262,7 @@ def _linear_64(x, st):
     n, k = torch.arange(N, device=w.device) // BLOCK, torch.arange(K, device=w.device) // BLOCK
     amax = torch.zeros(x.shape[0], _blocks(K), dtype=torch.float64, device=w.device)
     amax.scatter_reduce_(1, k.expand(x.shape[0], K), x.abs(), "amax")
-    s = torch.where(amax > 0, amax / E4M3_MAX, torch.ones_like(amax))[:, k]
+    s = torch.where(amax > 0, amax / torch.full_like(amax, E4M3_MAX), torch.ones_like(amax))[:, k]
     return (_e4m3_64(x / s) * s) @ (w * ws[n][:, k]).t()
 
 

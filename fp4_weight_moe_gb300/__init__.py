@@ -1,4 +1,6 @@
-"""GB300-native fused FP4-weight mixture-of-experts layer.
+"""GB300-native fused FP4-weight mixture-of-experts layer, and the operators
+around it (FP8 block-scaled products, norms, the router's choice; see
+``ops``).
 
 The compute path is ``libmoe_fp4.so`` (hand-written CUDA for sm_103a behind a
 C ABI, see ``include/moe_fp4.h``).  This package is its thin Python binding:
@@ -305,3 +307,16 @@ def workspace_status(workspace: Optional[torch.Tensor] = None, clear: bool = Fal
 def noalloc_status(clear: bool = False, stream=None) -> int:
     """Status word of moe_fp4_forward_noalloc's scratch array on the current device."""
     return _capi.moe_fp4_noalloc_status(clear, _stream(stream))
+
+
+from .ops import (  # noqa: E402,F401
+    SCORE_SIGMOID,
+    SCORE_SOFTMAX,
+    alloc_fp8_workspace,
+    block_norm,
+    fp8_linear,
+    fp8_matmul,
+    fp8_quantize,
+    fp8_status,
+    route_topk,
+)

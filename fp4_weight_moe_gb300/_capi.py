@@ -31,6 +31,8 @@ MOE_FP4_ACT_RELU2 = 3
 MOE_FP4_PREFILL_NVFP4 = 0
 MOE_FP4_PREFILL_BF16 = 1
 MOE_FP4_PREFILL_W4A8_MX = 2
+MOE_FP4_SCORE_SOFTMAX = 0
+MOE_FP4_SCORE_SIGMOID = 1
 MOE_FP4_STATUS_OK = 0
 MOE_FP4_STATUS_TEST_WAIT = 8192
 
@@ -41,10 +43,25 @@ class MoeFp4Activation(ctypes.Structure):
                 ("limit", ctypes.c_float)]
 
 
+class MoeFp4BlockNormArgs(ctypes.Structure):
+    """struct moe_fp4_block_norm_args."""
+    _fields_ = [("residual", ctypes.c_void_p), ("residual_row", ctypes.c_int64), ("block_out", ctypes.c_void_p),
+                ("block_row", ctypes.c_int64), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("gate_row", ctypes.c_int64), ("gate_col", ctypes.c_int64),
+                ("residual_out", ctypes.c_void_p), ("residual_out_row", ctypes.c_int64), ("normed", ctypes.c_void_p),
+                ("normed_row", ctypes.c_int64), ("q", ctypes.c_void_p), ("q_row", ctypes.c_int64),
+                ("s", ctypes.c_void_p), ("s_row", ctypes.c_int64), ("s_block", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("offset", ctypes.c_float),
+                ("residual_f32", ctypes.c_int), ("weights_f32", ctypes.c_int), ("gate_f32", ctypes.c_int),
+                ("M", ctypes.c_int), ("H", ctypes.c_int)]
+
+
 # (name, restype, argtypes) for every symbol declared in include/moe_fp4.h
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
 _PZ = ctypes.POINTER(ctypes.c_size_t)
 SIGNATURES = {
     "moe_fp4_status_string": (ctypes.c_char_p, [_I]),
@@ -89,6 +106,13 @@ SIGNATURES = {
     "moe_fp4_workspace_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32), _I, _P]),
     "moe_fp4_noalloc_status": (_I, [ctypes.POINTER(ctypes.c_uint32), _I, _P]),
     "moe_fp4_debug_wait_timeout": (_I, [_P, ctypes.c_uint, _P]),
+    "moe_fp4_fp8_quantize": (_I, [_P, _L, ctypes.POINTER(MoeFp4Activation), _P, _L, _P, _L, _L, _I, _I, _P]),
+    "moe_fp4_fp8_matmul": (_I, [_P, _L, _P, _L, _L, _P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _P]),
+    "moe_fp4_fp8_linear_workspace_bytes": (_Z, [_I, _I]),
+    "moe_fp4_fp8_linear": (_I, [_P, _L, _P, _L, _P, _L, _P, _L, _P, _L, _I, _I, _I, _I, _P, _Z, _P]),
+    "moe_fp4_fp8_status": (_I, [ctypes.POINTER(ctypes.c_uint32), _I, _P]),
+    "moe_fp4_block_norm": (_I, [ctypes.POINTER(MoeFp4BlockNormArgs), _P]),
+    "moe_fp4_route_topk": (_I, [_P, _L, _I, _P, _I, _I, _F, _P, _P, _I, _I, _I, _P]),
     "moe_fp4_debug_decode_plan": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int)]),
 }
 
@@ -329,6 +353,48 @@ def moe_fp4_debug_decode_plan(M, E, H, I, top_k):
     v = (ctypes.c_int * 4)()
     _check("moe_fp4_debug_decode_plan", lib().moe_fp4_debug_decode_plan(M, E, H, I, top_k, v))
     return tuple(v)
+
+
+def moe_fp4_fp8_quantize(x, x_row, act, q, q_row, s, s_row, s_block, M, K, stream):
+    """``act``: None (x itself) or a MoeFp4Activation (x = [gate | up])."""
+    return _check("moe_fp4_fp8_quantize",
+                  lib().moe_fp4_fp8_quantize(x, x_row, None if act is None else ctypes.byref(act), q, q_row, s, s_row,
+                                             s_block, M, K, stream))
+
+
+def moe_fp4_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32,
+                       M, N, K, stream):
+    return _check("moe_fp4_fp8_matmul",
+                  lib().moe_fp4_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, w_s, ws_row, add, add_row,
+                                           out, out_row, out_f32, M, N, K, stream))
+
+
+def moe_fp4_fp8_linear_workspace_bytes(M_max, K) -> int:
+    return int(lib().moe_fp4_fp8_linear_workspace_bytes(M_max, K))
+
+
+def moe_fp4_fp8_linear(x, x_row, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32, M, N, K, ws, ws_bytes,
+                       stream):
+    return _check("moe_fp4_fp8_linear",
+                  lib().moe_fp4_fp8_linear(x, x_row, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32, M, N,
+                                           K, ws, ws_bytes, stream))
+
+
+def moe_fp4_fp8_status(clear: bool, stream) -> int:
+    v = ctypes.c_uint32(0)
+    _check("moe_fp4_fp8_status", lib().moe_fp4_fp8_status(ctypes.byref(v), int(bool(clear)), stream))
+    return v.value
+
+
+def moe_fp4_block_norm(args: MoeFp4BlockNormArgs, stream):
+    return _check("moe_fp4_block_norm", lib().moe_fp4_block_norm(ctypes.byref(args), stream))
+
+
+def moe_fp4_route_topk(logits, logits_row, logits_f32, bias, score, renormalize, scale, ids, weights, M, E, top_k,
+                       stream):
+    return _check("moe_fp4_route_topk",
+                  lib().moe_fp4_route_topk(logits, logits_row, logits_f32, bias, score, renormalize, scale, ids,
+                                           weights, M, E, top_k, stream))
 
 
 def raw_status(name: str, *args) -> int:

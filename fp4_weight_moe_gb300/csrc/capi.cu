@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "tcgen05.cuh"
 
 namespace moe_fp4 {
@@ -77,14 +78,21 @@ int check_layer_shape(int E, int H, int I, int top_k, int fmt) {
 }  // namespace moe_fp4
 
 namespace {
-
 thread_local int g_last_cuda_error = 0;
-constexpr size_t kMaxWorkspace = (size_t)1 << 31;  // workspaces past 2^31 bytes are rejected
+}
 
-int fail_cuda(cudaError_t e) {
+namespace moe_fp4 {
+int report_cuda_error(cudaError_t e) {
   g_last_cuda_error = (int)e;
   return MOE_FP4_ECUDA;
 }
+}  // namespace moe_fp4
+
+namespace {
+
+constexpr size_t kMaxWorkspace = (size_t)1 << 31;  // workspaces past 2^31 bytes are rejected
+
+int fail_cuda(cudaError_t e) { return report_cuda_error(e); }
 
 int device_sms(int* sms) {
   int dev = 0;

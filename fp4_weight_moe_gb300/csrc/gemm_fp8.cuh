@@ -1,0 +1,352 @@
+// E4M3 x E4M3 products with FP32 scales per block of 128 on the
+// 5th-generation tensor cores (sm_103a):
+//   D[m][n] = sum_b sx[m][b] sw[n / 128][b] sum_{k in b} X[m][k] W[n][k],
+// b the 128-K blocks, X and W E4M3 (K-major rows), the inner sums in tensor
+// memory (tcgen05.mma kind::f8f6f4), the outer one in FP32 registers: a
+// scale per 128 K cannot ride on the MMA (its block scales are powers of
+// two per 32 K), so every K block gets an accumulator of its own, which the
+// scale warps read, scale and add up while the next block multiplies.
+//
+// A CTA computes 128 x BN tiles in turn with 2 + 4 * kHalves warps:
+//   warp 0 lane 0  TMA producer: per K block the 128-row box (128 x 128 B)
+//                  and the BN-row box, SWIZZLE_128B, into a ring;
+//   warp 1         allocates tensor memory and, converged, issues the four
+//                  K = 32 MMAs of a block into accumulator g % kAcc, then
+//                  commits that free the stage and publish the accumulator;
+//   scale warps    each reads its 32 accumulator lanes (and its half of the
+//                  columns where BN >= 64), adds them, scaled, into
+//                  registers, and stores the finished tile.
+// The scales of 16 K blocks at a time are copied to shared memory
+// (cp.async, any strides) one chunk ahead, across tile boundaries too.
+//
+// The 128-row operand is X (kSwap = false) or W (kSwap = true: few tokens,
+// the tokens on the MMA's N side).
+#pragma once
+
+#include "common.cuh"
+#include "tcgen05.cuh"
+
+namespace moe_fp4 {
+
+constexpr int kF8BM = 128;
+constexpr int kF8BK = 128;     // K elements (= bytes) per stage: one scale block
+constexpr int kF8Chunk = 16;   // K blocks of scales per shared-memory chunk
+
+struct Fp8Args {
+  const float* xs;  // activation scales, xs[m * xs_row + b * xs_blk]
+  int64_t xs_row, xs_blk;
+  const float* ws;  // weight scales, ws[(n / 128) * ws_row + b]
+  int64_t ws_row;
+  const __nv_bfloat16* add;  // added to the product before its rounding (or null)
+  int64_t add_row;
+  void* out;
+  int64_t out_row;
+  int out_f32;
+  int vec;  // out (and add) rows start 16-byte aligned
+  int M, N, K;
+  uint32_t* err;
+};
+
+template <int BN, bool kSwap>
+struct F8Cfg {
+  static constexpr int kHalves = BN >= 64 ? 2 : 1;
+  static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
+  static constexpr int kScaleWarps = 4 * kHalves;
+  static constexpr int kThreads = 32 * (2 + kScaleWarps);
+  static constexpr int kAcc = BN >= 256 ? 2 : 4;
+  static constexpr uint32_t kTmemCols = kAcc * BN < 32 ? 32 : kAcc * BN;
+  static constexpr int kXRows = kSwap ? BN : kF8BM;  // activation rows of a tile
+  static constexpr int kWRows = kSwap ? kF8BM : BN;
+  static constexpr int kWBlocks = kWRows / 128 < 1 ? 1 : kWRows / 128;
+  static constexpr uint32_t kStageA = kF8BM * kF8BK;
+  static constexpr uint32_t kStageB = BN * kF8BK;
+  static constexpr uint32_t kStageBytes = kStageA + kStageB;
+  static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
+  static constexpr uint32_t kBarBytes = 256;
+  static constexpr uint32_t kBudget = 227u * 1024u - 1024u - kBarBytes - kScaleBytes;
+  static constexpr int kStages = kBudget / kStageBytes > 6 ? 6 : (int)(kBudget / kStageBytes);
+  static constexpr uint32_t kSmem = kStages * kStageBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
+  static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
+  static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory");
+  static_assert((2 * kStages + 2 * kAcc) * 8 + 4 <= (int)kBarBytes, "barrier block");
+};
+
+// Instruction descriptor of tcgen05.mma kind::f8f6f4: E4M3 A and B (format
+// 0), both K-major, FP32 accumulator (format 1), M x N tile.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// One K = 32 MMA from one elected lane of a converged warp.
+__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// 16 (8) FP32 columns of this warp's 32 tensor-memory lanes, not waited for.
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Wait for this thread's tensor-memory loads; the registers pass through so
+// that no use of them moves above the wait.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void named_bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// One finished output value (with the addend, if any).
+__device__ __forceinline__ void f8_store_one(const Fp8Args& a, int m, int n, float v) {
+  if (a.add) v += __bfloat162float(a.add[(int64_t)m * a.add_row + n]);
+  const int64_t o = (int64_t)m * a.out_row + n;
+  if (a.out_f32)
+    static_cast<float*>(a.out)[o] = v;
+  else
+    static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
+}
+
+// Eight consecutive columns of one output row.
+__device__ __forceinline__ void f8_store_8(const Fp8Args& a, int m, int n, const float* v) {
+  if (!a.vec || n + 8 > a.N) {
+    for (int i = 0; i < 8; ++i)
+      if (n + i < a.N) f8_store_one(a, m, n + i, v[i]);
+    return;
+  }
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = v[i];
+  if (a.add) {
+    const uint4 u = *reinterpret_cast<const uint4*>(a.add + (int64_t)m * a.add_row + n);
+    const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[2 * i] += __uint_as_float(p[i] << 16);
+      w[2 * i + 1] += __uint_as_float(p[i] & 0xffff0000u);
+    }
+  }
+  if (a.out_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)m * a.out_row + n);
+    o[0] = make_float4(w[0], w[1], w[2], w[3]);
+    o[1] = make_float4(w[4], w[5], w[6], w[7]);
+  } else {
+    uint32_t p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(w[2 * i], w[2 * i + 1]);
+      p[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)m * a.out_row + n) =
+        make_uint4(p[0], p[1], p[2], p[3]);
+  }
+}
+
+// Persistent tile loop: CTA b computes tiles b, b + gridDim.x, ... of the
+// m_tiles x n_tiles grid (token tiles fastest).  map_a: the 128-row
+// operand's bytes, box 128 rows x 128 B; map_b: the other operand's, box BN
+// rows x 128 B; both SWIZZLE_128B, zero-filled past their rows and past K.
+template <int BN, bool kSwap>
+__device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
+                                                    const Fp8Args& a) {
+  using Cfg = F8Cfg<BN, kSwap>;
+  constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  float* xsc = reinterpret_cast<float*>(smem + S * Cfg::kStageBytes);       // [2][kF8Chunk][kXRows]
+  float* wsc = xsc + 2 * kF8Chunk * Cfg::kXRows;                            // [2][kF8Chunk][kWBlocks]
+  uint64_t* full = reinterpret_cast<uint64_t*>(wsc + 2 * kF8Chunk * Cfg::kWBlocks);
+  uint64_t* empty = full + S;
+  uint64_t* done = empty + S;     // [NA]
+  uint64_t* accfree = done + NA;  // [NA]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfree + NA);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m_tiles = (a.M + Cfg::kXRows - 1) / Cfg::kXRows;
+  const int n_tiles = (a.N + Cfg::kWRows - 1) / Cfg::kWRows;
+  const int tiles = m_tiles * n_tiles;
+  const int nk = (a.K + kF8BK - 1) / kF8BK;
+  uint32_t* err = a.err;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < NA; ++b) {
+      mbar_init(&done[b], 1);
+      mbar_init(&accfree[b], Cfg::kScaleWarps);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(map_a);
+    tma_prefetch_desc(map_b);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, Cfg::kTmemCols);
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+        const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
+        for (int s = 0; s < nk; ++s, ++g) {
+          const int slot = g % S, round = g / S;
+          if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1, err, 1u)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + slot * Cfg::kStageBytes;
+          mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
+          tma_load_2d(st, map_a, s * kF8BK, kSwap ? w0 : x0, &full[slot]);
+          tma_load_2d(st + Cfg::kStageA, map_b, s * kF8BK, kSwap ? x0 : w0, &full[slot]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
+    int g = 0;
+    bool ok = true;
+    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      for (int s = 0; s < nk; ++s, ++g) {
+        const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
+        bool w = use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u);
+        w = w && mbar_wait(&full[slot], round & 1, err, 2u);
+        if (!__all_sync(0xffffffffu, w)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t acc = tmem + (uint32_t)(ab * BN);
+        const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
+        const uint64_t db = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes + Cfg::kStageA), 16, 1024, kLayoutSW128);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
+          mma_f8_warp(acc, da + 2 * k, db + 2 * k, idesc, k > 0);
+        mma_commit_warp(&empty[slot]);
+        mma_commit_warp(&done[ab]);
+      }
+    }
+  } else {
+    const int t = threadIdx.x - 64;
+    const int half = (warp - 2) / 4;
+    const int row = (warp & 3) * 32 + lane;  // row of the 128-row operand (tensor-memory lane)
+    const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * Cfg::kCols);
+    // Copy the scales of K blocks [c0, c0 + kF8Chunk) of tile idx.
+    auto load_chunk = [&](int idx, int c0, int buf) {
+      const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
+      const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
+      float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
+      for (int i = t; i < n * Cfg::kXRows; i += 32 * Cfg::kScaleWarps) {
+        const int m = x0 + i % Cfg::kXRows;  // rows past M read the last row's scale; their sums are not stored
+        cp_async_4(xd + i, a.xs + (int64_t)(m < a.M ? m : a.M - 1) * a.xs_row + (int64_t)(c0 + i / Cfg::kXRows) * a.xs_blk);
+      }
+      float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
+      const int last = (a.N - 1) / 128;
+      if (t < n * Cfg::kWBlocks) {
+        const int b = wb + t % Cfg::kWBlocks;
+        cp_async_4(wd + t, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + c0 + t / Cfg::kWBlocks);
+      }
+    };
+    int g = 0, gc = 0;
+    bool ok = true;
+    if ((int)blockIdx.x < tiles) load_chunk(blockIdx.x, 0, 0);
+    for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x) {
+      const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
+      float2 acc[Cfg::kCols / 2];
+#pragma unroll
+      for (int i = 0; i < Cfg::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
+        // this chunk's scales have arrived, and every warp is past the chunk
+        // before it, so the other buffer is free for the next chunk
+        cp_async_wait_all();
+        named_bar_sync(1, 32 * Cfg::kScaleWarps);
+        const int buf = gc & 1;
+        if (c0 + kF8Chunk < nk)
+          load_chunk(idx, c0 + kF8Chunk, buf ^ 1);
+        else if (idx + (int)gridDim.x < tiles)
+          load_chunk(idx + gridDim.x, 0, buf ^ 1);
+        const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
+        const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
+        const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
+        for (int kk = 0; kk < n; ++kk, ++g) {
+          const int ab = g % NA, use = g / NA;
+          // a wait that gave up is recorded; its warp goes on, so that the
+          // scale warps' barriers stay whole, and waits no more
+          if (ok && !__all_sync(0xffffffffu, mbar_wait(&done[ab], use & 1, err, 4u))) ok = false;
+          if (!ok) continue;
+          tc_fence_after();
+          const uint32_t src = tm + (uint32_t)(ab * BN);
+          const float ws = wd[kk * Cfg::kWBlocks + (kSwap ? 0 : half * Cfg::kCols / 128)];
+          const float rs = kSwap ? 0.f : xd[kk * Cfg::kXRows + row] * ws;
+          uint32_t r[2][16];
+          tmem_ld16_async(src, r[0]);
+#pragma unroll
+          for (int j = 0; j < Cfg::kCols / 16; ++j) {
+            tmem_wait_ld16(r[j & 1]);
+            if (j + 1 < Cfg::kCols / 16) tmem_ld16_async(src + 16 * (j + 1), r[(j + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 v = make_float2(__uint_as_float(r[j & 1][2 * i]), __uint_as_float(r[j & 1][2 * i + 1]));
+              float2 s = make_float2(rs, rs);
+              if (kSwap) {
+                s = *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + 16 * j + 2 * i);
+                s.x *= ws;
+                s.y *= ws;
+              }
+              acc[8 * j + i] = ffma2(v, s, acc[8 * j + i]);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&accfree[ab]);
+        }
+      }
+      if (!ok) continue;
+      if (kSwap) {  // lanes along n: 32 consecutive columns of one token per store
+        const int nn = w0 + row;
+#pragma unroll
+        for (int i = 0; i < Cfg::kCols / 2; ++i) {
+          const int m = x0 + half * Cfg::kCols + 2 * i;
+          if (nn < a.N && m < a.M) f8_store_one(a, m, nn, acc[i].x);
+          if (nn < a.N && m + 1 < a.M) f8_store_one(a, m + 1, nn, acc[i].y);
+        }
+      } else if (x0 + row < a.M) {
+#pragma unroll
+        for (int i = 0; i < Cfg::kCols / 8; ++i) {
+          const int nn = w0 + half * Cfg::kCols + 8 * i;
+          const float v[8] = {acc[4 * i].x,     acc[4 * i].y,     acc[4 * i + 1].x, acc[4 * i + 1].y,
+                              acc[4 * i + 2].x, acc[4 * i + 2].y, acc[4 * i + 3].x, acc[4 * i + 3].y};
+          if (nn < a.N) f8_store_8(a, x0 + row, nn, v);
+        }
+      }
+    }
+    cp_async_wait_all();
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, Cfg::kTmemCols);
+}
+
+}  // namespace moe_fp4

@@ -22,6 +22,7 @@
 #include "gemm_fp4.cuh"
 #include "gemm_fp4_swap.cuh"
 #include "gemm_mxf8.cuh"
+#include "host.cuh"
 
 namespace moe_fp4 {
 
@@ -127,6 +128,17 @@ static CUresult make_typed_map(CUtensorMap* m, CUtensorMapDataType dtype, const 
     if (n_used < 64) ++n_used;
   }
   return r;
+}
+
+CUresult encode_u8_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t stride,
+                          uint32_t box_rows) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t d[2] = {inner, rows}, strides[1] = {stride};
+  const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), d, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // 2-D tensor map over a row-major byte matrix [rows][inner_bytes], box of

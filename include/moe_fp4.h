@@ -579,6 +579,142 @@ MOE_FP4_API int moe_fp4_debug_quant_rows(const float *in, int rows, int K, uint8
 MOE_FP4_API int moe_fp4_debug_quant_mxfp8_rows(const float *in, int rows, int K, uint8_t *q, uint8_t *s,
                                                void *stream);
 
+/*
+ * ---- The operators around the layer ------------------------------------
+ *
+ * What stands between a model's residual stream and the layer when it is
+ * served: the norms before and after a block, the router's choice of
+ * experts, and the products of the always-on (shared) expert, whose weights
+ * such checkpoints keep in E4M3 with an FP32 scale per 128 x 128 block.  The
+ * pages have no counterpart of these entry points; they are additions of
+ * this library.  Row strides are in elements of their array, columns are
+ * contiguous, pointers are device pointers, and M = 0 is a no-op.  They need
+ * no workspace unless stated, never allocate, and may be captured in CUDA
+ * graphs.
+ */
+
+/*
+ * FP8 activations: per row and block of 128 columns b = k / 128
+ *     s[m][b] = max_{k in b} |v[m][k]| / 448   (1 where that is zero)
+ *     q[m][k] = e4m3_rn(v[m][k] / s[m][b])
+ * each step an IEEE FP32 operation.  v is x (act == NULL: x [M][K] bf16), or
+ * the gated activation of x = [gate | up] [M][2K] bf16 (act: the kinds of
+ * moe_fp4_activation but MOE_FP4_ACT_RELU2), computed in FP32 and not rounded
+ * before it is quantised.  s[m][b] is written at m * s_row + b *
+ * s_block (the products read s_row = 1 fastest).  A block with a NaN gives
+ * NaN at that element; one with an infinity gives NaN there and zeros (whose
+ * scale is infinite) elsewhere, so that products of the row are NaN.
+ * K % 16 == 0, x and q 16-byte aligned, x_row % 8 == 0, q_row % 16 == 0
+ * (MOE_FP4_EINVAL for misaligned arrays, MOE_FP4_EUNSUPPORTED for K).
+ */
+MOE_FP4_API int moe_fp4_fp8_quantize(const void *x_bf16, int64_t x_row, const moe_fp4_activation *act, void *q,
+                                     int64_t q_row, float *s, int64_t s_row, int64_t s_block, int M, int K,
+                                     void *stream);
+
+/*
+ * The FP8 product
+ *     out[m][n] = sum_b x_s[m][b] w_s[n / 128][b] sum_{k in b} x_q[m][k] w[n][k]  (+ add[m][n])
+ * with x_q [M][K] and w [N][K] E4M3, x_s[m][b] at m * xs_row + b * xs_block,
+ * w_s [ceil(N/128)][ceil(K/128)] with row stride ws_row, add bf16 [M][N] or
+ * NULL, out bf16 (out_f32 = 0) or f32 [M][N]: the sums are FP32 and rounded
+ * once, after add.  Products of a block are summed on the tensor cores, the
+ * scaled blocks in FP32 registers, both in a fixed order: results are
+ * bitwise deterministic for given sizes and device.  out may be add itself;
+ * it must not overlap the other inputs.
+ * K % 16 == 0 (MOE_FP4_EUNSUPPORTED), x_q and w 16-byte aligned with row
+ * strides that are multiples of 16 (MOE_FP4_EINVAL); any M and N, last
+ * blocks of K and N may be short.
+ */
+MOE_FP4_API int moe_fp4_fp8_matmul(const void *x_q, int64_t x_row, const float *x_s, int64_t xs_row,
+                                   int64_t xs_block, const void *w, int64_t w_row, const float *w_s, int64_t ws_row,
+                                   const void *add_bf16, int64_t add_row, void *out, int64_t out_row, int out_f32,
+                                   int M, int N, int K, void *stream);
+
+/*
+ * moe_fp4_fp8_quantize (act == NULL) and moe_fp4_fp8_matmul in one call: out
+ * = x W^T with x [M][K] bf16, on a caller-owned workspace of
+ * moe_fp4_fp8_linear_workspace_bytes(M, K) bytes (256-byte aligned, needs no
+ * initialisation; MOE_FP4_EWORKSPACE if missing or too small).  The size is
+ * 0 for invalid arguments.
+ */
+MOE_FP4_API size_t moe_fp4_fp8_linear_workspace_bytes(int M_max, int K);
+MOE_FP4_API int moe_fp4_fp8_linear(const void *x_bf16, int64_t x_row, const void *w, int64_t w_row, const float *w_s,
+                                   int64_t ws_row, const void *add_bf16, int64_t add_row, void *out, int64_t out_row,
+                                   int out_f32, int M, int N, int K, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/*
+ * Status word of the FP8 products' bounded waits on the current device (as
+ * moe_fp4_workspace_status: 0, or sticky bits of waits that gave up, after
+ * which the outputs since the last clear are not valid).  Synchronises
+ * `stream`.
+ */
+MOE_FP4_API int moe_fp4_fp8_status(uint32_t *flags, int clear, void *stream);
+
+/*
+ * The norms before and after a block, its gate and its residual scale:
+ *     z  = b * rsqrt(mean(b^2) + eps) * (offset + w_post)   (w_post NULL: z = b)
+ *     r' = r + scale * gate * z                             (b NULL: r' = r)
+ *     n  = r' * rsqrt(mean(r'^2) + eps) * (offset + w_pre)  (w_pre NULL: no n, q, s)
+ * with r' written to residual_out (residual's type; NULL: not written; may
+ * be residual itself), n to normed (bf16, may be NULL) and, with q, the FP8
+ * form of n's bf16 values as moe_fp4_fp8_quantize gives it.  Arithmetic is
+ * FP32; n follows the FP32 r', before its rounding to residual_out.
+ *   residual  [M][H] bf16, or f32 (residual_f32)
+ *   block_out [M][H] bf16 or NULL
+ *   w_post, w_pre [H] bf16, or f32 (weights_f32); offset 1 for checkpoints
+ *             that store weights as differences from one, else 0
+ *   gate      bf16, or f32 (gate_f32), or NULL (1): gate[m * gate_row + h *
+ *             gate_col], gate_col 0 (a value per token) or 1; gate_row 0 for
+ *             a value per channel.  Read only with block_out.
+ * A row whose values are all zero gives n = 0 for eps > 0.  eps >= 0 and
+ * finite, scale and offset finite (MOE_FP4_EINVAL).  1 <= H <= 32768
+ * (MOE_FP4_EUNSUPPORTED).  Arrays need their element's alignment only; with
+ * q, H % 16 == 0 (MOE_FP4_EUNSUPPORTED) and every row of every array 16-byte
+ * aligned (MOE_FP4_EINVAL).
+ */
+typedef struct moe_fp4_block_norm_args {
+  const void *residual;
+  int64_t residual_row;
+  const void *block_out;
+  int64_t block_row;
+  const void *w_post, *w_pre;
+  const void *gate;
+  int64_t gate_row, gate_col;
+  void *residual_out;
+  int64_t residual_out_row;
+  void *normed;
+  int64_t normed_row;
+  void *q;
+  int64_t q_row;
+  float *s;
+  int64_t s_row, s_block;
+  float scale, eps, offset;
+  int residual_f32, weights_f32, gate_f32;
+  int M, H;
+} moe_fp4_block_norm_args;
+MOE_FP4_API int moe_fp4_block_norm(const moe_fp4_block_norm_args *args, void *stream);
+
+/*
+ * The router's choice: per token the top_k experts of logits [M][E] (bf16,
+ * or f32 with logits_f32) and their weights, as the layer takes them
+ * (topk_ids int32 and topk_weights f32, both [M][top_k], dense).
+ *   MOE_FP4_SCORE_SOFTMAX  by logit; weight softmax(logits)[e]
+ *   MOE_FP4_SCORE_SIGMOID  by sigmoid(logit) + bias[e] (bias f32 [E] or
+ *                          NULL); weight sigmoid(logit), without the bias
+ * divided by the sum of the row's chosen weights if renormalize, times scale.
+ * Order: descending, equal scores by ascending index.  Experts with a logit
+ * of -inf or NaN (or a NaN score) are never chosen; where a row has fewer
+ * than top_k others, its last ids are -1 with weight 0, which the layer takes
+ * as no expert.  1 <= top_k <= 16, top_k <= E <= 65536
+ * (MOE_FP4_EUNSUPPORTED); bias with the softmax score is MOE_FP4_EINVAL.
+ */
+#define MOE_FP4_SCORE_SOFTMAX 0
+#define MOE_FP4_SCORE_SIGMOID 1
+MOE_FP4_API int moe_fp4_route_topk(const void *logits, int64_t logits_row, int logits_f32, const float *bias,
+                                   int score, int renormalize, float scale, int32_t *topk_ids, float *topk_weights,
+                                   int M, int E, int top_k, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

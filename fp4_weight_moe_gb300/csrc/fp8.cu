@@ -110,23 +110,62 @@ __global__ void __launch_bounds__(F8Cfg<BN, kSwap>::kThreads, 1)
   gemm_fp8_persistent<BN, kSwap>(&map_a, &map_b, a);
 }
 
+template <int BN, bool kTwo>
+__global__ void __launch_bounds__(F8Cfg<BN, true, kTwo>::kThreads, kTwo ? 2 : 1)
+    fp8_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Fp8Args a,
+                     int split) {
+  a.err = &g_fp8_status;
+  gemm_fp8_persistent<BN, true, kTwo, true>(&map_a, &map_b, a, split);
+}
+
+struct Operands {
+  const void *x, *w;
+  int64_t x_row, w_row;
+};
+
+static cudaError_t encode(CUtensorMap* mx, CUtensorMap* mw, const Operands& o, const Fp8Args& a, int x_rows,
+                          int w_rows) {
+  CUresult r = encode_u8_map_2d(mx, o.x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)o.x_row, (uint32_t)x_rows);
+  if (r == CUDA_SUCCESS)
+    r = encode_u8_map_2d(mw, o.w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)o.w_row, (uint32_t)w_rows);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int BN, bool kSwap>
-static cudaError_t launch_gemm(const void* x, int64_t x_row, const void* w, int64_t w_row, const Fp8Args& a, int sms,
-                               cudaStream_t st) {
+static cudaError_t launch_gemm(const Operands& o, const Fp8Args& a, int sms, cudaStream_t st) {
   using Cfg = F8Cfg<BN, kSwap>;
   CUtensorMap mx, mw;
-  CUresult r = encode_u8_map_2d(&mx, x, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)x_row, Cfg::kXRows);
-  if (r == CUDA_SUCCESS)
-    r = encode_u8_map_2d(&mw, w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)w_row, Cfg::kWRows);
-  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  cudaError_t e = encode(&mx, &mw, o, a, Cfg::kXRows, Cfg::kWRows);
   static bool seen[64];
-  cudaError_t e = allow_smem(fp8_gemm_kernel<BN, kSwap>, Cfg::kSmem, seen);
+  if (e == cudaSuccess) e = allow_smem(fp8_gemm_kernel<BN, kSwap>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
   const int64_t tiles =
       (int64_t)((a.M + Cfg::kXRows - 1) / Cfg::kXRows) * ((a.N + Cfg::kWRows - 1) / Cfg::kWRows);
   const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
   fp8_gemm_kernel<BN, kSwap><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(kSwap ? mw : mx, kSwap ? mx : mw, a);
   return cudaGetLastError();
+}
+
+template <int BN, bool kTwo>
+static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, int split, cudaStream_t st) {
+  using Cfg = F8Cfg<BN, true, kTwo>;
+  CUtensorMap mx, mw;
+  cudaError_t e = encode(&mx, &mw, o, a, Cfg::kXRows, Cfg::kWRows);
+  static bool seen[64];
+  if (e == cudaSuccess) e = allow_smem(fp8_split_kernel<BN, kTwo>, Cfg::kSmem, seen);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(tiles * split));
+  c.blockDim = dim3(Cfg::kThreads);
+  c.dynamicSmemBytes = Cfg::kSmem;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, fp8_split_kernel<BN, kTwo>, mw, mx, a, split);
 }
 
 cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
@@ -152,7 +191,26 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   a.K = K;
   a.vec = ((uintptr_t)out & 15u) == 0 && (out_row * (out_f32 ? 4 : 2)) % 16 == 0 &&
           (!add || (((uintptr_t)add & 15u) == 0 && add_row % 8 == 0));
-  return launch_gemm<128, false>(x, x_row, w, w_row, a, sms, st);
+  const Operands o = {x, w, x_row, w_row};
+  // Few tiles: the weights' 128 rows on the MMA's row side, the tokens (16,
+  // 32, 64 or 128 of them) on its column side, and K split over a cluster
+  // until the CTAs fill the GPU (two per SM where a tile is small), with at
+  // least two K blocks each.
+  const int nk = (K + 127) / 128;
+  const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);
+  const int slots = bn == 128 ? sms : 2 * sms;
+  if (tiles <= slots / 2) {
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
+    switch (bn) {
+      case 16: return launch_split<16, true>(o, a, (int)tiles, split, st);
+      case 32: return launch_split<32, true>(o, a, (int)tiles, split, st);
+      case 64: return launch_split<64, true>(o, a, (int)tiles, split, st);
+      default: return launch_split<128, false>(o, a, (int)tiles, split, st);
+    }
+  }
+  return launch_gemm<128, false>(o, a, sms, st);
 }
 
 }  // namespace moe_fp4

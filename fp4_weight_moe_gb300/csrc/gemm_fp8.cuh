@@ -47,7 +47,8 @@ struct Fp8Args {
   uint32_t* err;
 };
 
-template <int BN, bool kSwap>
+// kTwo: shared memory and tensor memory for two CTAs per SM.
+template <int BN, bool kSwap, bool kTwo = false>
 struct F8Cfg {
   static constexpr int kHalves = BN >= 64 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
@@ -63,11 +64,13 @@ struct F8Cfg {
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
   static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
   static constexpr uint32_t kBarBytes = 256;
-  static constexpr uint32_t kBudget = 227u * 1024u - 1024u - kBarBytes - kScaleBytes;
+  static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes;
   static constexpr int kStages = kBudget / kStageBytes > 6 ? 6 : (int)(kBudget / kStageBytes);
   static constexpr uint32_t kSmem = kStages * kStageBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
-  static_assert(kStages >= 3 && kSmem <= 227 * 1024, "shared memory");
+  static_assert(kStages >= 3 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
+  static_assert(!kTwo || kTmemCols <= 256, "tensor memory of two CTAs");
+  static_assert(!kSwap || BN * 512u <= kStages * kStageBytes, "a tile's partial sums fit the ring");
   static_assert((2 * kStages + 2 * kAcc) * 8 + 4 <= (int)kBarBytes, "barrier block");
 };
 
@@ -158,14 +161,61 @@ __device__ __forceinline__ void f8_store_8(const Fp8Args& a, int m, int n, const
   }
 }
 
+// Four consecutive columns of one output row.
+__device__ __forceinline__ void f8_store_4(const Fp8Args& a, int m, int n, float4 v) {
+  if (!a.vec || n + 4 > a.N) {
+    const float w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) f8_store_one(a, m, n + i, w[i]);
+    return;
+  }
+  if (a.add) {
+    const uint2 u = *reinterpret_cast<const uint2*>(a.add + (int64_t)m * a.add_row + n);
+    v.x += __uint_as_float(u.x << 16);
+    v.y += __uint_as_float(u.x & 0xffff0000u);
+    v.z += __uint_as_float(u.y << 16);
+    v.w += __uint_as_float(u.y & 0xffff0000u);
+  }
+  if (a.out_f32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + (int64_t)m * a.out_row + n) = v;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)m * a.out_row + n) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Four floats at `saddr` (a shared-memory address of this CTA) in CTA `rank`
+// of the cluster.
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .u32 ra;\n\tmapa.shared::cluster.u32 ra, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [ra];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(saddr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // Persistent tile loop: CTA b computes tiles b, b + gridDim.x, ... of the
 // m_tiles x n_tiles grid (token tiles fastest).  map_a: the 128-row
 // operand's bytes, box 128 rows x 128 B; map_b: the other operand's, box BN
 // rows x 128 B; both SWIZZLE_128B, zero-filled past their rows and past K.
-template <int BN, bool kSwap>
+//
+// kSplit (kSwap only; a cluster of `split` CTAs per tile, one tile per
+// cluster): the CTAs of a cluster take consecutive ranges of the K blocks,
+// leave their partial tiles in their shared memory, and each sums the
+// cluster's partials, in rank order, for its share of the tile's tokens and
+// stores them.
+template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false>
 __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
-                                                    const Fp8Args& a) {
-  using Cfg = F8Cfg<BN, kSwap>;
+                                                    const Fp8Args& a, int split = 1) {
+  static_assert(!kSplit || kSwap, "the K split is for few tokens");
+  using Cfg = F8Cfg<BN, kSwap, kTwo>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -181,7 +231,13 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   const int m_tiles = (a.M + Cfg::kXRows - 1) / Cfg::kXRows;
   const int n_tiles = (a.N + Cfg::kWRows - 1) / Cfg::kWRows;
   const int tiles = m_tiles * n_tiles;
-  const int nk = (a.K + kF8BK - 1) / kF8BK;
+  const int nk_all = (a.K + kF8BK - 1) / kF8BK;
+  // this CTA's K blocks and its first tile
+  const int rank = kSplit ? (int)(blockIdx.x % split) : 0;
+  const int kb0 = kSplit ? (int)((int64_t)nk_all * rank / split) : 0;
+  const int nk = (kSplit ? (int)((int64_t)nk_all * (rank + 1) / split) : nk_all) - kb0;
+  const int first = kSplit ? (int)(blockIdx.x / split) : (int)blockIdx.x;
+  const int step = kSplit ? tiles : (int)gridDim.x;
   uint32_t* err = a.err;
 
   if (threadIdx.x == 0) {
@@ -208,7 +264,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     if (lane == 0) {
       int g = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+      for (int idx = first; ok && idx < tiles; idx += step) {
         const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
         for (int s = 0; s < nk; ++s, ++g) {
           const int slot = g % S, round = g / S;
@@ -218,8 +274,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           }
           uint8_t* st = smem + slot * Cfg::kStageBytes;
           mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
-          tma_load_2d(st, map_a, s * kF8BK, kSwap ? w0 : x0, &full[slot]);
-          tma_load_2d(st + Cfg::kStageA, map_b, s * kF8BK, kSwap ? x0 : w0, &full[slot]);
+          tma_load_2d(st, map_a, (kb0 + s) * kF8BK, kSwap ? w0 : x0, &full[slot]);
+          tma_load_2d(st + Cfg::kStageA, map_b, (kb0 + s) * kF8BK, kSwap ? x0 : w0, &full[slot]);
         }
       }
     }
@@ -227,7 +283,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
     int g = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; ok && idx < tiles; idx += gridDim.x) {
+    for (int idx = first; ok && idx < tiles; idx += step) {
       for (int s = 0; s < nk; ++s, ++g) {
         const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
         bool w = use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u);
@@ -252,26 +308,26 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     const int half = (warp - 2) / 4;
     const int row = (warp & 3) * 32 + lane;  // row of the 128-row operand (tensor-memory lane)
     const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * Cfg::kCols);
-    // Copy the scales of K blocks [c0, c0 + kF8Chunk) of tile idx.
+    // Copy the scales of this CTA's K blocks [c0, c0 + kF8Chunk) of tile idx.
     auto load_chunk = [&](int idx, int c0, int buf) {
       const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
       const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
       float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
       for (int i = t; i < n * Cfg::kXRows; i += 32 * Cfg::kScaleWarps) {
         const int m = x0 + i % Cfg::kXRows;  // rows past M read the last row's scale; their sums are not stored
-        cp_async_4(xd + i, a.xs + (int64_t)(m < a.M ? m : a.M - 1) * a.xs_row + (int64_t)(c0 + i / Cfg::kXRows) * a.xs_blk);
+        cp_async_4(xd + i, a.xs + (int64_t)(m < a.M ? m : a.M - 1) * a.xs_row + (int64_t)(kb0 + c0 + i / Cfg::kXRows) * a.xs_blk);
       }
       float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
       const int last = (a.N - 1) / 128;
       if (t < n * Cfg::kWBlocks) {
         const int b = wb + t % Cfg::kWBlocks;
-        cp_async_4(wd + t, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + c0 + t / Cfg::kWBlocks);
+        cp_async_4(wd + t, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + kb0 + c0 + t / Cfg::kWBlocks);
       }
     };
     int g = 0, gc = 0;
     bool ok = true;
-    if ((int)blockIdx.x < tiles) load_chunk(blockIdx.x, 0, 0);
-    for (int idx = blockIdx.x; idx < tiles; idx += gridDim.x) {
+    if (first < tiles) load_chunk(first, 0, 0);
+    for (int idx = first; idx < tiles; idx += step) {
       const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
       float2 acc[Cfg::kCols / 2];
 #pragma unroll
@@ -284,8 +340,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         const int buf = gc & 1;
         if (c0 + kF8Chunk < nk)
           load_chunk(idx, c0 + kF8Chunk, buf ^ 1);
-        else if (idx + (int)gridDim.x < tiles)
-          load_chunk(idx + gridDim.x, 0, buf ^ 1);
+        else if (idx + step < tiles)
+          load_chunk(idx + step, 0, buf ^ 1);
         const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
         const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
         const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
@@ -322,6 +378,17 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           if (lane == 0) mbar_arrive(&accfree[ab]);
         }
       }
+      if (kSplit) {
+        // the ring is idle: every load was multiplied, every MMA is done
+        float* part = reinterpret_cast<float*>(smem);  // [BN][128]
+#pragma unroll
+        for (int i = 0; i < Cfg::kCols / 2; ++i) {
+          const int c = half * Cfg::kCols + 2 * i;
+          part[c * 128 + row] = acc[i].x;
+          part[(c + 1) * 128 + row] = acc[i].y;
+        }
+        continue;
+      }
       if (!ok) continue;
       if (kSwap) {  // lanes along n: 32 consecutive columns of one token per store
         const int nn = w0 + row;
@@ -342,6 +409,28 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       }
     }
     cp_async_wait_all();
+  }
+  if (kSplit) {
+    __syncwarp();
+    cluster_sync();
+    const int x0 = (first % m_tiles) * Cfg::kXRows, w0 = (first / m_tiles) * Cfg::kWRows;
+    const int used = a.M - x0 < BN ? a.M - x0 : BN;  // tokens of this tile
+    const int c0 = used * rank / split, c1 = used * (rank + 1) / split;
+    for (int e = threadIdx.x; e < (c1 - c0) * 32; e += Cfg::kThreads) {
+      const int c = c0 + e / 32, r = e % 32 * 4;
+      const uint32_t at = smem_u32(smem) + (uint32_t)(c * 128 + r) * 4;
+      float4 v = ld_cluster_f4(at, 0);
+      for (int p = 1; p < split; ++p) {
+        const float4 u = ld_cluster_f4(at, (uint32_t)p);
+        v.x += u.x;
+        v.y += u.y;
+        v.z += u.z;
+        v.w += u.w;
+      }
+      if (w0 + r < a.N) f8_store_4(a, x0 + c, w0 + r, v);
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its partials
   }
   tc_fence_before();
   __syncwarp();

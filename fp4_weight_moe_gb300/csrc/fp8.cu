@@ -110,12 +110,12 @@ __global__ void __launch_bounds__(F8Cfg<BN, kSwap>::kThreads, 1)
   gemm_fp8_persistent<BN, kSwap>(&map_a, &map_b, a);
 }
 
-template <int BN, bool kTwo>
-__global__ void __launch_bounds__(F8Cfg<BN, true, kTwo>::kThreads, kTwo ? 2 : 1)
+template <int BN, bool kSwap, bool kTwo>
+__global__ void __launch_bounds__(F8Cfg<BN, kSwap, kTwo>::kThreads, kTwo ? 2 : 1)
     fp8_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Fp8Args a,
                      int split) {
   a.err = &g_fp8_status;
-  gemm_fp8_persistent<BN, true, kTwo, true>(&map_a, &map_b, a, split);
+  gemm_fp8_persistent<BN, kSwap, kTwo, true>(&map_a, &map_b, a, split);
 }
 
 struct Operands {
@@ -146,13 +146,13 @@ static cudaError_t launch_gemm(const Operands& o, const Fp8Args& a, int sms, cud
   return cudaGetLastError();
 }
 
-template <int BN, bool kTwo>
+template <int BN, bool kSwap, bool kTwo>
 static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, int split, cudaStream_t st) {
-  using Cfg = F8Cfg<BN, true, kTwo>;
+  using Cfg = F8Cfg<BN, kSwap, kTwo>;
   CUtensorMap mx, mw;
   cudaError_t e = encode(&mx, &mw, o, a, Cfg::kXRows, Cfg::kWRows);
   static bool seen[64];
-  if (e == cudaSuccess) e = allow_smem(fp8_split_kernel<BN, kTwo>, Cfg::kSmem, seen);
+  if (e == cudaSuccess) e = allow_smem(fp8_split_kernel<BN, kSwap, kTwo>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -165,7 +165,7 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
   c.stream = st;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, fp8_split_kernel<BN, kTwo>, mw, mx, a, split);
+  return cudaLaunchKernelEx(&c, fp8_split_kernel<BN, kSwap, kTwo>, kSwap ? mw : mx, kSwap ? mx : mw, a, split);
 }
 
 cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
@@ -192,10 +192,15 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   a.vec = ((uintptr_t)out & 15u) == 0 && (out_row * (out_f32 ? 4 : 2)) % 16 == 0 &&
           (!add || (((uintptr_t)add & 15u) == 0 && add_row % 8 == 0));
   const Operands o = {x, w, x_row, w_row};
-  // Few tiles: the weights' 128 rows on the MMA's row side, the tokens (16,
-  // 32, 64 or 128 of them) on its column side, and K split over a cluster
-  // until the CTAs fill the GPU (two per SM where a tile is small), with at
-  // least two K blocks each.
+  // Few tiles: K is split over a cluster until the CTAs fill the GPU, with at
+  // least two K blocks each.  Up to 64 tokens the weights' 128 rows lie on
+  // the MMA's row side and the tokens (16, 32 or 64) on its column side, two
+  // CTAs per SM; past that the tokens take the row side, where a scale
+  // thread's activation scale is one value instead of one per column.
+  // Measured (us, K x N): M=128 7168 x 4096, tokens on columns 14.5 / on rows
+  // 11.9; 2048 x 7168 11.2 / 9.6; M=64, tokens on rows 22.6 against 13.0 and
+  // 13.0 against 9.7; M=1 7168 x 4096 split 1 / 2 / 4 / 8: 22.3 / 12.4 / 8.1
+  // / 7.8; M=256 4096 x 4096 split 1 / 2 / 4: 18.4 / 12.8 / 18.5 (two waves).
   const int nk = (K + 127) / 128;
   const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);
@@ -204,12 +209,20 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
     int split = 1;
     while (split < 8 && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
     switch (bn) {
-      case 16: return launch_split<16, true>(o, a, (int)tiles, split, st);
-      case 32: return launch_split<32, true>(o, a, (int)tiles, split, st);
-      case 64: return launch_split<64, true>(o, a, (int)tiles, split, st);
-      default: return launch_split<128, false>(o, a, (int)tiles, split, st);
+      case 16: return launch_split<16, true, true>(o, a, (int)tiles, split, st);
+      case 32: return launch_split<32, true, true>(o, a, (int)tiles, split, st);
+      case 64: return launch_split<64, true, true>(o, a, (int)tiles, split, st);
+      default: return launch_split<128, false, false>(o, a, (int)tiles, split, st);
     }
   }
+  // Many tiles: 128 x 256 keeps the tensor cores busier, 128 x 128 leaves
+  // less of the last wave idle; a wave of the former takes about 1.25 times
+  // as long (M=512 4096 x 4096: 20.6 against 16.8 us, one wave each; M=768
+  // 20.8 against 30.6, one and two).
+  const int64_t t256 = (int64_t)((M + 127) / 128) * ((N + 255) / 256);
+  const int64_t t128 = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t w256 = (t256 + sms - 1) / sms, w128 = (t128 + sms - 1) / sms;
+  if (5 * w256 <= 4 * w128) return launch_gemm<256, false>(o, a, sms, st);
   return launch_gemm<128, false>(o, a, sms, st);
 }
 

@@ -7,7 +7,7 @@
 // two per 32 K), so every K block gets an accumulator of its own, which the
 // scale warps read, scale and add up while the next block multiplies.
 //
-// A CTA computes 128 x BN tiles in turn with 2 + 4 * kHalves warps:
+// A CTA computes 128 x BN tiles in turn with kFirst + 4 * kHalves warps:
 //   warp 0 lane 0  TMA producer: per K block the 128-row box (128 x 128 B)
 //                  and the BN-row box, SWIZZLE_128B, into a ring;
 //   warp 1         allocates tensor memory and, converged, issues the four
@@ -52,8 +52,14 @@ template <int BN, bool kSwap, bool kTwo = false>
 struct F8Cfg {
   static constexpr int kHalves = BN >= 64 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
+  static constexpr int kLd = kCols / 2 < 32 ? kCols / 2 : 32;  // ... per tensor-memory load (an even count of them)
   static constexpr int kScaleWarps = 4 * kHalves;
-  static constexpr int kThreads = 32 * (2 + kScaleWarps);
+  // 256 columns: 128 sums per scale thread and two loads in flight need more
+  // registers than an even split of the SM's gives ten warps, so the scale
+  // warps take them (setmaxnreg) from a warpgroup that holds warps 0 and 1
+  static constexpr bool kMoveRegs = BN >= 256;
+  static constexpr int kFirst = kMoveRegs ? 4 : 2;  // first scale warp
+  static constexpr int kThreads = 32 * (kFirst + kScaleWarps);
   static constexpr int kAcc = BN >= 256 ? 2 : 4;
   static constexpr uint32_t kTmemCols = kAcc * BN < 32 ? 32 : kAcc * BN;
   static constexpr int kXRows = kSwap ? BN : kF8BM;  // activation rows of a tile
@@ -70,7 +76,11 @@ struct F8Cfg {
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(kStages >= 3 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
   static_assert(!kTwo || kTmemCols <= 256, "tensor memory of two CTAs");
-  static_assert(!kSwap || BN * 512u <= kStages * kStageBytes, "a tile's partial sums fit the ring");
+  // a split tile's partial sums lie in the ring: [BN][128] tokens by columns
+  // (kSwap) or [128][BN + 4] (padded, so that lanes writing their own rows
+  // spread over the banks)
+  static constexpr uint32_t kPartRow = kSwap ? 128 : BN + 4;
+  static_assert(BN > 128 || (kSwap ? BN : 128) * kPartRow * 4u <= kStages * kStageBytes, "partial sums fit the ring");
   static_assert((2 * kStages + 2 * kAcc) * 8 + 4 <= (int)kBarBytes, "barrier block");
 };
 
@@ -90,22 +100,82 @@ __device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// 16 (8) FP32 columns of this warp's 32 tensor-memory lanes, not waited for.
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// kN FP32 columns of this warp's 32 tensor-memory lanes, not waited for, and
+// the wait for them: the registers pass through it so that no use of them
+// moves above it.
+template <int kN>
+struct TmemLd;
+template <>
+struct TmemLd<8> {
+  static __device__ __forceinline__ void start(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
+  }
+  static __device__ __forceinline__ void wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7])
+                 :
+                 : "memory");
+  }
+};
+template <>
+struct TmemLd<16> {
+  static __device__ __forceinline__ void start(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15])
+        : "r"(taddr));
+  }
+  static __device__ __forceinline__ void wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+  }
+};
+template <>
+struct TmemLd<32> {
+  static __device__ __forceinline__ void start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  }
+  static __device__ __forceinline__ void wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                   "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                   "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                   "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+  }
+};
+
+// Registers of the calling warpgroup's threads.
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// Wait for this thread's tensor-memory loads; the registers pass through so
-// that no use of them moves above the wait.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
@@ -206,7 +276,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
 // operand's bytes, box 128 rows x 128 B; map_b: the other operand's, box BN
 // rows x 128 B; both SWIZZLE_128B, zero-filled past their rows and past K.
 //
-// kSplit (kSwap only; a cluster of `split` CTAs per tile, one tile per
+// kSplit (a cluster of `split` CTAs per tile, one tile per
 // cluster): the CTAs of a cluster take consecutive ranges of the K blocks,
 // leave their partial tiles in their shared memory, and each sums the
 // cluster's partials, in rank order, for its share of the tile's tokens and
@@ -214,7 +284,6 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
 template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false>
 __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
                                                     const Fp8Args& a, int split = 1) {
-  static_assert(!kSplit || kSwap, "the K split is for few tokens");
   using Cfg = F8Cfg<BN, kSwap, kTwo>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
@@ -260,52 +329,57 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // (the registers move: 384 threads x 168 at launch = 128 x 40 + 256 x 232)
+  if (warp < Cfg::kFirst) {
+    if (Cfg::kMoveRegs) regs_dec<40>();
+    if (warp == 0) {
+      if (lane == 0) {
+        int g = 0;
+        bool ok = true;
+        for (int idx = first; ok && idx < tiles; idx += step) {
+          const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
+          for (int s = 0; s < nk; ++s, ++g) {
+            const int slot = g % S, round = g / S;
+            if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1, err, 1u)) {
+              ok = false;
+              break;
+            }
+            uint8_t* st = smem + slot * Cfg::kStageBytes;
+            mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
+            tma_load_2d(st, map_a, (kb0 + s) * kF8BK, kSwap ? w0 : x0, &full[slot]);
+            tma_load_2d(st + Cfg::kStageA, map_b, (kb0 + s) * kF8BK, kSwap ? x0 : w0, &full[slot]);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
       int g = 0;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
-        const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
         for (int s = 0; s < nk; ++s, ++g) {
-          const int slot = g % S, round = g / S;
-          if (round > 0 && !mbar_wait(&empty[slot], (round - 1) & 1, err, 1u)) {
+          const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
+          bool w = use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u);
+          w = w && mbar_wait(&full[slot], round & 1, err, 2u);
+          if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + slot * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
-          tma_load_2d(st, map_a, (kb0 + s) * kF8BK, kSwap ? w0 : x0, &full[slot]);
-          tma_load_2d(st + Cfg::kStageA, map_b, (kb0 + s) * kF8BK, kSwap ? x0 : w0, &full[slot]);
-        }
-      }
-    }
-  } else if (warp == 1) {
-    constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
-    int g = 0;
-    bool ok = true;
-    for (int idx = first; ok && idx < tiles; idx += step) {
-      for (int s = 0; s < nk; ++s, ++g) {
-        const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
-        bool w = use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u);
-        w = w && mbar_wait(&full[slot], round & 1, err, 2u);
-        if (!__all_sync(0xffffffffu, w)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t acc = tmem + (uint32_t)(ab * BN);
-        const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
-        const uint64_t db = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes + Cfg::kStageA), 16, 1024, kLayoutSW128);
+          tc_fence_after();
+          const uint32_t acc = tmem + (uint32_t)(ab * BN);
+          const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
+          const uint64_t db = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes + Cfg::kStageA), 16, 1024, kLayoutSW128);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
-          mma_f8_warp(acc, da + 2 * k, db + 2 * k, idesc, k > 0);
-        mma_commit_warp(&empty[slot]);
-        mma_commit_warp(&done[ab]);
+          for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
+            mma_f8_warp(acc, da + 2 * k, db + 2 * k, idesc, k > 0);
+          mma_commit_warp(&empty[slot]);
+          mma_commit_warp(&done[ab]);
+        }
       }
     }
   } else {
-    const int t = threadIdx.x - 64;
-    const int half = (warp - 2) / 4;
+    if (Cfg::kMoveRegs) regs_inc<232>();
+    const int t = threadIdx.x - 32 * Cfg::kFirst;
+    const int half = (warp - Cfg::kFirst) / 4;
     const int row = (warp & 3) * 32 + lane;  // row of the 128-row operand (tensor-memory lane)
     const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * Cfg::kCols);
     // Copy the scales of this CTA's K blocks [c0, c0 + kF8Chunk) of tile idx.
@@ -345,47 +419,67 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
         const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
         const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
-        for (int kk = 0; kk < n; ++kk, ++g) {
-          const int ab = g % NA, use = g / NA;
-          // a wait that gave up is recorded; its warp goes on, so that the
-          // scale warps' barriers stay whole, and waits no more
-          if (ok && !__all_sync(0xffffffffu, mbar_wait(&done[ab], use & 1, err, 4u))) ok = false;
-          if (!ok) continue;
+        // Wait for K block gg's accumulator and start its first load.  A wait
+        // that gave up is recorded; its warp goes on, so that the scale
+        // warps' barriers stay whole, and waits no more.
+        uint32_t r[2][Cfg::kLd];
+        auto begin = [&](int gg) {
+          const int ab = gg % NA;
+          if (ok && !__all_sync(0xffffffffu, mbar_wait(&done[ab], (gg / NA) & 1, err, 4u))) ok = false;
+          if (!ok) return;
           tc_fence_after();
+          TmemLd<Cfg::kLd>::start(tm + (uint32_t)(ab * BN), r[0]);
+        };
+        begin(g);
+        for (int kk = 0; kk < n; ++kk, ++g) {
+          if (!ok) continue;
+          const int ab = g % NA;
           const uint32_t src = tm + (uint32_t)(ab * BN);
           const float ws = wd[kk * Cfg::kWBlocks + (kSwap ? 0 : half * Cfg::kCols / 128)];
           const float rs = kSwap ? 0.f : xd[kk * Cfg::kXRows + row] * ws;
-          uint32_t r[2][16];
-          tmem_ld16_async(src, r[0]);
+          constexpr int kLoads = Cfg::kCols / Cfg::kLd;
 #pragma unroll
-          for (int j = 0; j < Cfg::kCols / 16; ++j) {
-            tmem_wait_ld16(r[j & 1]);
-            if (j + 1 < Cfg::kCols / 16) tmem_ld16_async(src + 16 * (j + 1), r[(j + 1) & 1]);
+          for (int j = 0; j < kLoads; ++j) {
+            TmemLd<Cfg::kLd>::wait(r[j & 1]);
+            if (j + 1 < kLoads) {
+              TmemLd<Cfg::kLd>::start(src + Cfg::kLd * (j + 1), r[(j + 1) & 1]);
+            } else {
+              // the accumulator is read out: hand it back, and start on the
+              // next one while this one's last columns are added
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&accfree[ab]);
+              if (kk + 1 < n) begin(g + 1);
+            }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < Cfg::kLd / 2; ++i) {
               const float2 v = make_float2(__uint_as_float(r[j & 1][2 * i]), __uint_as_float(r[j & 1][2 * i + 1]));
               float2 s = make_float2(rs, rs);
               if (kSwap) {
-                s = *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + 16 * j + 2 * i);
+                s = *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + Cfg::kLd * j + 2 * i);
                 s.x *= ws;
                 s.y *= ws;
               }
-              acc[8 * j + i] = ffma2(v, s, acc[8 * j + i]);
+              acc[Cfg::kLd / 2 * j + i] = ffma2(v, s, acc[Cfg::kLd / 2 * j + i]);
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&accfree[ab]);
         }
       }
       if (kSplit) {
         // the ring is idle: every load was multiplied, every MMA is done
-        float* part = reinterpret_cast<float*>(smem);  // [BN][128]
+        float* part = reinterpret_cast<float*>(smem);
+        if (kSwap) {
 #pragma unroll
-        for (int i = 0; i < Cfg::kCols / 2; ++i) {
-          const int c = half * Cfg::kCols + 2 * i;
-          part[c * 128 + row] = acc[i].x;
-          part[(c + 1) * 128 + row] = acc[i].y;
+          for (int i = 0; i < Cfg::kCols / 2; ++i) {
+            const int c = half * Cfg::kCols + 2 * i;
+            part[c * Cfg::kPartRow + row] = acc[i].x;
+            part[(c + 1) * Cfg::kPartRow + row] = acc[i].y;
+          }
+        } else {
+          float4* p = reinterpret_cast<float4*>(part + row * Cfg::kPartRow + half * Cfg::kCols);
+#pragma unroll
+          for (int i = 0; i < Cfg::kCols / 4; ++i)
+            p[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
         }
         continue;
       }
@@ -414,11 +508,12 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     __syncwarp();
     cluster_sync();
     const int x0 = (first % m_tiles) * Cfg::kXRows, w0 = (first / m_tiles) * Cfg::kWRows;
-    const int used = a.M - x0 < BN ? a.M - x0 : BN;  // tokens of this tile
+    const int used = a.M - x0 < Cfg::kXRows ? a.M - x0 : Cfg::kXRows;  // tokens of this tile
     const int c0 = used * rank / split, c1 = used * (rank + 1) / split;
-    for (int e = threadIdx.x; e < (c1 - c0) * 32; e += Cfg::kThreads) {
-      const int c = c0 + e / 32, r = e % 32 * 4;
-      const uint32_t at = smem_u32(smem) + (uint32_t)(c * 128 + r) * 4;
+    constexpr int kQuads = Cfg::kWRows / 4;
+    for (int e = threadIdx.x; e < (c1 - c0) * kQuads; e += Cfg::kThreads) {
+      const int c = c0 + e / kQuads, r = e % kQuads * 4;
+      const uint32_t at = smem_u32(smem) + (uint32_t)(c * Cfg::kPartRow + r) * 4;
       float4 v = ld_cluster_f4(at, 0);
       for (int p = 1; p < split; ++p) {
         const float4 u = ld_cluster_f4(at, (uint32_t)p);

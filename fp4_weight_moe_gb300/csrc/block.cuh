@@ -8,10 +8,24 @@ namespace moe_fp4 {
 
 cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,
                                 int64_t s_row, int64_t s_blk, int M, int K, cudaStream_t st);
+// A product's weight scales, addend, output and sizes.
+struct Fp8Product {
+  const float* ws;
+  int64_t ws_row;
+  const void* add;
+  int64_t add_row;
+  void* out;
+  int64_t out_row;
+  int out_f32;
+  int M, N, K;
+};
+// `after_quantizer`: the stream's last launch is launch_fp8_quantize of x.
 cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
-                              const void* w, int64_t w_row, const float* ws, int64_t ws_row, const void* add,
-                              int64_t add_row, void* out, int64_t out_row, int out_f32, int M, int N, int K,
-                              cudaStream_t st);
+                              const void* w, int64_t w_row, Fp8Product p, bool after_quantizer, cudaStream_t st);
+// BF16 x, where fp8_linear_is_fused(M, K).
+bool fp8_linear_is_fused(int M, int K);
+cudaError_t launch_fp8_linear_fused(const void* x, int64_t x_row, const void* w, int64_t w_row, Fp8Product p,
+                                    cudaStream_t st);
 cudaError_t fp8_status_address(void** p);
 
 struct NormArgs {

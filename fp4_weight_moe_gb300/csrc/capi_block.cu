@@ -75,8 +75,9 @@ int moe_fp4_fp8_matmul(const void* x_q, int64_t x_row, const float* x_s, int64_t
   st = check_fp8_operands(x_q, x_row, w, w_row, w_s, ws_row, add_bf16, add_row, out, out_row, out_f32, M, N, K);
   if (st != MOE_FP4_OK) return st;
   if (!x_s || !aligned(x_s, 4) || x_row % 16 != 0 || xs_row < 0 || xs_block < 0) return MOE_FP4_EINVAL;
-  return done(launch_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, w_s, ws_row, add_bf16, add_row, out,
-                                out_row, out_f32, M, N, K, static_cast<cudaStream_t>(stream)));
+  const Fp8Product p = {w_s, ws_row, add_bf16, add_row, out, out_row, out_f32, M, N, K};
+  return done(launch_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, p, false,
+                                static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_fp4_fp8_linear_workspace_bytes(int M_max, int K) {
@@ -94,14 +95,17 @@ int moe_fp4_fp8_linear(const void* x_bf16, int64_t x_row, const void* w, int64_t
   st = check_fp8_operands(x_bf16, x_row, w, w_row, w_s, ws_row, add_bf16, add_row, out, out_row, out_f32, M, N, K);
   if (st != MOE_FP4_OK) return st;
   if (x_row % 8 != 0) return MOE_FP4_EINVAL;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < moe_fp4_fp8_linear_workspace_bytes(M, K))
+  const bool fused = fp8_linear_is_fused(M, K);
+  if (!workspace && !fused) return MOE_FP4_EWORKSPACE;
+  if (workspace && (!aligned(workspace, 256) || workspace_bytes < moe_fp4_fp8_linear_workspace_bytes(M, K)))
     return MOE_FP4_EWORKSPACE;
+  const Fp8Product p = {w_s, ws_row, add_bf16, add_row, out, out_row, out_f32, M, N, K};
+  if (fused) return done(launch_fp8_linear_fused(x_bf16, x_row, w, w_row, p, static_cast<cudaStream_t>(stream)));
   float* s = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)M * K));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_fp8_quantize(x_bf16, x_row, nullptr, workspace, K, s, 1, M, M, K, cs);
   if (e != cudaSuccess) return report_cuda_error(e);
-  return done(launch_fp8_matmul(workspace, K, s, 1, M, w, w_row, w_s, ws_row, add_bf16, add_row, out, out_row, out_f32,
-                                M, N, K, cs));
+  return done(launch_fp8_matmul(workspace, K, s, 1, M, w, w_row, p, true, cs));
 }
 
 int moe_fp4_fp8_status(uint32_t* flags, int clear, void* stream) {

@@ -1,6 +1,7 @@
 // FP8 products with a scale per block of 128 (moe_fp4_fp8_*): the activation
 // quantiser and the launches of the product kernels of gemm_fp8.cuh.
 #include "block.cuh"
+#include "fp8_quant.cuh"
 #include "gemm_fp8.cuh"
 #include "host.cuh"
 
@@ -12,27 +13,11 @@ static __device__ uint32_t g_fp8_status;
 cudaError_t fp8_status_address(void** p) { return cudaGetSymbolAddress(p, g_fp8_status); }
 
 // ---------------------------------------------------------------- quantiser
-// Per row and 128 columns: s = max|v| / 448 (1 where that is zero),
-// q = e4m3_rn(v / s), each step an IEEE FP32 operation; v is the input, or
-// act(gate) * up of a gated row [gate | up].  HBM bound: 16 lanes hold one
-// block's 128 elements (16 bytes of BF16 each), so the block maximum is four
-// shuffles and a block is read and written once.
-__device__ __forceinline__ void bf16x8_to_float(uint4 u, float (&v)[8]) {
-  const uint32_t p[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(p[i] << 16);
-    v[2 * i + 1] = __uint_as_float(p[i] & 0xffff0000u);
-  }
-}
-
-// Four floats -> four E4M3 bytes (round to nearest even, saturating).
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
-}
+// Per row and 128 columns: s = max|v| / 448 (1 where that is zero), q =
+// e4m3_rn(v / s), each step an IEEE FP32 operation; v is the input, or
+// act(gate) * up of a gated row [gate | up].  HBM bound: a warp takes 1024
+// columns of a row, all its loads (four of 16 bytes per lane) under way
+// before the first block's maximum.
 
 // SiLU in full FP32 precision: the scale of a block follows its largest
 // product, and an element near the middle of two E4M3 values turns on it.
@@ -41,64 +26,64 @@ __device__ __forceinline__ float gated_exact(float g, float u, const ActParams& 
   return gated_act(g, u, act);
 }
 
+constexpr int kQuantCols = 1024;  // columns per warp
+
 template <bool kGated>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __restrict__ x, int64_t x_row, ActParams act,
                                                            uint8_t* __restrict__ q, int64_t q_row,
                                                            float* __restrict__ s, int64_t s_row, int64_t s_blk, int M,
                                                            int K) {
-  const int nb = (K + 127) / 128;
-  const int64_t units = (int64_t)M * nb;
-  const int lane16 = threadIdx.x & 15;
-  // the stride is a multiple of the two units of a warp, so a warp's 32 lanes
-  // leave the loop together but for the last unit
-  for (int64_t u = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 16; u < ((units + 1) & ~(int64_t)1);
-       u += (int64_t)gridDim.x * blockDim.x / 16) {
-    const bool have = u < units;
-    const int64_t m = have ? u / nb : 0;
-    const int b = have ? (int)(u % nb) : 0;
-    const int k = b * 128 + lane16 * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (have && k < K) {
-      bf16x8_to_float(*reinterpret_cast<const uint4*>(x + m * x_row + k), v);
-      if (kGated) {
-        float up[8];
-        bf16x8_to_float(*reinterpret_cast<const uint4*>(x + m * x_row + K + k), up);
+  pdl_launch_dependents();
+  const unsigned groups = (unsigned)(K + kQuantCols - 1) / kQuantCols;
+  const unsigned task = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+  const unsigned m = task / groups;
+  if (m >= (unsigned)M) return;
+  const int lane = threadIdx.x & 31;
+  const int k0 = (int)(task % groups) * kQuantCols + lane * 8;
+  const uint16_t* row = x + m * x_row;
+  uint4 raw[4], raw_up[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = gated_exact(v[i], up[i], act);
-      }
+  for (int i = 0; i < 4; ++i) {
+    const int k = k0 + i * 256;
+    raw[i] = raw_up[i] = make_uint4(0, 0, 0, 0);
+    if (k < K) {
+      raw[i] = *reinterpret_cast<const uint4*>(row + k);
+      if (kGated) raw_up[i] = *reinterpret_cast<const uint4*>(row + K + k);
     }
-    float amax = 0.f;
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  for (int i = 0; i < 4; ++i) {
+    const int k = k0 + i * 256;
+    if ((k & ~255) >= K) break;  // (the whole warp)
+    float v[8];
+    bf16x8_to_float(raw[i], v);
+    if (kGated) {
+      float up[8];
+      bf16x8_to_float(raw_up[i], up);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float sc = __fdiv_rn(amax, 448.f);
-    if (sc == 0.f) sc = 1.f;  // an all-zero block, or one below FP32's reach
-    if (have && k < K) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], sc);
-      *reinterpret_cast<uint2*>(q + m * q_row + k) =
-          make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+      for (int j = 0; j < 8; ++j) v[j] = gated_exact(v[j], up[j], act);
     }
-    if (have && lane16 == 0) s[m * s_row + (int64_t)b * s_blk] = sc;
+    const float sc = block_scale(block_amax(v));
+    if (k < K) {
+      *reinterpret_cast<uint2*>(q + m * q_row + k) = e4m3_quotients(v, sc);
+      if ((lane & 15) == 0) s[m * s_row + (int64_t)(k / 128) * s_blk] = sc;
+    }
   }
 }
 
 cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,
                                 int64_t s_row, int64_t s_blk, int M, int K, cudaStream_t st) {
-  int sms = 0;
-  cudaError_t e = current_device_sms(&sms);
-  if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)M * ((K + 127) / 128);
-  const int64_t want = (units + 15) / 16, most = (int64_t)sms * 8;
-  const unsigned grid = (unsigned)(want < most ? want : most);
+  // (tasks fit 32 bits: each stands for up to 1024 values in memory)
+  const int64_t tasks = (int64_t)M * ((K + kQuantCols - 1) / kQuantCols);
+  const unsigned warps = tasks < 1024 ? 2 : 8;  // few tasks: spread over the SMs
+  const unsigned grid = (unsigned)((tasks + warps - 1) / warps);
   const ActParams none = {MOE_FP4_ACT_SILU, 0.f, 0.f, 0.f};
   if (act)
-    fp8_quantize_kernel<true><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), x_row, *act,
-                                                    static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
+    fp8_quantize_kernel<true><<<grid, 32 * warps, 0, st>>>(static_cast<const uint16_t*>(x), x_row, *act,
+                                                           static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
   else
-    fp8_quantize_kernel<false><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(x), x_row, none,
-                                                     static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
+    fp8_quantize_kernel<false><<<grid, 32 * warps, 0, st>>>(static_cast<const uint16_t*>(x), x_row, none,
+                                                            static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
   return cudaGetLastError();
 }
 
@@ -118,10 +103,67 @@ __global__ void __launch_bounds__(F8Cfg<BN, kSwap, kTwo>::kThreads, kTwo ? 2 : 1
   gemm_fp8_persistent<BN, kSwap, kTwo, true>(&map_a, &map_b, a, split);
 }
 
+// The same for at most 16 BF16 tokens (a.xb), quantised by the kernel.
+__global__ void __launch_bounds__(F8Cfg<16, true, true, true>::kThreads, 2)
+    fp8_linear_kernel(const __grid_constant__ CUtensorMap map_w, Fp8Args a, int split) {
+  a.err = &g_fp8_status;
+  gemm_fp8_persistent<16, true, true, true, true>(&map_w, &map_w, a, split);
+}
+
+// The product kernels' arguments but for the activations.
+static Fp8Args args_of(const Fp8Product& p) {
+  Fp8Args a = {};
+  a.ws = p.ws;
+  a.ws_row = p.ws_row;
+  a.add = static_cast<const __nv_bfloat16*>(p.add);
+  a.add_row = p.add_row;
+  a.out = p.out;
+  a.out_row = p.out_row;
+  a.out_f32 = p.out_f32;
+  a.M = p.M;
+  a.N = p.N;
+  a.K = p.K;
+  a.vec = ((uintptr_t)p.out & 15u) == 0 && (p.out_row * (p.out_f32 ? 4 : 2)) % 16 == 0 &&
+          (!p.add || (((uintptr_t)p.add & 15u) == 0 && p.add_row % 8 == 0));
+  return a;
+}
+
 struct Operands {
   const void *x, *w;
   int64_t x_row, w_row;
+  bool after_quantizer;  // the launch before this one on the stream is the quantiser of x
 };
+
+// Launch with a cluster of `split` CTAs and, behind our own quantiser, with
+// programmatic dependent launch: the kernel's prologue and its first weight
+// loads then run beside the quantiser, and griddepcontrol.wait comes before
+// everything else it reads.  (The quantiser itself is launched in plain
+// stream order, so whatever wrote the weights has finished.)
+template <class Kern, class... Args>
+static cudaError_t launch_product(Kern kern, int64_t ctas, int threads, size_t smem, int split, bool dependent,
+                                  cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (split > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = (unsigned)split;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (dependent) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)ctas);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = n;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
 
 static cudaError_t encode(CUtensorMap* mx, CUtensorMap* mw, const Operands& o, const Fp8Args& a, int x_rows,
                           int w_rows) {
@@ -141,9 +183,8 @@ static cudaError_t launch_gemm(const Operands& o, const Fp8Args& a, int sms, cud
   if (e != cudaSuccess) return e;
   const int64_t tiles =
       (int64_t)((a.M + Cfg::kXRows - 1) / Cfg::kXRows) * ((a.N + Cfg::kWRows - 1) / Cfg::kWRows);
-  const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
-  fp8_gemm_kernel<BN, kSwap><<<grid, Cfg::kThreads, Cfg::kSmem, st>>>(kSwap ? mw : mx, kSwap ? mx : mw, a);
-  return cudaGetLastError();
+  return launch_product(fp8_gemm_kernel<BN, kSwap>, tiles < sms ? tiles : sms, Cfg::kThreads, Cfg::kSmem, 1,
+                        o.after_quantizer, st, kSwap ? mw : mx, kSwap ? mx : mw, a);
 }
 
 template <int BN, bool kSwap, bool kTwo>
@@ -154,48 +195,57 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
   static bool seen[64];
   if (e == cudaSuccess) e = allow_smem(fp8_split_kernel<BN, kSwap, kTwo>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)(tiles * split));
-  c.blockDim = dim3(Cfg::kThreads);
-  c.dynamicSmemBytes = Cfg::kSmem;
-  c.stream = st;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, fp8_split_kernel<BN, kSwap, kTwo>, kSwap ? mw : mx, kSwap ? mx : mw, a, split);
+  return launch_product(fp8_split_kernel<BN, kSwap, kTwo>, (int64_t)tiles * split, Cfg::kThreads, Cfg::kSmem, split,
+                        o.after_quantizer, st, kSwap ? mw : mx, kSwap ? mx : mw, a, split);
 }
 
-cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
-                              const void* w, int64_t w_row, const float* ws, int64_t ws_row, const void* add,
-                              int64_t add_row, void* out, int64_t out_row, int out_f32, int M, int N, int K,
-                              cudaStream_t st) {
+// Few tiles: K is split over a cluster until the CTAs fill `slots`, with at
+// least two K blocks each.  Up to 16 tokens a CTA has at most 16 blocks
+// where eight CTAs can manage that: the kernel that quantises its own tokens
+// holds as many (and shares this rule, so that its results are the same).
+static int k_split(int64_t tiles, int slots, int nk, int bn) {
+  int split = 1;
+  while (split < 8 && nk >= 4 * split && (tiles * split * 2 <= slots || (bn == 16 && nk > 16 * split && nk <= 128)))
+    split *= 2;
+  return split;
+}
+
+// M <= 16 and K <= 16384: one launch, no workspace.
+bool fp8_linear_is_fused(int M, int K) { return M <= 16 && K <= 128 * 128; }
+
+cudaError_t launch_fp8_linear_fused(const void* x, int64_t x_row, const void* w, int64_t w_row, Fp8Product p,
+                                    cudaStream_t st) {
+  using Cfg = F8Cfg<16, true, true, true>;
   int sms = 0;
   cudaError_t e = current_device_sms(&sms);
   if (e != cudaSuccess) return e;
-  Fp8Args a = {};
+  Fp8Args a = args_of(p);
+  a.xb = static_cast<const uint16_t*>(x);
+  a.xb_row = x_row;
+  CUtensorMap mw;
+  if (encode_u8_map_2d(&mw, w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)w_row, kF8BM) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  static bool seen[64];
+  e = allow_smem(fp8_linear_kernel, Cfg::kSmem, seen);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (a.N + 127) / 128;
+  const int split = k_split(tiles, 2 * sms, (a.K + 127) / 128, 16);
+  return launch_product(fp8_linear_kernel, tiles * split, Cfg::kThreads, Cfg::kSmem, split, false, st, mw, a, split);
+}
+
+cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
+                              const void* w, int64_t w_row, Fp8Product p, bool after_quantizer, cudaStream_t st) {
+  int sms = 0;
+  cudaError_t e = current_device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  Fp8Args a = args_of(p);
   a.xs = xs;
   a.xs_row = xs_row;
   a.xs_blk = xs_blk;
-  a.ws = ws;
-  a.ws_row = ws_row;
-  a.add = static_cast<const __nv_bfloat16*>(add);
-  a.add_row = add_row;
-  a.out = out;
-  a.out_row = out_row;
-  a.out_f32 = out_f32;
-  a.M = M;
-  a.N = N;
-  a.K = K;
-  a.vec = ((uintptr_t)out & 15u) == 0 && (out_row * (out_f32 ? 4 : 2)) % 16 == 0 &&
-          (!add || (((uintptr_t)add & 15u) == 0 && add_row % 8 == 0));
-  const Operands o = {x, w, x_row, w_row};
-  // Few tiles: K is split over a cluster until the CTAs fill the GPU, with at
-  // least two K blocks each.  Up to 64 tokens the weights' 128 rows lie on
-  // the MMA's row side and the tokens (16, 32 or 64) on its column side, two
-  // CTAs per SM; past that the tokens take the row side, where a scale
+  const int M = p.M, N = p.N, K = p.K;
+  const Operands o = {x, w, x_row, w_row, after_quantizer};
+  // Up to 64 tokens the weights' 128 rows lie on the MMA's row side and the
+  // tokens (16, 32 or 64) on its column side, two CTAs per SM; past that the tokens take the row side, where a scale
   // thread's activation scale is one value instead of one per column.
   // Measured (us, K x N): M=128 7168 x 4096, tokens on columns 14.5 / on rows
   // 11.9; 2048 x 7168 11.2 / 9.6; M=64, tokens on rows 22.6 against 13.0 and
@@ -205,9 +255,8 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);
   const int slots = bn == 128 ? sms : 2 * sms;
-  if (tiles <= slots / 2) {
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= slots && nk >= 4 * split) split *= 2;
+  if (tiles <= slots / 2 || bn == 16) {
+    const int split = k_split(tiles, slots, nk, bn);
     switch (bn) {
       case 16: return launch_split<16, true, true>(o, a, (int)tiles, split, st);
       case 32: return launch_split<32, true, true>(o, a, (int)tiles, split, st);

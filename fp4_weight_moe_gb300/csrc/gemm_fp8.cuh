@@ -24,6 +24,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "fp8_quant.cuh"
 #include "tcgen05.cuh"
 
 namespace moe_fp4 {
@@ -35,6 +36,8 @@ constexpr int kF8Chunk = 16;   // K blocks of scales per shared-memory chunk
 struct Fp8Args {
   const float* xs;  // activation scales, xs[m * xs_row + b * xs_blk]
   int64_t xs_row, xs_blk;
+  const uint16_t* xb;  // kFuse: the BF16 activations, xb[m * xb_row + k], in place of E4M3 ones and xs
+  int64_t xb_row;
   const float* ws;  // weight scales, ws[(n / 128) * ws_row + b]
   int64_t ws_row;
   const __nv_bfloat16* add;  // added to the product before its rounding (or null)
@@ -47,9 +50,11 @@ struct Fp8Args {
   uint32_t* err;
 };
 
-// kTwo: shared memory and tensor memory for two CTAs per SM.
-template <int BN, bool kSwap, bool kTwo = false>
+// kTwo: shared memory and tensor memory for two CTAs per SM.  kFuse: the
+// tokens are quantised by the kernel into kF8Chunk K blocks of their own.
+template <int BN, bool kSwap, bool kTwo = false, bool kFuse = false>
 struct F8Cfg {
+  static_assert(!kFuse || kSwap, "the kernel quantises a few tokens only");
   static constexpr int kHalves = BN >= 64 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
   static constexpr int kLd = kCols / 2 < 32 ? kCols / 2 : 32;  // ... per tensor-memory load (an even count of them)
@@ -66,13 +71,14 @@ struct F8Cfg {
   static constexpr int kWRows = kSwap ? kF8BM : BN;
   static constexpr int kWBlocks = kWRows / 128 < 1 ? 1 : kWRows / 128;
   static constexpr uint32_t kStageA = kF8BM * kF8BK;
-  static constexpr uint32_t kStageB = BN * kF8BK;
+  static constexpr uint32_t kStageB = kFuse ? 0 : BN * kF8BK;
+  static constexpr uint32_t kXqBytes = kFuse ? kF8Chunk * BN * kF8BK : 0;
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
   static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
   static constexpr uint32_t kBarBytes = 256;
-  static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes;
+  static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes - kXqBytes;
   static constexpr int kStages = kBudget / kStageBytes > 6 ? 6 : (int)(kBudget / kStageBytes);
-  static constexpr uint32_t kSmem = kStages * kStageBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
+  static constexpr uint32_t kSmem = kStages * kStageBytes + kXqBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(kStages >= 3 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
   static_assert(!kTwo || kTmemCols <= 256, "tensor memory of two CTAs");
@@ -81,7 +87,7 @@ struct F8Cfg {
   // spread over the banks)
   static constexpr uint32_t kPartRow = kSwap ? 128 : BN + 4;
   static_assert(BN > 128 || (kSwap ? BN : 128) * kPartRow * 4u <= kStages * kStageBytes, "partial sums fit the ring");
-  static_assert((2 * kStages + 2 * kAcc) * 8 + 4 <= (int)kBarBytes, "barrier block");
+  static_assert((2 * kStages + 2 * kAcc + 1) * 8 + 4 <= (int)kBarBytes, "barrier block");
 };
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: E4M3 A and B (format
@@ -281,20 +287,29 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
 // leave their partial tiles in their shared memory, and each sums the
 // cluster's partials, in rank order, for its share of the tile's tokens and
 // stores them.
-template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false>
+//
+// kFuse (with kSplit; at most kF8Chunk K blocks per CTA): the scale warps
+// first quantise the BF16 tokens of the CTA's K range into shared memory,
+// in the swizzled layout the MMA reads, while the weights are on their way.
+// Rows past M stay unwritten: they reach only accumulator columns that are
+// not stored.
+template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false, bool kFuse = false>
 __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
                                                     const Fp8Args& a, int split = 1) {
-  using Cfg = F8Cfg<BN, kSwap, kTwo>;
+  static_assert(!kFuse || kSplit, "one tile per CTA");
+  using Cfg = F8Cfg<BN, kSwap, kTwo, kFuse>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  float* xsc = reinterpret_cast<float*>(smem + S * Cfg::kStageBytes);       // [2][kF8Chunk][kXRows]
+  uint8_t* xq = smem + S * Cfg::kStageBytes;                                // kFuse: [kF8Chunk][BN][128]
+  float* xsc = reinterpret_cast<float*>(xq + Cfg::kXqBytes);                // [2][kF8Chunk][kXRows]
   float* wsc = xsc + 2 * kF8Chunk * Cfg::kXRows;                            // [2][kF8Chunk][kWBlocks]
   uint64_t* full = reinterpret_cast<uint64_t*>(wsc + 2 * kF8Chunk * Cfg::kWBlocks);
   uint64_t* empty = full + S;
   uint64_t* done = empty + S;     // [NA]
   uint64_t* accfree = done + NA;  // [NA]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accfree + NA);
+  uint64_t* xready = accfree + NA;  // kFuse: the tokens are quantised
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xready + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m_tiles = (a.M + Cfg::kXRows - 1) / Cfg::kXRows;
@@ -318,9 +333,10 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       mbar_init(&done[b], 1);
       mbar_init(&accfree[b], Cfg::kScaleWarps);
     }
+    mbar_init(xready, Cfg::kScaleWarps);
     fence_mbar_init();
     tma_prefetch_desc(map_a);
-    tma_prefetch_desc(map_b);
+    if (!kFuse) tma_prefetch_desc(map_b);
   }
   if (warp == 1) tmem_alloc(tmem_slot, Cfg::kTmemCols);
   tc_fence_before();
@@ -334,6 +350,19 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     if (Cfg::kMoveRegs) regs_dec<40>();
     if (warp == 0) {
       if (lane == 0) {
+        auto load_w = [&](int slot, int s, int w0) {
+          uint8_t* st = smem + slot * Cfg::kStageBytes;
+          mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
+          tma_load_2d(kSwap ? st : st + Cfg::kStageA, kSwap ? map_a : map_b, (kb0 + s) * kF8BK, w0, &full[slot]);
+        };
+        auto load_x = [&](int slot, int s, int x0) {
+          uint8_t* st = smem + slot * Cfg::kStageBytes;
+          tma_load_2d(kSwap ? st + Cfg::kStageA : st, kSwap ? map_b : map_a, (kb0 + s) * kF8BK, x0, &full[slot]);
+        };
+        // the first stages' weights do not depend on the quantiser before us
+        const int ahead = first < tiles ? (nk < S ? nk : S) : 0;
+        for (int s = 0; s < ahead; ++s) load_w(s, s, (first / m_tiles) * Cfg::kWRows);
+        pdl_wait();
         int g = 0;
         bool ok = true;
         for (int idx = first; ok && idx < tiles; idx += step) {
@@ -344,17 +373,15 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
               ok = false;
               break;
             }
-            uint8_t* st = smem + slot * Cfg::kStageBytes;
-            mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
-            tma_load_2d(st, map_a, (kb0 + s) * kF8BK, kSwap ? w0 : x0, &full[slot]);
-            tma_load_2d(st + Cfg::kStageA, map_b, (kb0 + s) * kF8BK, kSwap ? x0 : w0, &full[slot]);
+            if (g >= ahead) load_w(slot, s, w0);
+            if (!kFuse) load_x(slot, s, x0);
           }
         }
       }
     } else if (warp == 1) {
       constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
       int g = 0;
-      bool ok = true;
+      bool ok = !kFuse || __all_sync(0xffffffffu, mbar_wait(xready, 0, err, 8u));
       for (int idx = first; ok && idx < tiles; idx += step) {
         for (int s = 0; s < nk; ++s, ++g) {
           const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
@@ -367,7 +394,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           tc_fence_after();
           const uint32_t acc = tmem + (uint32_t)(ab * BN);
           const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
-          const uint64_t db = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes + Cfg::kStageA), 16, 1024, kLayoutSW128);
+          const uint8_t* bst = kFuse ? xq + s * (BN * kF8BK) : smem + slot * Cfg::kStageBytes + Cfg::kStageA;
+          const uint64_t db = smem_desc(smem_u32(bst), 16, 1024, kLayoutSW128);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
             mma_f8_warp(acc, da + 2 * k, db + 2 * k, idesc, k > 0);
@@ -387,7 +415,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
       const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
       float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
-      for (int i = t; i < n * Cfg::kXRows; i += 32 * Cfg::kScaleWarps) {
+      for (int i = kFuse ? n * Cfg::kXRows : t; i < n * Cfg::kXRows; i += 32 * Cfg::kScaleWarps) {
         const int m = x0 + i % Cfg::kXRows;  // rows past M read the last row's scale; their sums are not stored
         cp_async_4(xd + i, a.xs + (int64_t)(m < a.M ? m : a.M - 1) * a.xs_row + (int64_t)(kb0 + c0 + i / Cfg::kXRows) * a.xs_blk);
       }
@@ -398,9 +426,42 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         cp_async_4(wd + t, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + kb0 + c0 + t / Cfg::kWBlocks);
       }
     };
+    pdl_wait();
     int g = 0, gc = 0;
     bool ok = true;
     if (first < tiles) load_chunk(first, 0, 0);
+    if (kFuse) {
+      // a block of 128 values per 16 lanes, kAhead blocks under way at once
+      constexpr int kUnits = 2 * Cfg::kScaleWarps, kAhead = 4;
+      const int x0 = (first % m_tiles) * Cfg::kXRows;
+      const int used = a.M - x0 < BN ? a.M - x0 : BN;
+      const int l = lane & 15, units = used * nk;
+      for (int u0 = t / 16; u0 - (lane >> 4) < units; u0 += kUnits * kAhead) {
+        uint4 raw[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int u = u0 + i * kUnits, k = (kb0 + u % nk) * kF8BK + l * 8;
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (u < units && k < a.K)
+            raw[i] = *reinterpret_cast<const uint4*>(a.xb + (int64_t)(x0 + u / nk) * a.xb_row + k);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int u = u0 + i * kUnits, kb = u % nk, r = u / nk;
+          float v[8];
+          bf16x8_to_float(raw[i], v);
+          const float sc = block_scale(block_amax(v));
+          if (u < units) {
+            *reinterpret_cast<uint2*>(xq + kb * (BN * kF8BK) + r * kF8BK + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8) =
+                e4m3_quotients(v, sc);
+            if (l == 0) xsc[kb * BN + r] = sc;
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(xready);
+    }
     for (int idx = first; idx < tiles; idx += step) {
       const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
       float2 acc[Cfg::kCols / 2];

@@ -9,6 +9,7 @@
 // Sums, r' and the norms are FP32; r' enters the second norm before it is
 // rounded to the residual stream's type.
 #include "block.cuh"
+#include "fp8_quant.cuh"
 #include "host.cuh"
 
 namespace moe_fp4 {
@@ -161,27 +162,11 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a, int res_f3
     if (a.q) {
       // the BF16 values' FP8 form, so that it is the one a quantiser of n
       // gives; 16 lanes hold a block of 128 columns
-      float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = k + j < a.H ? __bfloat162float(__float2bfloat16_rn(v[i][j])) : 0.f;
-        amax = fmaxf(amax, fabsf(v[i][j]));
-      }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float sc = __fdiv_rn(amax, 448.f);
-      if (sc == 0.f) sc = 1.f;
+      for (int j = 0; j < 8; ++j) v[i][j] = k + j < a.H ? __bfloat162float(__float2bfloat16_rn(v[i][j])) : 0.f;
+      const float sc = block_scale(block_amax(v[i]));
       if (k < a.H) {
-        uint32_t u[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint16_t lo, hi;
-          const float* p = &v[i][4 * j];
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(p[1], sc)), "f"(__fdiv_rn(p[0], sc)));
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(p[3], sc)), "f"(__fdiv_rn(p[2], sc)));
-          u[j] = (uint32_t)lo | ((uint32_t)hi << 16);
-        }
-        *reinterpret_cast<uint2*>(a.q + m * a.q_row + k) = make_uint2(u[0], u[1]);
+        *reinterpret_cast<uint2*>(a.q + m * a.q_row + k) = e4m3_quotients(v[i], sc);
         if ((threadIdx.x & 15) == 0) a.s[m * a.s_row + (int64_t)(k / 128) * a.s_blk] = sc;
       }
     }

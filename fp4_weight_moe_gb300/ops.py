@@ -159,18 +159,23 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``fp8_matmul`` of the bfloat16 ``x [M, K]``, quantised as
     ``fp8_quantize`` does.  ``workspace`` (alloc_fp8_workspace) holds the
-    quantised rows; without one the call takes it from torch's allocator."""
+    quantised rows; without one the call takes it from torch's allocator (up
+    to 16 rows of at most 16384 columns need none)."""
     go = _Launch(x, stream)
     row = _matrix(x, "x", (_BF16,), go.device)
     M, K = x.shape
     args, out = _product_operands(w, w_scale, addend, out, out_dtype, go, M, K)
+    ws_ptr = ws_bytes = 0
     if workspace is None:
-        with go:
-            workspace = torch.empty(_capi.moe_fp4_fp8_linear_workspace_bytes(M, K), dtype=torch.uint8,
-                                    device=go.device)
+        if M > 16 or K > 16384:
+            with go:
+                workspace = torch.empty(_capi.moe_fp4_fp8_linear_workspace_bytes(M, K), dtype=torch.uint8,
+                                        device=go.device)
     elif workspace.device != go.device or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on x's device")
-    _capi.moe_fp4_fp8_linear(x.data_ptr(), row, *args, workspace.data_ptr(), workspace.nbytes, go.stream)
+    if workspace is not None:
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    _capi.moe_fp4_fp8_linear(x.data_ptr(), row, *args, ws_ptr, ws_bytes, go.stream)
     return out
 
 

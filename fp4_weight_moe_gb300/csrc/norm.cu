@@ -8,6 +8,7 @@
 // once; two block sums (of b^2, then of r'^2) are all that separates them.
 // Sums, r' and the norms are FP32; r' enters the second norm before it is
 // rounded to the residual stream's type.
+#include <cstdlib>
 #include "block.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"
@@ -85,59 +86,111 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
+// Eight residual values as loaded: packed (bf16) or not (f32).
+template <bool kF32>
+struct Raw8 {
+  uint32_t w[kF32 ? 8 : 4];
+  template <bool kVec>
+  __device__ __forceinline__ void load(const void* p, int64_t base, int k, int H) {
+    if (kVec) {
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (base + k) * (kF32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
+        uint4 u;
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(q + i)
+                     : "memory");
+        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+      }
+    } else {
+      float v[8];
+      load8<false>(p, kF32, base, k, H, v);
+#pragma unroll
+      for (int i = 0; i < (kF32 ? 8 : 4); ++i)
+        w[i] = kF32 ? __float_as_uint(v[i])
+                    : (__float_as_uint(v[2 * i]) >> 16) | (__float_as_uint(v[2 * i + 1]) & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = kF32 ? __uint_as_float(w[i])
+                  : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+
 // kCh chunks of eight columns per thread: chunk c = threadIdx.x + i *
-// blockDim.x covers columns 8c .. 8c + 7.
-template <int kCh, bool kVec>
-__global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a, int res_f32) {
+// blockDim.x covers columns 8c .. 8c + 7.  All of a row's loads are under way
+// before the first sum.
+template <int kCh, int kMaxThreads, bool kVec, bool kF32>
+__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][32];
   const int64_t m = blockIdx.x;
   const float inv_h = 1.0f / (float)a.H;
-  float v[kCh][8];  // r'
+  Raw8<kF32> raw[kCh];
+  Raw8<false> rawb[kCh];
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
     const int k = 8 * (threadIdx.x + i * blockDim.x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-    if (k < a.H) load8<kVec>(a.r, res_f32, m * a.r_row, k, a.H, v[i]);
+    raw[i].zero();
+    rawb[i].zero();
+    if (k < a.H) {
+      if (a.b) rawb[i].template load<kVec>(a.b, m * a.b_row, k, a.H);
+      raw[i].template load<kVec>(a.r, m * a.r_row, k, a.H);
+    }
   }
+  float v[kCh][8];  // r'
   if (a.b) {
-    float z[kCh][8];
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kCh; ++i) {
-      const int k = 8 * (threadIdx.x + i * blockDim.x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z[i][j] = 0.f;
-      if (k < a.H) load8<kVec>(a.b, 0, m * a.b_row, k, a.H, z[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += z[i][j] * z[i][j];
-    }
     float inv = 1.f;
-    if (a.w_post) inv = rsqrtf(block_sum(sum, part[0]) * inv_h + a.eps);
-    const float token_gate =
-        a.gate && a.g_col == 0
-            ? (a.g_f32 ? static_cast<const float*>(a.gate)[m * a.g_row]
-                       : __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.gate)[m * a.g_row] << 16))
-            : 1.f;
+    if (a.w_post) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCh; ++i) {
+        float z[8];
+        rawb[i].get(z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum += z[j] * z[j];
+      }
+      inv = rsqrtf(block_sum(sum, part[0]) * inv_h + a.eps);
+    }
+    float token_gate = 1.f;
+    if (a.gate && a.g_col == 0)
+      token_gate = a.g_f32 ? static_cast<const float*>(a.gate)[m * a.g_row]
+                           : __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.gate)[m * a.g_row] << 16);
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
       const int k = 8 * (threadIdx.x + i * blockDim.x);
-      if (k >= a.H) continue;
-      if (a.w_post) {
-        float w[8];
-        load8<kVec>(a.w_post, a.w_f32, 0, k, a.H, w);
+      float z[8];
+      rawb[i].get(z);
+      raw[i].get(v[i]);
+      if (k < a.H) {
+        if (a.w_post) {
+          float w[8];
+          load8<kVec>(a.w_post, a.w_f32, 0, k, a.H, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * inv * (a.offset + w[j]);
+          for (int j = 0; j < 8; ++j) z[j] = z[j] * inv * (a.offset + w[j]);
+        }
+        if (a.gate && a.g_col) {
+          float g[8];
+          load8<kVec>(a.gate, a.g_f32, m * a.g_row, k, a.H, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[j] *= g[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[j] *= token_gate;
+        }
       }
-      if (a.gate) {
-        float g[8];
-        if (a.g_col) load8<kVec>(a.gate, a.g_f32, m * a.g_row, k, a.H, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] *= a.g_col ? g[j] : token_gate;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += a.scale * z[i][j];
+      for (int j = 0; j < 8; ++j) v[i][j] += a.scale * z[j];
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) raw[i].get(v[i]);
   }
   float sum = 0.f;
 #pragma unroll
@@ -145,7 +198,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a, int res_f3
     const int k = 8 * (threadIdx.x + i * blockDim.x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += k + j < a.H ? v[i][j] * v[i][j] : 0.f;
-    if (a.r_out && k < a.H) store8<kVec>(a.r_out, res_f32, m * a.ro_row, k, a.H, v[i]);
+    if (a.r_out && k < a.H) store8<kVec>(a.r_out, kF32, m * a.ro_row, k, a.H, v[i]);
   }
   if (!a.w_pre) return;
   const float inv = rsqrtf(block_sum(sum, part[1]) * inv_h + a.eps);
@@ -173,22 +226,35 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormArgs a, int res_f3
   }
 }
 
-template <int kCh>
-static cudaError_t launch_ch(const NormArgs& a, int res_f32, bool vec, unsigned threads, cudaStream_t st) {
-  if (vec)
-    block_norm_kernel<kCh, true><<<(unsigned)a.M, threads, 0, st>>>(a, res_f32);
+template <int kCh, int kMaxThreads>
+static cudaError_t launch_ch(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {
+  const unsigned threads = (unsigned)((a.H + 256 * kCh - 1) / (256 * kCh)) * 32;
+  const unsigned grid = (unsigned)a.M;
+  if (vec && res_f32)
+    block_norm_kernel<kCh, kMaxThreads, true, true><<<grid, threads, 0, st>>>(a);
+  else if (vec)
+    block_norm_kernel<kCh, kMaxThreads, true, false><<<grid, threads, 0, st>>>(a);
+  else if (res_f32)
+    block_norm_kernel<kCh, kMaxThreads, false, true><<<grid, threads, 0, st>>>(a);
   else
-    block_norm_kernel<kCh, false><<<(unsigned)a.M, threads, 0, st>>>(a, res_f32);
+    block_norm_kernel<kCh, kMaxThreads, false, false><<<grid, threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {
-  const int chunks = (a.H + 7) / 8;
-  const int ch = chunks <= 1024 ? 1 : chunks <= 2048 ? 2 : 4;
-  const unsigned threads = (unsigned)((chunks + 32 * ch - 1) / (32 * ch)) * 32;
-  if (ch == 1) return launch_ch<1>(a, res_f32, vec, threads, st);
-  if (ch == 2) return launch_ch<2>(a, res_f32, vec, threads, st);
-  return launch_ch<4>(a, res_f32, vec, threads, st);
+  int sms = 0;
+  const cudaError_t e = current_device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  if (a.H > 16384) return launch_ch<4, 1024>(a, res_f32, vec, st);
+  if (a.H > 8192) return launch_ch<4, 512>(a, res_f32, vec, st);
+  if (getenv("NCH")) {
+    int c = atoi(getenv("NCH"));
+    if (c == 1) return launch_ch<1, 1024>(a, res_f32, vec, st);
+    if (c == 2) return launch_ch<2, 512>(a, res_f32, vec, st);
+    return launch_ch<4, 256>(a, res_f32, vec, st);
+  }
+  if (a.M <= sms) return launch_ch<1, 1024>(a, res_f32, vec, st);
+  return launch_ch<4, 256>(a, res_f32, vec, st);
 }
 
 }  // namespace moe_fp4

@@ -23,61 +23,64 @@ SCORE_SOFTMAX, SCORE_SIGMOID = _capi.MOE_FP4_SCORE_SOFTMAX, _capi.MOE_FP4_SCORE_
 FP8 = torch.float8_e4m3fn
 _BF16, _F32 = torch.bfloat16, torch.float32
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty
+_PACK_NORM = _capi.MoeFp4BlockNormArgs.PACK.pack
 
 
-class _Launch:
-    """Where a call runs: allocations inside ``with`` come from the launch
-    stream's own pool, so that a caller's explicit ``stream`` never receives
-    memory that work on the current stream may still be using."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("libmoe_fp4 takes CUDA tensors only (there is no CPU path)")
-        self.device = t.device
-        self._ctx = None
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"tensors are on {t.device}, the current device is {torch.cuda.current_device()}")
-        if stream is None:
-            self.stream = _raw_stream(t.device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
-        else:
-            self.stream = stream if isinstance(stream, int) else stream.cuda_stream
-            self._ctx = torch.cuda.stream(stream if not isinstance(stream, int)
-                                          else torch.cuda.ExternalStream(stream, device=t.device))
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
-        return False
+# Each call costs the host as much as a small kernel costs the GPU, so the
+# functions below test what they need in few steps and leave it to _matrix,
+# _vector and _device to find and name what is wrong.
+def _on(stream, t: torch.Tensor):
+    """``stream`` (a torch stream or a raw handle) as the current stream: the
+    call's outputs and workspace then come from that stream's own pool, never
+    from memory that work on another stream may still be using."""
+    _device(t)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=t.device) if isinstance(stream, int) else stream)
 
 
-def _matrix(t: torch.Tensor, name: str, dtypes, dev, rows: Optional[int] = None, cols: Optional[int] = None):
+def _device(t: torch.Tensor) -> int:
+    """The tensor's device index, which must be the current device's."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("libmoe_fp4 takes CUDA tensors only (there is no CPU path)")
+    if i != _current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is {_current_device()}")
+    return i
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes, dev: int, rows: Optional[int] = None, cols: Optional[int] = None):
     """Check a [rows, cols] tensor with contiguous columns; returns its row
     stride."""
+    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 2:
+        r, c = t.shape
+        if (rows is None or r == rows) and (cols is None or c == cols):
+            row, col = t.stride()
+            if col == 1 or c <= 1:
+                return row if r != 1 else c  # (one row has no stride of its own)
+            raise ValueError(f"{name} must have contiguous columns")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}], "
-                         f"not {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must have contiguous columns")
-    return t.stride(0) if t.shape[0] != 1 else t.shape[1]  # (one row has no stride of its own)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
+    raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}], "
+                     f"not {list(t.shape)}")
 
 
-def _vector(t: torch.Tensor, name: str, dtypes, dev, n: int):
+def _vector(t: torch.Tensor, name: str, dtypes, dev: int, n: int):
+    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 1 and t.shape[0] == n and \
+            (n <= 1 or t.stride(0) == 1):
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} values, not {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
+    raise ValueError(f"{name} must be a contiguous vector of {n} values, not {list(t.shape)}")
+
+
+_IS_BF16, _IS_F32, _IS_FP8, _IS_FLOAT = (_BF16,), (_F32,), (FP8,), (_BF16, _F32)
 
 
 def _blocks(n: int) -> int:
@@ -92,36 +95,42 @@ def fp8_quantize(x: torch.Tensor, act: Optional[int] = None, alpha: float = 0.0,
     With ``act`` (ACT_SILU, ACT_GELU_TANH, or ACT_SWIGLUOAI with alpha, beta,
     limit) ``x`` is ``[gate | up] [M, 2K]`` and act(gate) * up is quantised.
     ``s`` is laid out block by block (its strides are (1, M))."""
-    go = _Launch(x, stream)
-    row = _matrix(x, "x", (_BF16,), go.device)
+    if stream is not None:
+        with _on(stream, x):
+            return fp8_quantize(x, act, alpha, beta, limit)
+    dev = _device(x)
+    row = _matrix(x, "x", _IS_BF16, dev)
     M, K = x.shape
     if act is not None:
         if K % 2:
             raise ValueError("a gated x has an even number of columns")
         K //= 2
         act = _capi.MoeFp4Activation(act, alpha, beta, limit)
-    with go:
-        q = torch.empty((M, K), dtype=FP8, device=go.device)
-        s = torch.empty((_blocks(K), M), dtype=_F32, device=go.device)
-    _capi.moe_fp4_fp8_quantize(x.data_ptr(), row, act, q.data_ptr(), K, s.data_ptr(), 1, M, M, K, go.stream)
-    return q, s.t()
+    q = _empty((M, K), dtype=FP8, device=x.device)
+    s = torch.empty_strided((M, _blocks(K)), (1, M), dtype=_F32, device=x.device)
+    _capi.moe_fp4_fp8_quantize(x.data_ptr(), row, act, q.data_ptr(), K, s.data_ptr(), 1, M, M, K, _raw_stream(dev))
+    return q, s
 
 
-def _product_operands(w, w_scale, addend, out, out_dtype, go, M, K):
-    w_row = _matrix(w, "w", (FP8,), go.device, cols=K)
+def _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K):
+    w_row = _matrix(w, "w", _IS_FP8, dev, None, K)
     N = w.shape[0]
-    ws_row = _matrix(w_scale, "w_scale", (_F32,), go.device, _blocks(N), _blocks(K))
-    add_row = 0 if addend is None else _matrix(addend, "addend", (_BF16,), go.device, M, N)
+    ws_row = _matrix(w_scale, "w_scale", _IS_F32, dev, (N + 127) // 128, (K + 127) // 128)
+    add = add_row = 0
+    if addend is not None:
+        add, add_row = addend.data_ptr(), _matrix(addend, "addend", _IS_BF16, dev, M, N)
     if out is None:
-        with go:
-            out = torch.empty((M, N), dtype=out_dtype or _BF16, device=go.device)
-        out_row = N
+        out_dtype = out_dtype or _BF16
+        if out_dtype not in _IS_FLOAT:
+            raise TypeError(f"out must be bfloat16 or float32, not {out_dtype}")
+        out, out_row = _empty((M, N), dtype=out_dtype, device=w.device), N
     else:
-        out_row = _matrix(out, "out", (_BF16, _F32) if out_dtype is None else (out_dtype,), go.device, M, N)
-    if out.dtype is not _BF16 and out.dtype is not _F32:
-        raise TypeError(f"out must be bfloat16 or float32, not {out.dtype}")
-    return (w.data_ptr(), w_row, w_scale.data_ptr(), ws_row, 0 if addend is None else addend.data_ptr(), add_row,
-            out.data_ptr(), out_row, 1 if out.dtype is _F32 else 0, M, N, K), out
+        out_row = _matrix(out, "out", _IS_FLOAT if out_dtype is None else (out_dtype,), dev, M, N)
+        out_dtype = out.dtype
+        if out_dtype not in _IS_FLOAT:
+            raise TypeError(f"out must be bfloat16 or float32, not {out_dtype}")
+    return (w.data_ptr(), w_row, w_scale.data_ptr(), ws_row, add, add_row, out.data_ptr(), out_row,
+            1 if out_dtype is _F32 else 0, M, N, K), out
 
 
 def fp8_matmul(x_q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -131,18 +140,20 @@ def fp8_matmul(x_q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
     ``x_scale [M, ceil(K / 128)]`` (any strides) and E4M3 ``w [N, K]`` with
     scales ``w_scale [ceil(N / 128), ceil(K / 128)]``; out bfloat16 (default)
     or float32, rounded once after the bfloat16 ``addend [M, N]``."""
-    go = _Launch(x_q, stream)
-    row = _matrix(x_q, "x_q", (FP8,), go.device)
+    if stream is not None:
+        with _on(stream, x_q):
+            return fp8_matmul(x_q, x_scale, w, w_scale, out, addend, out_dtype)
+    dev = _device(x_q)
+    row = _matrix(x_q, "x_q", _IS_FP8, dev)
     M, K = x_q.shape
     if x_scale.dtype is not _F32:
         raise TypeError(f"x_scale must be float32, not {x_scale.dtype}")
-    if x_scale.shape != (M, _blocks(K)):
+    if x_scale.shape != (M, (K + 127) // 128):
         raise ValueError(f"x_scale must be [{M}, {_blocks(K)}], not {list(x_scale.shape)}")
-    if x_scale.device != go.device:
-        raise ValueError(f"x_scale is on {x_scale.device}, not {go.device}")
-    args, out = _product_operands(w, w_scale, addend, out, out_dtype, go, M, K)
-    _capi.moe_fp4_fp8_matmul(x_q.data_ptr(), row, x_scale.data_ptr(), x_scale.stride(0), x_scale.stride(1), *args,
-                             go.stream)
+    if x_scale.get_device() != dev:
+        raise ValueError(f"x_scale is on {x_scale.device}, not cuda:{dev}")
+    args, out = _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K)
+    _capi.moe_fp4_fp8_matmul(x_q.data_ptr(), row, x_scale.data_ptr(), *x_scale.stride(), *args, _raw_stream(dev))
     return out
 
 
@@ -161,21 +172,22 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
     ``fp8_quantize`` does.  ``workspace`` (alloc_fp8_workspace) holds the
     quantised rows; without one the call takes it from torch's allocator (up
     to 16 rows of at most 16384 columns need none)."""
-    go = _Launch(x, stream)
-    row = _matrix(x, "x", (_BF16,), go.device)
+    if stream is not None:
+        with _on(stream, x):
+            return fp8_linear(x, w, w_scale, out, addend, out_dtype, workspace)
+    dev = _device(x)
+    row = _matrix(x, "x", _IS_BF16, dev)
     M, K = x.shape
-    args, out = _product_operands(w, w_scale, addend, out, out_dtype, go, M, K)
+    args, out = _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K)
     ws_ptr = ws_bytes = 0
     if workspace is None:
         if M > 16 or K > 16384:
-            with go:
-                workspace = torch.empty(_capi.moe_fp4_fp8_linear_workspace_bytes(M, K), dtype=torch.uint8,
-                                        device=go.device)
-    elif workspace.device != go.device or not workspace.is_contiguous():
+            workspace = _empty(_capi.moe_fp4_fp8_linear_workspace_bytes(M, K), dtype=torch.uint8, device=x.device)
+    elif workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on x's device")
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _capi.moe_fp4_fp8_linear(x.data_ptr(), row, *args, ws_ptr, ws_bytes, go.stream)
+    _capi.moe_fp4_fp8_linear(x.data_ptr(), row, *args, ws_ptr, ws_bytes, _raw_stream(dev))
     return out
 
 
@@ -207,72 +219,73 @@ def block_norm(residual: torch.Tensor, pre_weight: Optional[torch.Tensor] = None
     which may be ``residual``; residual itself without block_out), n bfloat16
     (None without pre_weight).  With ``quantize``, ``(r', n, q, s)``: n as
     ``fp8_quantize`` gives it."""
-    go = _Launch(residual, stream)
-    dev = go.device
-    a = _capi.MoeFp4BlockNormArgs()
-    a.residual_row = _matrix(residual, "residual", (_BF16, _F32), dev)
+    if stream is not None:
+        with _on(stream, residual):
+            return block_norm(residual, pre_weight, block_out, post_weight, gate, scale, eps, weight_offset,
+                              residual_out, quantize)
+    dev = _device(residual)
+    row = _matrix(residual, "residual", _IS_FLOAT, dev)
     M, H = residual.shape
-    a.M, a.H = M, H
-    a.residual = residual.data_ptr()
-    a.residual_f32 = 1 if residual.dtype is _F32 else 0
-    a.scale, a.eps, a.offset = scale, eps, weight_offset
-    wdt = (_BF16, _F32)
-    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight)):
-        if w is not None:
-            _vector(w, name, wdt, dev, H)
-            a.weights_f32 = 1 if w.dtype is _F32 else 0
-            wdt = (w.dtype,)
-    if block_out is None:
-        if post_weight is not None or gate is not None:
-            raise ValueError("post_weight and gate need block_out")
-    else:
-        a.block_row = _matrix(block_out, "block_out", (_BF16,), dev, M, H)
-        a.block_out = block_out.data_ptr()
-        if post_weight is not None:
-            a.w_post = post_weight.data_ptr()
-        if gate is not None:
-            _gate(a, gate, dev, M, H)
-    if pre_weight is None and (quantize or block_out is None):
+    dtype, device = residual.dtype, residual.device
+    b = b_row = w_post = w_pre = g = g_row = g_col = ro = ro_row = n = q_ptr = s_ptr = s_block = 0
+    w_f32 = g_f32 = 0
+    if pre_weight is not None:
+        _vector(pre_weight, "pre_weight", _IS_FLOAT, dev, H)
+        w_pre, w_f32 = pre_weight.data_ptr(), 1 if pre_weight.dtype is _F32 else 0
+    elif quantize or block_out is None:
         raise ValueError("without pre_weight there is nothing to " + ("quantize" if quantize else "compute"))
+    if block_out is not None:
+        b, b_row = block_out.data_ptr(), _matrix(block_out, "block_out", _IS_BF16, dev, M, H)
+        if post_weight is not None:
+            _vector(post_weight, "post_weight", _IS_FLOAT if pre_weight is None else (pre_weight.dtype,), dev, H)
+            w_post, w_f32 = post_weight.data_ptr(), 1 if post_weight.dtype is _F32 else 0
+        if gate is not None:
+            g_row, g_col = _gate(gate, dev, M, H)
+            g, g_f32 = gate.data_ptr(), 1 if gate.dtype is _F32 else 0
+    elif post_weight is not None or gate is not None:
+        raise ValueError("post_weight and gate need block_out")
+    if residual_out is not None:
+        ro_row = _matrix(residual_out, "residual_out", (dtype,), dev, M, H)
+        ro = residual_out.data_ptr()
+    elif block_out is not None:
+        residual_out = _empty((M, H), dtype=dtype, device=device)
+        ro, ro_row = residual_out.data_ptr(), H
+    else:
+        residual_out = residual
     normed = q = s = None
-    with go:
-        if residual_out is not None:
-            a.residual_out_row = _matrix(residual_out, "residual_out", (residual.dtype,), dev, M, H)
-            a.residual_out = residual_out.data_ptr()
-        elif block_out is not None:
-            residual_out = torch.empty((M, H), dtype=residual.dtype, device=dev)
-            a.residual_out_row = H
-            a.residual_out = residual_out.data_ptr()
-        else:
-            residual_out = residual
-        if pre_weight is not None:
-            a.w_pre = pre_weight.data_ptr()
-            normed = torch.empty((M, H), dtype=_BF16, device=dev)
-            a.normed, a.normed_row = normed.data_ptr(), H
-        if quantize:
-            q = torch.empty((M, H), dtype=FP8, device=dev)
-            s = torch.empty((_blocks(H), M), dtype=_F32, device=dev)
-            a.q, a.q_row, a.s, a.s_row, a.s_block = q.data_ptr(), H, s.data_ptr(), 1, M
-    _capi.moe_fp4_block_norm(a, go.stream)
-    return (residual_out, normed, q, s.t()) if quantize else (residual_out, normed)
+    if pre_weight is not None:
+        normed = _empty((M, H), dtype=_BF16, device=device)
+        n = normed.data_ptr()
+    if quantize:
+        q = _empty((M, H), dtype=FP8, device=device)
+        s = torch.empty_strided((M, (H + 127) // 128), (1, M), dtype=_F32, device=device)
+        q_ptr, s_ptr, s_block = q.data_ptr(), s.data_ptr(), M
+    _capi.moe_fp4_block_norm(
+        _PACK_NORM(residual.data_ptr(), row, b, b_row, w_post, w_pre, g, g_row, g_col, ro, ro_row, n, H, q_ptr, H,
+                   s_ptr, 1, s_block, scale, eps, weight_offset, 1 if dtype is _F32 else 0, w_f32, g_f32, M, H),
+        _raw_stream(dev))
+    return (residual_out, normed, q, s) if quantize else (residual_out, normed)
 
 
-def _gate(a, gate, dev, M, H):
-    if gate.dtype not in (_BF16, _F32):
+def _gate(gate, dev, M, H):
+    """(row, column) strides of a gate."""
+    if gate.dtype not in _IS_FLOAT:
         raise TypeError(f"gate must be bfloat16 or float32, not {gate.dtype}")
-    if gate.device != dev:
-        raise ValueError(f"gate is on {gate.device}, not {dev}")
+    if gate.get_device() != dev:
+        raise ValueError(f"gate is on {gate.device}, not cuda:{dev}")
     if gate.shape == (H,):
-        a.gate_row, a.gate_col = 0, gate.stride(0)
+        row, col = 0, gate.stride(0)
     elif gate.shape == (M, H):
-        a.gate_row, a.gate_col = gate.stride()
+        row, col = gate.stride()
     elif gate.shape == (M, 1):
-        a.gate_row, a.gate_col = gate.stride(0), 0
+        row, col = gate.stride(0), 0
     else:
         raise ValueError(f"gate must be [{H}], [{M}, 1] or [{M}, {H}], not {list(gate.shape)}")
-    if a.gate_col not in (0, 1):
-        raise ValueError("gate must have contiguous columns")
-    a.gate, a.gate_f32 = gate.data_ptr(), 1 if gate.dtype is _F32 else 0
+    if col != 0 and col != 1:
+        if H != 1:
+            raise ValueError("gate must have contiguous columns")
+        col = 1
+    return row, col
 
 
 # ----------------------------------------------------------------------- router
@@ -286,17 +299,21 @@ def route_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bia
     of -inf or NaN are never chosen, and a row that runs out of experts ends
     in id -1 with weight 0.  ``renormalize`` divides by the chosen weights'
     sum; ``scale`` multiplies the weights."""
-    go = _Launch(logits, stream)
-    row = _matrix(logits, "logits", (_F32, _BF16), go.device)
+    if stream is not None:
+        with _on(stream, logits):
+            return route_topk(logits, top_k, score, bias, renormalize, scale)
+    dev = _device(logits)
+    row = _matrix(logits, "logits", _IS_FLOAT, dev)
     M, E = logits.shape
+    b = 0
     if bias is not None:
-        _vector(bias, "bias", (_F32,), go.device, E)
+        _vector(bias, "bias", _IS_F32, dev, E)
+        b = bias.data_ptr()
     if top_k < 1:
         raise ValueError("top_k must be at least 1")
-    with go:
-        ids = torch.empty((M, top_k), dtype=torch.int32, device=go.device)
-        weights = torch.empty((M, top_k), dtype=_F32, device=go.device)
-    _capi.moe_fp4_route_topk(logits.data_ptr(), row, 1 if logits.dtype is _F32 else 0,
-                             None if bias is None else bias.data_ptr(), score, 1 if renormalize else 0, scale,
-                             ids.data_ptr(), weights.data_ptr(), M, E, top_k, go.stream)
+    ids = _empty((M, top_k), dtype=torch.int32, device=logits.device)
+    weights = _empty((M, top_k), dtype=_F32, device=logits.device)
+    _capi.moe_fp4_route_topk(logits.data_ptr(), row, 1 if logits.dtype is _F32 else 0, b, score,
+                             1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), M, E, top_k,
+                             _raw_stream(dev))
     return ids, weights

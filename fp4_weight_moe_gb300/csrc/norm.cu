@@ -8,67 +8,117 @@
 // once; two block sums (of b^2, then of r'^2) are all that separates them.
 // Sums, r' and the norms are FP32; r' enters the second norm before it is
 // rounded to the residual stream's type.
-#include <cstdlib>
 #include "block.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"
 
 namespace moe_fp4 {
 
-// Eight consecutive values from p + k (kVec: 16-byte aligned and k + 8 <= H),
-// zeros past H.
+// A thread's eight columns of chunk i.  kVec (rows 16-byte aligned, H % 8 ==
+// 0): eight consecutive ones from 8 (threadIdx.x + i blockDim.x).  Otherwise
+// columns threadIdx.x + (8 i + j) blockDim.x, so that a warp's scalar
+// accesses are consecutive.  Columns past H read as zeros and are not stored.
 template <bool kVec>
-__device__ __forceinline__ void load8(const void* p, int f32, int64_t base, int k, int H, float (&v)[8]) {
-  if (kVec) {
-    if (f32) {
-      const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base + k);
-      const float4 a = q[0], b = q[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + base + k);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ int column(int i, int j) {
+  return kVec ? 8 * (threadIdx.x + i * blockDim.x) + j : (int)(threadIdx.x + (8 * i + j) * blockDim.x);
+}
+
+// Eight bf16 (kF32: f32) values of a row as loaded, packed.
+template <bool kF32>
+struct Raw8 {
+  uint32_t w[kF32 ? 8 : 4];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0;
+  }
+  // kStream: read once, not worth a line of L1.
+  template <bool kVec, bool kStream>
+  __device__ __forceinline__ void load(const void* row, int i, int H) {
+    if (kVec) {
+      const int k = column<true>(i, 0);
+      if (k >= H) return;
+      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)k * (kF32 ? 4 : 2));
+#pragma unroll
+      for (int c = 0; c < (kF32 ? 2 : 1); ++c) {
+        uint4 u;
+        if (kStream)
+          asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                       : "l"(q + c)
+                       : "memory");
+        else
+          u = q[c];
+        w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = column<false>(i, j);
+        uint32_t u = 0;
+        if (k < H) u = kF32 ? static_cast<const uint32_t*>(row)[k] : (uint32_t) static_cast<const uint16_t*>(row)[k];
+        if (kF32)
+          w[j] = u;
+        else if (j % 2 == 0)
+          w[j / 2] = u;
+        else
+          w[j / 2] |= u << 16;
       }
     }
-  } else {
+  }
+  __device__ __forceinline__ float2 pair(int p) const {
+    return kF32 ? make_float2(__uint_as_float(w[2 * p]), __uint_as_float(w[2 * p + 1]))
+                : make_float2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u));
+  }
+};
+
+// The chunk's values of a vector or row of either type.
+template <bool kVec>
+__device__ __forceinline__ void load_pairs(const void* row, int f32, int i, int H, float2 (&v)[4]) {
+  if (f32) {
+    Raw8<true> r;
+    r.zero();
+    r.template load<kVec, false>(row, i, H);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = 0.f;
-      if (k + i < H)
-        v[i] = f32 ? static_cast<const float*>(p)[base + k + i]
-                   : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[base + k + i] << 16);
-    }
+    for (int p = 0; p < 4; ++p) v[p] = r.pair(p);
+  } else {
+    Raw8<false> r;
+    r.zero();
+    r.template load<kVec, false>(row, i, H);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v[p] = r.pair(p);
   }
 }
 
-__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t bf16x2_bits(float2 v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kVec>
-__device__ __forceinline__ void store8(void* p, int f32, int64_t base, int k, int H, const float (&v)[8]) {
+template <bool kVec, bool kF32>
+__device__ __forceinline__ void store_pairs(void* row, int i, int H, const float2 (&v)[4]) {
   if (kVec) {
-    if (f32) {
-      float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + base + k);
-      q[0] = make_float4(v[0], v[1], v[2], v[3]);
-      q[1] = make_float4(v[4], v[5], v[6], v[7]);
+    const int k = column<true>(i, 0);
+    if (k >= H) return;
+    if (kF32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(row) + k);
+      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
     } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + base + k) = make_uint4(
-          bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + k) =
+          make_uint4(bf16x2_bits(v[0]), bf16x2_bits(v[1]), bf16x2_bits(v[2]), bf16x2_bits(v[3]));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (k + i < H) {
-        if (f32)
-          static_cast<float*>(p)[base + k + i] = v[i];
+    for (int j = 0; j < 8; ++j) {
+      const int k = column<false>(i, j);
+      const float x = j % 2 ? v[j / 2].y : v[j / 2].x;
+      if (k < H) {
+        if (kF32)
+          static_cast<float*>(row)[k] = x;
         else
-          static_cast<__nv_bfloat16*>(p)[base + k + i] = __float2bfloat16_rn(v[i]);
+          static_cast<__nv_bfloat16*>(row)[k] = __float2bfloat16_rn(x);
       }
+    }
   }
 }
 
@@ -86,140 +136,108 @@ __device__ __forceinline__ float block_sum(float v, float* part) {
   return v;
 }
 
-// Eight residual values as loaded: packed (bf16) or not (f32).
-template <bool kF32>
-struct Raw8 {
-  uint32_t w[kF32 ? 8 : 4];
-  template <bool kVec>
-  __device__ __forceinline__ void load(const void* p, int64_t base, int k, int H) {
-    if (kVec) {
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + (base + k) * (kF32 ? 4 : 2));
-#pragma unroll
-      for (int i = 0; i < (kF32 ? 2 : 1); ++i) {
-        uint4 u;
-        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "l"(q + i)
-                     : "memory");
-        w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-      }
-    } else {
-      float v[8];
-      load8<false>(p, kF32, base, k, H, v);
-#pragma unroll
-      for (int i = 0; i < (kF32 ? 8 : 4); ++i)
-        w[i] = kF32 ? __float_as_uint(v[i])
-                    : (__float_as_uint(v[2 * i]) >> 16) | (__float_as_uint(v[2 * i + 1]) & 0xffff0000u);
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0;
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = kF32 ? __uint_as_float(w[i])
-                  : __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
-  }
-};
+// Value `m` of a gate or the like, of either type.
+__device__ __forceinline__ float scalar_of(const void* p, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i]
+             : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
+}
 
-// kCh chunks of eight columns per thread: chunk c = threadIdx.x + i *
-// blockDim.x covers columns 8c .. 8c + 7.  All of a row's loads are under way
-// before the first sum.
+// A CTA per row, kCh chunks of eight columns per thread; all of a row's loads
+// are under way before the first sum.
 template <int kCh, int kMaxThreads, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][32];
   const int64_t m = blockIdx.x;
-  const float inv_h = 1.0f / (float)a.H;
+  const int H = a.H;
+  const float inv_h = 1.0f / (float)H;
   Raw8<kF32> raw[kCh];
   Raw8<false> rawb[kCh];
+  const uint16_t* b = a.b ? a.b + m * a.b_row : nullptr;
+  const void* r = static_cast<const char*>(a.r) + m * a.r_row * (kF32 ? 4 : 2);
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
-    const int k = 8 * (threadIdx.x + i * blockDim.x);
     raw[i].zero();
     rawb[i].zero();
-    if (k < a.H) {
-      if (a.b) rawb[i].template load<kVec>(a.b, m * a.b_row, k, a.H);
-      raw[i].template load<kVec>(a.r, m * a.r_row, k, a.H);
-    }
+    if (b) rawb[i].template load<kVec, true>(b, i, H);
+    raw[i].template load<kVec, true>(r, i, H);
   }
-  float v[kCh][8];  // r'
-  if (a.b) {
-    float inv = 1.f;
+  float2 v[kCh][4];  // r'
+  if (b) {
+    float factor = a.scale;  // what the row's values of z share
     if (a.w_post) {
-      float sum = 0.f;
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kCh; ++i) {
-        float z[8];
-        rawb[i].get(z);
+      for (int i = 0; i < kCh; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum += z[j] * z[j];
-      }
-      inv = rsqrtf(block_sum(sum, part[0]) * inv_h + a.eps);
+        for (int p = 0; p < 4; ++p) {
+          const float2 z = rawb[i].pair(p);
+          sum = ffma2(z, z, sum);
+        }
+      factor *= rsqrtf(block_sum(sum.x + sum.y, part[0]) * inv_h + a.eps);
     }
-    float token_gate = 1.f;
-    if (a.gate && a.g_col == 0)
-      token_gate = a.g_f32 ? static_cast<const float*>(a.gate)[m * a.g_row]
-                           : __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.gate)[m * a.g_row] << 16);
+    if (a.gate && a.g_col == 0) factor *= scalar_of(a.gate, a.g_f32, m * a.g_row);
+    const float2 f = make_float2(factor, factor);
+    const float2 of = make_float2(a.offset * factor, a.offset * factor);
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
-      const int k = 8 * (threadIdx.x + i * blockDim.x);
-      float z[8];
-      rawb[i].get(z);
-      raw[i].get(v[i]);
-      if (k < a.H) {
-        if (a.w_post) {
-          float w[8];
-          load8<kVec>(a.w_post, a.w_f32, 0, k, a.H, w);
+      float2 t[4];  // factor * (offset + w_post) * gate
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] = z[j] * inv * (a.offset + w[j]);
-        }
-        if (a.gate && a.g_col) {
-          float g[8];
-          load8<kVec>(a.gate, a.g_f32, m * a.g_row, k, a.H, g);
+      for (int p = 0; p < 4; ++p) t[p] = f;
+      if (a.w_post) {
+        float2 w[4];
+        load_pairs<kVec>(a.w_post, a.w_f32, i, H, w);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] *= g[j];
-        } else {
+        for (int p = 0; p < 4; ++p) t[p] = ffma2(w[p], f, of);
+      }
+      if (a.gate && a.g_col) {
+        float2 g[4];
+        load_pairs<kVec>(static_cast<const char*>(a.gate) + m * a.g_row * (a.g_f32 ? 4 : 2), a.g_f32, i, H, g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] *= token_gate;
-        }
+        for (int p = 0; p < 4; ++p) t[p] = fmul2(t[p], g[p]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] += a.scale * z[j];
+      for (int p = 0; p < 4; ++p) v[i][p] = ffma2(rawb[i].pair(p), t[p], raw[i].pair(p));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) raw[i].get(v[i]);
+    for (int i = 0; i < kCh; ++i)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) v[i][p] = raw[i].pair(p);
   }
-  float sum = 0.f;
+  if (a.r_out) {
+    void* row = static_cast<char*>(a.r_out) + m * a.ro_row * (kF32 ? 4 : 2);
 #pragma unroll
-  for (int i = 0; i < kCh; ++i) {
-    const int k = 8 * (threadIdx.x + i * blockDim.x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += k + j < a.H ? v[i][j] * v[i][j] : 0.f;
-    if (a.r_out && k < a.H) store8<kVec>(a.r_out, kF32, m * a.ro_row, k, a.H, v[i]);
+    for (int i = 0; i < kCh; ++i) store_pairs<kVec, kF32>(row, i, H, v[i]);
   }
   if (!a.w_pre) return;
-  const float inv = rsqrtf(block_sum(sum, part[1]) * inv_h + a.eps);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < kCh; ++i)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) sum = ffma2(v[i][p], v[i][p], sum);  // (columns past H are zeros)
+  const float inv = rsqrtf(block_sum(sum.x + sum.y, part[1]) * inv_h + a.eps);
+  const float2 f = make_float2(inv, inv), of = make_float2(a.offset * inv, a.offset * inv);
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
-    const int k = 8 * (threadIdx.x + i * blockDim.x);
-    if (k < a.H) {
-      float w[8];
-      load8<kVec>(a.w_pre, a.w_f32, 0, k, a.H, w);
+    float2 w[4];
+    load_pairs<kVec>(a.w_pre, a.w_f32, i, H, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * inv * (a.offset + w[j]);
-      if (a.n) store8<kVec>(a.n, 0, m * a.n_row, k, a.H, v[i]);
-    }
-    if (a.q) {
+    for (int p = 0; p < 4; ++p) v[i][p] = fmul2(v[i][p], ffma2(w[p], f, of));
+    if (a.n) store_pairs<kVec, false>(a.n + m * a.n_row, i, H, v[i]);
+    if (kVec && a.q) {
       // the BF16 values' FP8 form, so that it is the one a quantiser of n
       // gives; 16 lanes hold a block of 128 columns
+      const int k = column<true>(i, 0);
+      float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = k + j < a.H ? __bfloat162float(__float2bfloat16_rn(v[i][j])) : 0.f;
-      const float sc = block_scale(block_amax(v[i]));
-      if (k < a.H) {
-        *reinterpret_cast<uint2*>(a.q + m * a.q_row + k) = e4m3_quotients(v[i], sc);
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t u = bf16x2_bits(v[i][p]);
+        x[2 * p] = __uint_as_float(u << 16);
+        x[2 * p + 1] = __uint_as_float(u & 0xffff0000u);
+      }
+      const float sc = block_scale(block_amax(x));
+      if (k < H) {
+        *reinterpret_cast<uint2*>(a.q + m * a.q_row + k) = e4m3_quotients(x, sc);
         if ((threadIdx.x & 15) == 0) a.s[m * a.s_row + (int64_t)(k / 128) * a.s_blk] = sc;
       }
     }
@@ -247,13 +265,16 @@ cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStre
   if (e != cudaSuccess) return e;
   if (a.H > 16384) return launch_ch<4, 1024>(a, res_f32, vec, st);
   if (a.H > 8192) return launch_ch<4, 512>(a, res_f32, vec, st);
-  if (getenv("NCH")) {
-    int c = atoi(getenv("NCH"));
-    if (c == 1) return launch_ch<1, 1024>(a, res_f32, vec, st);
-    if (c == 2) return launch_ch<2, 512>(a, res_f32, vec, st);
-    return launch_ch<4, 256>(a, res_f32, vec, st);
-  }
-  if (a.M <= sms) return launch_ch<1, 1024>(a, res_f32, vec, st);
+  // Chunks per thread: one while a row per CTA leaves SMs with one or two
+  // rows (latency) and where a row is short or read by scalar loads; beyond,
+  // as many as keep a CTA at 256 threads, so that more rows share an SM and
+  // their waits for the two sums overlap.  Measured with 1 / 2 / 4 chunks
+  // (us, bf16 residual, no norm after the block): H=7168 M=64 2.5 / - / 3.3,
+  // M=16384 151 / - / 138; H=4096 M=64 2.3 / 2.6 / 3.3, M=16384 81.4 / 80.0 /
+  // 80.7; f32 residual with that norm, M=16384: H=7168 365 / - / 221, H=4096
+  // 133 / 126 / 129, H=2560 85 / 77 / 81.
+  if (!vec || a.H <= 2048 || a.M <= 2 * sms) return launch_ch<1, 1024>(a, res_f32, vec, st);
+  if (a.H <= 4096) return launch_ch<2, 256>(a, res_f32, vec, st);
   return launch_ch<4, 256>(a, res_f32, vec, st);
 }
 

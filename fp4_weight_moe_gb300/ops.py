@@ -13,6 +13,8 @@ shapes, allocate outputs, and launch on the current stream (or ``stream``).
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -51,36 +53,52 @@ def _device(t: torch.Tensor) -> int:
     return i
 
 
-def _matrix(t: torch.Tensor, name: str, dtypes, dev: int, rows: Optional[int] = None, cols: Optional[int] = None):
-    """Check a [rows, cols] tensor with contiguous columns; returns its row
-    stride."""
-    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 2:
-        r, c = t.shape
-        if (rows is None or r == rows) and (cols is None or c == cols):
-            row, col = t.stride()
-            if col == 1 or c <= 1:
-                return row if r != 1 else c  # (one row has no stride of its own)
-            raise ValueError(f"{name} must have contiguous columns")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
+    """Check a [rows, cols] tensor of one type with contiguous columns;
+    returns its row stride."""
+    if t.dtype is dtype and t.shape == (rows, cols) and t.get_device() == dev and t.is_contiguous():
+        return cols
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
-    raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}], "
-                     f"not {list(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], not {list(t.shape)}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return t.stride(0) if rows != 1 else cols  # (one row has no stride of its own)
 
 
-def _vector(t: torch.Tensor, name: str, dtypes, dev: int, n: int):
-    if t.dtype in dtypes and t.get_device() == dev and t.dim() == 1 and t.shape[0] == n and \
-            (n <= 1 or t.stride(0) == 1):
+def _sizes(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, not {list(t.shape)}")
+    return t.shape
+
+
+def _float_type(t: torch.Tensor, name: str):
+    dtype = t.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"{name} must be {_BF16} or {_F32}, not {dtype}")
+    return dtype
+
+
+def _vector(t: torch.Tensor, name: str, dtype, dev: int, n: int):
+    if t.dtype is dtype and t.shape == (n,) and t.get_device() == dev and t.is_contiguous():
         return
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not cuda:{dev}")
     raise ValueError(f"{name} must be a contiguous vector of {n} values, not {list(t.shape)}")
 
 
-_IS_BF16, _IS_F32, _IS_FP8, _IS_FLOAT = (_BF16,), (_F32,), (FP8,), (_BF16, _F32)
+def _fail(fn: str, status: int):
+    raise _capi.MoeFp4Error(fn, status)
+
+
+@functools.lru_cache(maxsize=64)
+def _activation(kind: int, alpha: float, beta: float, limit: float):
+    return ctypes.byref(_capi.MoeFp4Activation(kind, alpha, beta, limit))
 
 
 def _blocks(n: int) -> int:
@@ -99,38 +117,38 @@ def fp8_quantize(x: torch.Tensor, act: Optional[int] = None, alpha: float = 0.0,
         with _on(stream, x):
             return fp8_quantize(x, act, alpha, beta, limit)
     dev = _device(x)
-    row = _matrix(x, "x", _IS_BF16, dev)
-    M, K = x.shape
+    M, K = _sizes(x, "x")
+    row = _matrix(x, "x", _BF16, dev, M, K)
     if act is not None:
         if K % 2:
             raise ValueError("a gated x has an even number of columns")
         K //= 2
-        act = _capi.MoeFp4Activation(act, alpha, beta, limit)
+        act = _activation(act, alpha, beta, limit)
     q = _empty((M, K), dtype=FP8, device=x.device)
-    s = torch.empty_strided((M, _blocks(K)), (1, M), dtype=_F32, device=x.device)
-    _capi.moe_fp4_fp8_quantize(x.data_ptr(), row, act, q.data_ptr(), K, s.data_ptr(), 1, M, M, K, _raw_stream(dev))
+    s = torch.empty_strided((M, (K + 127) // 128), (1, M), dtype=_F32, device=x.device)
+    st = _capi.lib().moe_fp4_fp8_quantize(x.data_ptr(), row, act, q.data_ptr(), K, s.data_ptr(), 1, M, M, K,
+                                          _raw_stream(dev))
+    if st:
+        _fail("moe_fp4_fp8_quantize", st)
     return q, s
 
 
-def _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K):
-    w_row = _matrix(w, "w", _IS_FP8, dev, None, K)
-    N = w.shape[0]
-    ws_row = _matrix(w_scale, "w_scale", _IS_F32, dev, (N + 127) // 128, (K + 127) // 128)
+def _product_output(addend, out, out_dtype, dev, device, M, N):
+    """(addend pointer, its row stride, out, its row stride, whether float32)."""
     add = add_row = 0
     if addend is not None:
-        add, add_row = addend.data_ptr(), _matrix(addend, "addend", _IS_BF16, dev, M, N)
+        add_row = _matrix(addend, "addend", _BF16, dev, M, N)
+        add = addend.data_ptr()
     if out is None:
         out_dtype = out_dtype or _BF16
-        if out_dtype not in _IS_FLOAT:
-            raise TypeError(f"out must be bfloat16 or float32, not {out_dtype}")
-        out, out_row = _empty((M, N), dtype=out_dtype, device=w.device), N
+        if out_dtype is not _BF16 and out_dtype is not _F32:
+            raise TypeError(f"out must be {_BF16} or {_F32}, not {out_dtype}")
+        out, out_row = _empty((M, N), dtype=out_dtype, device=device), N
     else:
-        out_row = _matrix(out, "out", _IS_FLOAT if out_dtype is None else (out_dtype,), dev, M, N)
-        out_dtype = out.dtype
-        if out_dtype not in _IS_FLOAT:
-            raise TypeError(f"out must be bfloat16 or float32, not {out_dtype}")
-    return (w.data_ptr(), w_row, w_scale.data_ptr(), ws_row, add, add_row, out.data_ptr(), out_row,
-            1 if out_dtype is _F32 else 0, M, N, K), out
+        out_dtype = out_dtype or _float_type(out, "out")
+        out_row = _matrix(out, "out", out_dtype, dev, M, N)
+        _float_type(out, "out")
+    return add, add_row, out, out_row, 1 if out_dtype is _F32 else 0
 
 
 def fp8_matmul(x_q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -144,16 +162,24 @@ def fp8_matmul(x_q: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scal
         with _on(stream, x_q):
             return fp8_matmul(x_q, x_scale, w, w_scale, out, addend, out_dtype)
     dev = _device(x_q)
-    row = _matrix(x_q, "x_q", _IS_FP8, dev)
-    M, K = x_q.shape
+    M, K = _sizes(x_q, "x_q")
+    N = _sizes(w, "w")[0]
+    row = _matrix(x_q, "x_q", FP8, dev, M, K)
+    w_row = _matrix(w, "w", FP8, dev, N, K)
+    ws_row = _matrix(w_scale, "w_scale", _F32, dev, (N + 127) // 128, (K + 127) // 128)
     if x_scale.dtype is not _F32:
         raise TypeError(f"x_scale must be float32, not {x_scale.dtype}")
     if x_scale.shape != (M, (K + 127) // 128):
         raise ValueError(f"x_scale must be [{M}, {_blocks(K)}], not {list(x_scale.shape)}")
     if x_scale.get_device() != dev:
         raise ValueError(f"x_scale is on {x_scale.device}, not cuda:{dev}")
-    args, out = _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K)
-    _capi.moe_fp4_fp8_matmul(x_q.data_ptr(), row, x_scale.data_ptr(), *x_scale.stride(), *args, _raw_stream(dev))
+    xs_row, xs_block = x_scale.stride()
+    add, add_row, out, out_row, f32 = _product_output(addend, out, out_dtype, dev, w.device, M, N)
+    st = _capi.lib().moe_fp4_fp8_matmul(x_q.data_ptr(), row, x_scale.data_ptr(), xs_row, xs_block, w.data_ptr(),
+                                        w_row, w_scale.data_ptr(), ws_row, add, add_row, out.data_ptr(), out_row, f32,
+                                        M, N, K, _raw_stream(dev))
+    if st:
+        _fail("moe_fp4_fp8_matmul", st)
     return out
 
 
@@ -176,9 +202,12 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
         with _on(stream, x):
             return fp8_linear(x, w, w_scale, out, addend, out_dtype, workspace)
     dev = _device(x)
-    row = _matrix(x, "x", _IS_BF16, dev)
-    M, K = x.shape
-    args, out = _product_operands(w, w_scale, addend, out, out_dtype, dev, M, K)
+    M, K = _sizes(x, "x")
+    N = _sizes(w, "w")[0]
+    row = _matrix(x, "x", _BF16, dev, M, K)
+    w_row = _matrix(w, "w", FP8, dev, N, K)
+    ws_row = _matrix(w_scale, "w_scale", _F32, dev, (N + 127) // 128, (K + 127) // 128)
+    add, add_row, out, out_row, f32 = _product_output(addend, out, out_dtype, dev, w.device, M, N)
     ws_ptr = ws_bytes = 0
     if workspace is None:
         if M > 16 or K > 16384:
@@ -187,7 +216,11 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
         raise ValueError("the workspace must be a contiguous tensor on x's device")
     if workspace is not None:
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    _capi.moe_fp4_fp8_linear(x.data_ptr(), row, *args, ws_ptr, ws_bytes, _raw_stream(dev))
+    st = _capi.lib().moe_fp4_fp8_linear(x.data_ptr(), row, w.data_ptr(), w_row, w_scale.data_ptr(), ws_row, add,
+                                        add_row, out.data_ptr(), out_row, f32, M, N, K, ws_ptr, ws_bytes,
+                                        _raw_stream(dev))
+    if st:
+        _fail("moe_fp4_fp8_linear", st)
     return out
 
 
@@ -224,28 +257,33 @@ def block_norm(residual: torch.Tensor, pre_weight: Optional[torch.Tensor] = None
             return block_norm(residual, pre_weight, block_out, post_weight, gate, scale, eps, weight_offset,
                               residual_out, quantize)
     dev = _device(residual)
-    row = _matrix(residual, "residual", _IS_FLOAT, dev)
-    M, H = residual.shape
-    dtype, device = residual.dtype, residual.device
+    M, H = _sizes(residual, "residual")
+    dtype, device = _float_type(residual, "residual"), residual.device
+    row = _matrix(residual, "residual", dtype, dev, M, H)
     b = b_row = w_post = w_pre = g = g_row = g_col = ro = ro_row = n = q_ptr = s_ptr = s_block = 0
     w_f32 = g_f32 = 0
     if pre_weight is not None:
-        _vector(pre_weight, "pre_weight", _IS_FLOAT, dev, H)
-        w_pre, w_f32 = pre_weight.data_ptr(), 1 if pre_weight.dtype is _F32 else 0
+        w_dtype = _float_type(pre_weight, "pre_weight")
+        _vector(pre_weight, "pre_weight", w_dtype, dev, H)
+        w_pre, w_f32 = pre_weight.data_ptr(), 1 if w_dtype is _F32 else 0
     elif quantize or block_out is None:
         raise ValueError("without pre_weight there is nothing to " + ("quantize" if quantize else "compute"))
     if block_out is not None:
-        b, b_row = block_out.data_ptr(), _matrix(block_out, "block_out", _IS_BF16, dev, M, H)
+        b_row = _matrix(block_out, "block_out", _BF16, dev, M, H)
+        b = block_out.data_ptr()
         if post_weight is not None:
-            _vector(post_weight, "post_weight", _IS_FLOAT if pre_weight is None else (pre_weight.dtype,), dev, H)
-            w_post, w_f32 = post_weight.data_ptr(), 1 if post_weight.dtype is _F32 else 0
+            if pre_weight is None:
+                w_dtype = _float_type(post_weight, "post_weight")
+                w_f32 = 1 if w_dtype is _F32 else 0
+            _vector(post_weight, "post_weight", w_dtype, dev, H)
+            w_post = post_weight.data_ptr()
         if gate is not None:
             g_row, g_col = _gate(gate, dev, M, H)
             g, g_f32 = gate.data_ptr(), 1 if gate.dtype is _F32 else 0
     elif post_weight is not None or gate is not None:
         raise ValueError("post_weight and gate need block_out")
     if residual_out is not None:
-        ro_row = _matrix(residual_out, "residual_out", (dtype,), dev, M, H)
+        ro_row = _matrix(residual_out, "residual_out", dtype, dev, M, H)
         ro = residual_out.data_ptr()
     elif block_out is not None:
         residual_out = _empty((M, H), dtype=dtype, device=device)
@@ -260,17 +298,18 @@ def block_norm(residual: torch.Tensor, pre_weight: Optional[torch.Tensor] = None
         q = _empty((M, H), dtype=FP8, device=device)
         s = torch.empty_strided((M, (H + 127) // 128), (1, M), dtype=_F32, device=device)
         q_ptr, s_ptr, s_block = q.data_ptr(), s.data_ptr(), M
-    _capi.moe_fp4_block_norm(
+    st = _capi.lib().moe_fp4_block_norm(
         _PACK_NORM(residual.data_ptr(), row, b, b_row, w_post, w_pre, g, g_row, g_col, ro, ro_row, n, H, q_ptr, H,
                    s_ptr, 1, s_block, scale, eps, weight_offset, 1 if dtype is _F32 else 0, w_f32, g_f32, M, H),
         _raw_stream(dev))
+    if st:
+        _fail("moe_fp4_block_norm", st)
     return (residual_out, normed, q, s) if quantize else (residual_out, normed)
 
 
 def _gate(gate, dev, M, H):
     """(row, column) strides of a gate."""
-    if gate.dtype not in _IS_FLOAT:
-        raise TypeError(f"gate must be bfloat16 or float32, not {gate.dtype}")
+    _float_type(gate, "gate")
     if gate.get_device() != dev:
         raise ValueError(f"gate is on {gate.device}, not cuda:{dev}")
     if gate.shape == (H,):
@@ -303,17 +342,20 @@ def route_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bia
         with _on(stream, logits):
             return route_topk(logits, top_k, score, bias, renormalize, scale)
     dev = _device(logits)
-    row = _matrix(logits, "logits", _IS_FLOAT, dev)
-    M, E = logits.shape
+    M, E = _sizes(logits, "logits")
+    dtype = _float_type(logits, "logits")
+    row = _matrix(logits, "logits", dtype, dev, M, E)
     b = 0
     if bias is not None:
-        _vector(bias, "bias", _IS_F32, dev, E)
+        _vector(bias, "bias", _F32, dev, E)
         b = bias.data_ptr()
     if top_k < 1:
         raise ValueError("top_k must be at least 1")
     ids = _empty((M, top_k), dtype=torch.int32, device=logits.device)
     weights = _empty((M, top_k), dtype=_F32, device=logits.device)
-    _capi.moe_fp4_route_topk(logits.data_ptr(), row, 1 if logits.dtype is _F32 else 0, b, score,
-                             1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), M, E, top_k,
-                             _raw_stream(dev))
+    st = _capi.lib().moe_fp4_route_topk(logits.data_ptr(), row, 1 if dtype is _F32 else 0, b, score,
+                                        1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), M, E,
+                                        top_k, _raw_stream(dev))
+    if st:
+        _fail("moe_fp4_route_topk", st)
     return ids, weights

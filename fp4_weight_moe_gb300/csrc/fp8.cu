@@ -103,11 +103,12 @@ __global__ void __launch_bounds__(F8Cfg<BN, kSwap, kTwo>::kThreads, kTwo ? 2 : 1
   gemm_fp8_persistent<BN, kSwap, kTwo, true>(&map_a, &map_b, a, split);
 }
 
-// The same for at most 16 BF16 tokens (a.xb), quantised by the kernel.
-__global__ void __launch_bounds__(F8Cfg<16, true, true, true>::kThreads, 2)
+// The same for at most eight BF16 tokens (a.xb), quantised by the kernel.
+template <int kXq>
+__global__ void __launch_bounds__(F8Cfg<16, true, true, kXq>::kThreads, 2)
     fp8_linear_kernel(const __grid_constant__ CUtensorMap map_w, Fp8Args a, int split) {
   a.err = &g_fp8_status;
-  gemm_fp8_persistent<16, true, true, true, true>(&map_w, &map_w, a, split);
+  gemm_fp8_persistent<16, true, true, true, kXq>(&map_w, &map_w, a, split);
 }
 
 // The product kernels' arguments but for the activations.
@@ -202,7 +203,7 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
 // Few tiles: K is split over a cluster until the CTAs fill `slots`, with at
 // least two K blocks each.  Up to 16 tokens a CTA has at most 16 blocks
 // where eight CTAs can manage that: the kernel that quantises its own tokens
-// holds as many (and shares this rule, so that its results are the same).
+// holds as many (it shares this rule, so that its results are the same).
 static int k_split(int64_t tiles, int slots, int nk, int bn) {
   int split = 1;
   while (split < 8 && nk >= 4 * split && (tiles * split * 2 <= slots || (bn == 16 && nk > 16 * split && nk <= 128)))
@@ -210,12 +211,25 @@ static int k_split(int64_t tiles, int slots, int nk, int bn) {
   return split;
 }
 
-// M <= 16 and K <= 16384: one launch, no workspace.
-bool fp8_linear_is_fused(int M, int K) { return M <= 16 && K <= 128 * 128; }
+// The decode band (M <= MOE_FP4_DECODE_MAX_M) with K <= 16384: one launch, no
+// workspace.  On the GPU the two launches, the product's prologue and first
+// weights beside the quantiser, are a little faster (K x N 7168 x 4096, M=1:
+// 8.6 against 9.4 us in a graph, M=8 9.3 against 10.9), but each launch costs
+// the host about 3 us, which is what calls of this size wait for.
+bool fp8_linear_is_fused(int M, int K) { return M <= MOE_FP4_DECODE_MAX_M && K <= 128 * 128; }
+
+template <int kXq>
+static cudaError_t launch_fused(const CUtensorMap& mw, const Fp8Args& a, int64_t tiles, int split, cudaStream_t st) {
+  using Cfg = F8Cfg<16, true, true, kXq>;
+  static bool seen[64];
+  const cudaError_t e = allow_smem(fp8_linear_kernel<kXq>, Cfg::kSmem, seen);
+  if (e != cudaSuccess) return e;
+  return launch_product(fp8_linear_kernel<kXq>, tiles * split, Cfg::kThreads, Cfg::kSmem, split, false, st, mw, a,
+                        split);
+}
 
 cudaError_t launch_fp8_linear_fused(const void* x, int64_t x_row, const void* w, int64_t w_row, Fp8Product p,
                                     cudaStream_t st) {
-  using Cfg = F8Cfg<16, true, true, true>;
   int sms = 0;
   cudaError_t e = current_device_sms(&sms);
   if (e != cudaSuccess) return e;
@@ -225,12 +239,11 @@ cudaError_t launch_fp8_linear_fused(const void* x, int64_t x_row, const void* w,
   CUtensorMap mw;
   if (encode_u8_map_2d(&mw, w, (uint64_t)a.K, (uint64_t)a.N, (uint64_t)w_row, kF8BM) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  static bool seen[64];
-  e = allow_smem(fp8_linear_kernel, Cfg::kSmem, seen);
-  if (e != cudaSuccess) return e;
   const int64_t tiles = (a.N + 127) / 128;
-  const int split = k_split(tiles, 2 * sms, (a.K + 127) / 128, 16);
-  return launch_product(fp8_linear_kernel, tiles * split, Cfg::kThreads, Cfg::kSmem, split, false, st, mw, a, split);
+  const int nk = (a.K + 127) / 128;
+  int split = k_split(tiles, 2 * sms, nk, 16);
+  if ((nk + split - 1) / split <= 8) return launch_fused<8>(mw, a, tiles, split, st);
+  return launch_fused<16>(mw, a, tiles, split, st);
 }
 
 cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
@@ -264,14 +277,14 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
       default: return launch_split<128, false, false>(o, a, (int)tiles, split, st);
     }
   }
-  // Many tiles: 128 x 256 keeps the tensor cores busier, 128 x 128 leaves
-  // less of the last wave idle; a wave of the former takes about 1.25 times
-  // as long (M=512 4096 x 4096: 20.6 against 16.8 us, one wave each; M=768
-  // 20.8 against 30.6, one and two).
+  // Many tiles: 128 x 256 takes in less per product, 128 x 128 leaves less of
+  // the last wave idle; a wave of the former takes about 1.11 times as long
+  // (M=512 4096 x 4096: 18.0 against 16.2 us, one wave each; M=768: 18.4
+  // against 29.1, one and two).
   const int64_t t256 = (int64_t)((M + 127) / 128) * ((N + 255) / 256);
   const int64_t t128 = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
   const int64_t w256 = (t256 + sms - 1) / sms, w128 = (t128 + sms - 1) / sms;
-  if (5 * w256 <= 4 * w128) return launch_gemm<256, false>(o, a, sms, st);
+  if (10 * w256 <= 9 * w128) return launch_gemm<256, false>(o, a, sms, st);
   return launch_gemm<128, false>(o, a, sms, st);
 }
 

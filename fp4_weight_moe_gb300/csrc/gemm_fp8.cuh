@@ -36,7 +36,7 @@ constexpr int kF8Chunk = 16;   // K blocks of scales per shared-memory chunk
 struct Fp8Args {
   const float* xs;  // activation scales, xs[m * xs_row + b * xs_blk]
   int64_t xs_row, xs_blk;
-  const uint16_t* xb;  // kFuse: the BF16 activations, xb[m * xb_row + k], in place of E4M3 ones and xs
+  const uint16_t* xb;  // kXq: the BF16 activations, xb[m * xb_row + k], in place of E4M3 ones and xs
   int64_t xb_row;
   const float* ws;  // weight scales, ws[(n / 128) * ws_row + b]
   int64_t ws_row;
@@ -50,10 +50,12 @@ struct Fp8Args {
   uint32_t* err;
 };
 
-// kTwo: shared memory and tensor memory for two CTAs per SM.  kFuse: the
-// tokens are quantised by the kernel into kF8Chunk K blocks of their own.
-template <int BN, bool kSwap, bool kTwo = false, bool kFuse = false>
+// kTwo: shared memory and tensor memory for two CTAs per SM.  kXq > 0: the
+// kernel quantises its tokens, into kXq K blocks of their own.
+template <int BN, bool kSwap, bool kTwo = false, int kXq = 0>
 struct F8Cfg {
+  static constexpr bool kFuse = kXq > 0;
+  static_assert(kXq <= kF8Chunk, "the scales of all K blocks lie in one chunk");
   static_assert(!kFuse || kSwap, "the kernel quantises a few tokens only");
   static constexpr int kHalves = BN >= 64 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
@@ -64,7 +66,9 @@ struct F8Cfg {
   // warps take them (setmaxnreg) from a warpgroup that holds warps 0 and 1
   static constexpr bool kMoveRegs = BN >= 256;
   static constexpr int kFirst = kMoveRegs ? 4 : 2;  // first scale warp
-  static constexpr int kThreads = 32 * (kFirst + kScaleWarps);
+  static constexpr int kMmaWarps = kMoveRegs ? 2 : 1;
+  static constexpr int kQuantWarps = kFuse ? 4 : 0;  // they help the scale warps quantise, then leave
+  static constexpr int kThreads = 32 * (kFirst + kScaleWarps + kQuantWarps);
   static constexpr int kAcc = BN >= 256 ? 2 : 4;
   static constexpr uint32_t kTmemCols = kAcc * BN < 32 ? 32 : kAcc * BN;
   static constexpr int kXRows = kSwap ? BN : kF8BM;  // activation rows of a tile
@@ -72,12 +76,15 @@ struct F8Cfg {
   static constexpr int kWBlocks = kWRows / 128 < 1 ? 1 : kWRows / 128;
   static constexpr uint32_t kStageA = kF8BM * kF8BK;
   static constexpr uint32_t kStageB = kFuse ? 0 : BN * kF8BK;
-  static constexpr uint32_t kXqBytes = kFuse ? kF8Chunk * BN * kF8BK : 0;
+  // eight rows per K block (one swizzle group); the MMA's rows 8 .. 15 read
+  // into the block after, and so past the last one
+  static constexpr uint32_t kXqBytes = kXq > 0 ? (kXq + 1) * 1024 : 0;
+  static_assert(kXq == 0 || BN == 16, "at most eight tokens");
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
   static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
   static constexpr uint32_t kBarBytes = 256;
   static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes - kXqBytes;
-  static constexpr int kStages = kBudget / kStageBytes > 6 ? 6 : (int)(kBudget / kStageBytes);
+  static constexpr int kStages = kBudget / kStageBytes > 12 ? 12 : (int)(kBudget / kStageBytes);
   static constexpr uint32_t kSmem = kStages * kStageBytes + kXqBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(kStages >= 3 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
@@ -184,6 +191,26 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// Two FP32 values in one 64-bit register, and acc += a * b on them.
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ float pair_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float pair_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
+// Wait of a converged warp, polling at most `limit` times.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t limit) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < limit; ++i)
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return false;
+}
+
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -288,27 +315,28 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
 // cluster's partials, in rank order, for its share of the tile's tokens and
 // stores them.
 //
-// kFuse (with kSplit; at most kF8Chunk K blocks per CTA): the scale warps
-// first quantise the BF16 tokens of the CTA's K range into shared memory,
+// kXq > 0 (with kSplit; at most kXq K blocks per CTA): the scale warps and
+// four more first quantise the BF16 tokens of the CTA's K range into shared memory,
 // in the swizzled layout the MMA reads, while the weights are on their way.
-// Rows past M stay unwritten: they reach only accumulator columns that are
-// not stored.
-template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false, bool kFuse = false>
+// At most eight tokens: what the MMA's other rows read reaches only
+// accumulator columns that are not stored.
+template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false, int kXq = 0>
 __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
                                                     const Fp8Args& a, int split = 1) {
+  using Cfg = F8Cfg<BN, kSwap, kTwo, kXq>;
+  constexpr bool kFuse = Cfg::kFuse;
   static_assert(!kFuse || kSplit, "one tile per CTA");
-  using Cfg = F8Cfg<BN, kSwap, kTwo, kFuse>;
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* xq = smem + S * Cfg::kStageBytes;                                // kFuse: [kF8Chunk][BN][128]
+  uint8_t* xq = smem + S * Cfg::kStageBytes;                                // [kXq][8][128]
   float* xsc = reinterpret_cast<float*>(xq + Cfg::kXqBytes);                // [2][kF8Chunk][kXRows]
   float* wsc = xsc + 2 * kF8Chunk * Cfg::kXRows;                            // [2][kF8Chunk][kWBlocks]
   uint64_t* full = reinterpret_cast<uint64_t*>(wsc + 2 * kF8Chunk * Cfg::kWBlocks);
   uint64_t* empty = full + S;
   uint64_t* done = empty + S;     // [NA]
   uint64_t* accfree = done + NA;  // [NA]
-  uint64_t* xready = accfree + NA;  // kFuse: the tokens are quantised
+  uint64_t* xready = accfree + NA;  // kXq: the tokens are quantised
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xready + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,6 +352,17 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   const int step = kSplit ? tiles : (int)gridDim.x;
   uint32_t* err = a.err;
 
+  // the producer's loads of local K block s
+  auto load_w = [&](int slot, int s, int w0) {
+    uint8_t* st = smem + slot * Cfg::kStageBytes;
+    mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
+    tma_load_2d(kSwap ? st : st + Cfg::kStageA, kSwap ? map_a : map_b, (kb0 + s) * kF8BK, w0, &full[slot]);
+  };
+  auto load_x = [&](int slot, int s, int x0) {
+    uint8_t* st = smem + slot * Cfg::kStageBytes;
+    tma_load_2d(kSwap ? st + Cfg::kStageA : st, kSwap ? map_b : map_a, (kb0 + s) * kF8BK, x0, &full[slot]);
+  };
+  const int ahead = first < tiles ? (nk < S ? nk : S) : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
@@ -333,10 +372,35 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       mbar_init(&done[b], 1);
       mbar_init(&accfree[b], Cfg::kScaleWarps);
     }
-    mbar_init(xready, Cfg::kScaleWarps);
+    mbar_init(xready, Cfg::kScaleWarps + Cfg::kQuantWarps);
     fence_mbar_init();
-    tma_prefetch_desc(map_a);
+    // this thread is the producer: the first stages' weights, which do not
+    // depend on the quantiser before us, set out at once
+    for (int s = 0; s < ahead; ++s) load_w(s, s, (first / m_tiles) * Cfg::kWRows);
     if (!kFuse) tma_prefetch_desc(map_b);
+  }
+  // kXq: the scale and quantiser warps' half-warps take a K block of 128
+  // values of a row each, lane l of 16 eight of them: half-warp h the local
+  // K block h % 16 (h % 8 where a CTA has no more) of every row (every second
+  // row).  The first rows set out here too.
+  constexpr int kAhead = 4;
+  const int qh = (int)(threadIdx.x - 32 * Cfg::kFirst) / 16, ql = lane & 15;
+  const int qkb = nk > 8 ? qh & 15 : qh & 7, qr = nk > 8 ? qh >> 4 : qh >> 3;
+  const int qstep = 2 * (Cfg::kScaleWarps + Cfg::kQuantWarps) / (nk > 8 ? 16 : 8);
+  const int qk = (kb0 + qkb) * kF8BK + ql * 8;
+  const int used = a.M < Cfg::kXRows ? a.M : Cfg::kXRows;  // (kXq: one token tile)
+  uint4 raw[kFuse ? kAhead : 1];
+  auto load_rows = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int r = r0 + i * qstep;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (qkb < nk && r < used && qk < a.K)
+        raw[i] = *reinterpret_cast<const uint4*>(a.xb + (int64_t)r * a.xb_row + qk);
+    }
+  };
+  if constexpr (kFuse) {
+    if (warp >= Cfg::kFirst) load_rows(qr);
   }
   if (warp == 1) tmem_alloc(tmem_slot, Cfg::kTmemCols);
   tc_fence_before();
@@ -345,23 +409,31 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  auto quantise = [&]() {
+    for (int r0 = qr; r0 < used; r0 += kAhead * qstep) {  // (the same rows for a whole warp)
+      if (r0 != qr) load_rows(r0);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int r = r0 + i * qstep;
+        float v[8];
+        bf16x8_to_float(raw[i], v);
+        const float sc = block_scale(block_amax(v));
+        if (qkb < nk && r < used) {
+          *reinterpret_cast<uint2*>(xq + qkb * 1024 + r * kF8BK + (((ql >> 1) ^ (r & 7)) << 4) + (ql & 1) * 8) =
+              e4m3_quotients(v, sc);
+          if (ql == 0) xsc[qkb * BN + r] = sc;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(xready);
+  };
   // (the registers move: 384 threads x 168 at launch = 128 x 40 + 256 x 232)
   if (warp < Cfg::kFirst) {
     if (Cfg::kMoveRegs) regs_dec<40>();
     if (warp == 0) {
       if (lane == 0) {
-        auto load_w = [&](int slot, int s, int w0) {
-          uint8_t* st = smem + slot * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(&full[slot], Cfg::kStageBytes);
-          tma_load_2d(kSwap ? st : st + Cfg::kStageA, kSwap ? map_a : map_b, (kb0 + s) * kF8BK, w0, &full[slot]);
-        };
-        auto load_x = [&](int slot, int s, int x0) {
-          uint8_t* st = smem + slot * Cfg::kStageBytes;
-          tma_load_2d(kSwap ? st + Cfg::kStageA : st, kSwap ? map_b : map_a, (kb0 + s) * kF8BK, x0, &full[slot]);
-        };
-        // the first stages' weights do not depend on the quantiser before us
-        const int ahead = first < tiles ? (nk < S ? nk : S) : 0;
-        for (int s = 0; s < ahead; ++s) load_w(s, s, (first / m_tiles) * Cfg::kWRows);
         pdl_wait();
         int g = 0;
         bool ok = true;
@@ -377,16 +449,19 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
             if (!kFuse) load_x(slot, s, x0);
           }
         }
+        if (!ok)  // gave up: see the copies under way in before the CTA ends
+          for (int q = g > S ? g - S : 0; q < g; ++q) mbar_wait(&full[q % S], (q / S) & 1, err, 16u);
       }
-    } else if (warp == 1) {
+    } else if (warp <= Cfg::kMmaWarps) {
       constexpr uint32_t idesc = idesc_e4m3(kF8BM, BN);
       int g = 0;
       bool ok = !kFuse || __all_sync(0xffffffffu, mbar_wait(xready, 0, err, 8u));
       for (int idx = first; ok && idx < tiles; idx += step) {
         for (int s = 0; s < nk; ++s, ++g) {
           const int slot = g % S, round = g / S, ab = g % NA, use = g / NA;
-          bool w = use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u);
-          w = w && mbar_wait(&full[slot], round & 1, err, 2u);
+          if (Cfg::kMmaWarps > 1 && ab % Cfg::kMmaWarps != warp - 1) continue;
+          bool w = mbar_wait(&full[slot], round & 1, err, 2u);
+          w = w && (use == 0 || mbar_wait(&accfree[ab], (use - 1) & 1, err, 2u));
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
@@ -394,7 +469,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           tc_fence_after();
           const uint32_t acc = tmem + (uint32_t)(ab * BN);
           const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
-          const uint8_t* bst = kFuse ? xq + s * (BN * kF8BK) : smem + slot * Cfg::kStageBytes + Cfg::kStageA;
+          const uint8_t* bst = kFuse ? xq + s * 1024 : smem + slot * Cfg::kStageBytes + Cfg::kStageA;
           const uint64_t db = smem_desc(smem_u32(bst), 16, 1024, kLayoutSW128);
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
@@ -404,6 +479,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         }
       }
     }
+  } else if (kFuse && warp >= Cfg::kFirst + Cfg::kScaleWarps) {
+    if constexpr (kFuse) quantise();
   } else {
     if (Cfg::kMoveRegs) regs_inc<232>();
     const int t = threadIdx.x - 32 * Cfg::kFirst;
@@ -428,45 +505,21 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     };
     pdl_wait();
     int g = 0, gc = 0;
-    bool ok = true;
+    uint32_t polls = kWaitPollLimit;  // 1 once a wait gave up: the warp then goes through its barriers without waiting
     if (first < tiles) load_chunk(first, 0, 0);
-    if (kFuse) {
-      // a block of 128 values per 16 lanes, kAhead blocks under way at once
-      constexpr int kUnits = 2 * Cfg::kScaleWarps, kAhead = 4;
-      const int x0 = (first % m_tiles) * Cfg::kXRows;
-      const int used = a.M - x0 < BN ? a.M - x0 : BN;
-      const int l = lane & 15, units = used * nk;
-      for (int u0 = t / 16; u0 - (lane >> 4) < units; u0 += kUnits * kAhead) {
-        uint4 raw[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int u = u0 + i * kUnits, k = (kb0 + u % nk) * kF8BK + l * 8;
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (u < units && k < a.K)
-            raw[i] = *reinterpret_cast<const uint4*>(a.xb + (int64_t)(x0 + u / nk) * a.xb_row + k);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int u = u0 + i * kUnits, kb = u % nk, r = u / nk;
-          float v[8];
-          bf16x8_to_float(raw[i], v);
-          const float sc = block_scale(block_amax(v));
-          if (u < units) {
-            *reinterpret_cast<uint2*>(xq + kb * (BN * kF8BK) + r * kF8BK + (((l >> 1) ^ (r & 7)) << 4) + (l & 1) * 8) =
-                e4m3_quotients(v, sc);
-            if (l == 0) xsc[kb * BN + r] = sc;
-          }
-        }
+    if constexpr (kFuse) {
+      quantise();
+      // (the scales of the quantiser warps' rows)
+      if (!warp_wait(xready, 0, polls)) {
+        polls = 1;
+        atomicOr(err, 8u);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(xready);
     }
     for (int idx = first; idx < tiles; idx += step) {
       const int x0 = (idx % m_tiles) * Cfg::kXRows, w0 = (idx / m_tiles) * Cfg::kWRows;
-      float2 acc[Cfg::kCols / 2];
+      uint64_t acc[Cfg::kCols / 2];  // pairs of sums
 #pragma unroll
-      for (int i = 0; i < Cfg::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < Cfg::kCols / 2; ++i) acc[i] = 0;
       for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
         // this chunk's scales have arrived, and every warp is past the chunk
         // before it, so the other buffer is free for the next chunk
@@ -480,49 +533,53 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
         const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
         const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
-        // Wait for K block gg's accumulator and start its first load.  A wait
-        // that gave up is recorded; its warp goes on, so that the scale
-        // warps' barriers stay whole, and waits no more.
-        uint32_t r[2][Cfg::kLd];
-        auto begin = [&](int gg) {
-          const int ab = gg % NA;
-          if (ok && !__all_sync(0xffffffffu, mbar_wait(&done[ab], (gg / NA) & 1, err, 4u))) ok = false;
-          if (!ok) return;
-          tc_fence_after();
-          TmemLd<Cfg::kLd>::start(tm + (uint32_t)(ab * BN), r[0]);
-        };
-        begin(g);
+        // The accumulator's columns pass through two register buffers.  A
+        // wait for tensor-memory loads is for all of them, so both buffers'
+        // loads fly together, each started as its buffer is used up.  (No
+        // conditions here: with loads under a branch the compiler copies the
+        // buffers.)
+        constexpr int kLoads = Cfg::kCols / Cfg::kLd;
+#pragma unroll 1
         for (int kk = 0; kk < n; ++kk, ++g) {
-          if (!ok) continue;
           const int ab = g % NA;
           const uint32_t src = tm + (uint32_t)(ab * BN);
           const float ws = wd[kk * Cfg::kWBlocks + (kSwap ? 0 : half * Cfg::kCols / 128)];
           const float rs = kSwap ? 0.f : xd[kk * Cfg::kXRows + row] * ws;
-          constexpr int kLoads = Cfg::kCols / Cfg::kLd;
+          const uint64_t rs2 = pack2(__float_as_uint(rs), __float_as_uint(rs));
+          // acc += scales * (columns of load j)
+          auto add = [&](int j, const uint32_t (&r)[Cfg::kLd]) {
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            TmemLd<Cfg::kLd>::wait(r[j & 1]);
-            if (j + 1 < kLoads) {
-              TmemLd<Cfg::kLd>::start(src + Cfg::kLd * (j + 1), r[(j + 1) & 1]);
-            } else {
-              // the accumulator is read out: hand it back, and start on the
-              // next one while this one's last columns are added
+            for (int i = 0; i < Cfg::kLd / 2; ++i) {
+              uint64_t s = rs2;
+              if (kSwap) {
+                const float2 f =
+                    *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + Cfg::kLd * j + 2 * i);
+                s = pack2(__float_as_uint(f.x * ws), __float_as_uint(f.y * ws));
+              }
+              fma2(acc[Cfg::kLd / 2 * j + i], pack2(r[2 * i], r[2 * i + 1]), s);
+            }
+          };
+          if (!warp_wait(&done[ab], (g / NA) & 1, polls)) {
+            polls = 1;
+            atomicOr(err, 4u);
+          }
+          tc_fence_after();
+          uint32_t r0[Cfg::kLd], r1[Cfg::kLd];
+          TmemLd<Cfg::kLd>::start(src, r0);
+          TmemLd<Cfg::kLd>::start(src + Cfg::kLd, r1);
+#pragma unroll
+          for (int j = 0; j < kLoads; j += 2) {
+            TmemLd<Cfg::kLd>::wait(r0);
+            TmemLd<Cfg::kLd>::wait(r1);
+            if (j + 2 == kLoads) {  // the accumulator is read out
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&accfree[ab]);
-              if (kk + 1 < n) begin(g + 1);
             }
-#pragma unroll
-            for (int i = 0; i < Cfg::kLd / 2; ++i) {
-              const float2 v = make_float2(__uint_as_float(r[j & 1][2 * i]), __uint_as_float(r[j & 1][2 * i + 1]));
-              float2 s = make_float2(rs, rs);
-              if (kSwap) {
-                s = *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + Cfg::kLd * j + 2 * i);
-                s.x *= ws;
-                s.y *= ws;
-              }
-              acc[Cfg::kLd / 2 * j + i] = ffma2(v, s, acc[Cfg::kLd / 2 * j + i]);
-            }
+            add(j, r0);
+            if (j + 2 < kLoads) TmemLd<Cfg::kLd>::start(src + Cfg::kLd * (j + 2), r0);
+            add(j + 1, r1);
+            if (j + 2 < kLoads) TmemLd<Cfg::kLd>::start(src + Cfg::kLd * (j + 3), r1);
           }
         }
       }
@@ -533,32 +590,33 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
 #pragma unroll
           for (int i = 0; i < Cfg::kCols / 2; ++i) {
             const int c = half * Cfg::kCols + 2 * i;
-            part[c * Cfg::kPartRow + row] = acc[i].x;
-            part[(c + 1) * Cfg::kPartRow + row] = acc[i].y;
+            part[c * Cfg::kPartRow + row] = pair_lo(acc[i]);
+            part[(c + 1) * Cfg::kPartRow + row] = pair_hi(acc[i]);
           }
         } else {
           float4* p = reinterpret_cast<float4*>(part + row * Cfg::kPartRow + half * Cfg::kCols);
 #pragma unroll
           for (int i = 0; i < Cfg::kCols / 4; ++i)
-            p[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+            p[i] = make_float4(pair_lo(acc[2 * i]), pair_hi(acc[2 * i]), pair_lo(acc[2 * i + 1]), pair_hi(acc[2 * i + 1]));
         }
         continue;
       }
-      if (!ok) continue;
+      if (polls == 1) continue;
       if (kSwap) {  // lanes along n: 32 consecutive columns of one token per store
         const int nn = w0 + row;
 #pragma unroll
         for (int i = 0; i < Cfg::kCols / 2; ++i) {
           const int m = x0 + half * Cfg::kCols + 2 * i;
-          if (nn < a.N && m < a.M) f8_store_one(a, m, nn, acc[i].x);
-          if (nn < a.N && m + 1 < a.M) f8_store_one(a, m + 1, nn, acc[i].y);
+          if (nn < a.N && m < a.M) f8_store_one(a, m, nn, pair_lo(acc[i]));
+          if (nn < a.N && m + 1 < a.M) f8_store_one(a, m + 1, nn, pair_hi(acc[i]));
         }
       } else if (x0 + row < a.M) {
 #pragma unroll
         for (int i = 0; i < Cfg::kCols / 8; ++i) {
           const int nn = w0 + half * Cfg::kCols + 8 * i;
-          const float v[8] = {acc[4 * i].x,     acc[4 * i].y,     acc[4 * i + 1].x, acc[4 * i + 1].y,
-                              acc[4 * i + 2].x, acc[4 * i + 2].y, acc[4 * i + 3].x, acc[4 * i + 3].y};
+          float v[8];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) v[2 * p] = pair_lo(acc[4 * i + p]), v[2 * p + 1] = pair_hi(acc[4 * i + p]);
           if (nn < a.N) f8_store_8(a, x0 + row, nn, v);
         }
       }

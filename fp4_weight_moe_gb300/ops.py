@@ -197,7 +197,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
     """``fp8_matmul`` of the bfloat16 ``x [M, K]``, quantised as
     ``fp8_quantize`` does.  ``workspace`` (alloc_fp8_workspace) holds the
     quantised rows; without one the call takes it from torch's allocator (up
-    to 16 rows of at most 16384 columns need none)."""
+    to 8 rows of at most 16384 columns need none)."""
     if stream is not None:
         with _on(stream, x):
             return fp8_linear(x, w, w_scale, out, addend, out_dtype, workspace)
@@ -210,7 +210,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, out: Opt
     add, add_row, out, out_row, f32 = _product_output(addend, out, out_dtype, dev, w.device, M, N)
     ws_ptr = ws_bytes = 0
     if workspace is None:
-        if M > 16 or K > 16384:
+        if M > _capi.MOE_FP4_DECODE_MAX_M or K > 16384:
             workspace = _empty(_capi.moe_fp4_fp8_linear_workspace_bytes(M, K), dtype=torch.uint8, device=x.device)
     elif workspace.device != x.device or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on x's device")

@@ -634,9 +634,9 @@ MOE_FP4_API int moe_fp4_fp8_matmul(const void *x_q, int64_t x_row, const float *
  * moe_fp4_fp8_quantize (act == NULL) and moe_fp4_fp8_matmul in one call: out
  * = x W^T with x [M][K] bf16, on a caller-owned workspace of
  * moe_fp4_fp8_linear_workspace_bytes(M, K) bytes (256-byte aligned, needs no
- * initialisation; MOE_FP4_EWORKSPACE if missing or too small).  Up to 16
- * rows with K <= 16384 the product quantises its own rows, in one launch: the
- * workspace is then not used and may be NULL.  Results are those of the two
+ * initialisation; MOE_FP4_EWORKSPACE if missing or too small).  Up to
+ * MOE_FP4_DECODE_MAX_M rows with K <= 16384 the product quantises its own
+ * rows, in one launch: the workspace is then not used and may be NULL.  Results are those of the two
  * calls, bitwise.  The size is 0 for invalid arguments.
  */
 MOE_FP4_API size_t moe_fp4_fp8_linear_workspace_bytes(int M_max, int K);

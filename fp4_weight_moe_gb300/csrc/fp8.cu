@@ -257,15 +257,16 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   a.xs_blk = xs_blk;
   const int M = p.M, N = p.N, K = p.K;
   const Operands o = {x, w, x_row, w_row, after_quantizer};
-  // Up to 64 tokens the weights' 128 rows lie on the MMA's row side and the
-  // tokens (16, 32 or 64) on its column side, two CTAs per SM; past that the tokens take the row side, where a scale
-  // thread's activation scale is one value instead of one per column.
-  // Measured (us, K x N): M=128 7168 x 4096, tokens on columns 14.5 / on rows
-  // 11.9; 2048 x 7168 11.2 / 9.6; M=64, tokens on rows 22.6 against 13.0 and
-  // 13.0 against 9.7; M=1 7168 x 4096 split 1 / 2 / 4 / 8: 22.3 / 12.4 / 8.1
-  // / 7.8; M=256 4096 x 4096 split 1 / 2 / 4: 18.4 / 12.8 / 18.5 (two waves).
+  // Up to 32 tokens the weights' 128 rows lie on the MMA's row side and the
+  // tokens (16 or 32) on its column side, two CTAs per SM; past that the
+  // tokens take the row side, where a scale thread's activation scale is one
+  // value instead of one per column.  Measured (us, K x N): 7168 x 4096, M=64
+  // tokens on 64 columns 12.4, M=128 on columns 14.5, on rows 11.4; 4096 x
+  // 4096 M=64 on columns 9.6, M=65 on rows 8.8; M=1 7168 x 4096 split 1 / 2 /
+  // 4 / 8: 22.3 / 12.4 / 8.1 / 7.8; M=256 4096 x 4096 split 1 / 2 / 4: 18.4 /
+  // 12.8 / 18.5 (two waves).
   const int nk = (K + 127) / 128;
-  const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const int bn = M <= 16 ? 16 : M <= 32 ? 32 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);
   const int slots = bn == 128 ? sms : 2 * sms;
   if (tiles <= slots / 2 || bn == 16) {
@@ -273,7 +274,6 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
     switch (bn) {
       case 16: return launch_split<16, true, true>(o, a, (int)tiles, split, st);
       case 32: return launch_split<32, true, true>(o, a, (int)tiles, split, st);
-      case 64: return launch_split<64, true, true>(o, a, (int)tiles, split, st);
       default: return launch_split<128, false, false>(o, a, (int)tiles, split, st);
     }
   }

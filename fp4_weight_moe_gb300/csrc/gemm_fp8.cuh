@@ -7,20 +7,26 @@
 // two per 32 K), so every K block gets an accumulator of its own, which the
 // scale warps read, scale and add up while the next block multiplies.
 //
-// A CTA computes 128 x BN tiles in turn with kFirst + 4 * kHalves warps:
+// A CTA computes 128 x BN tiles in turn:
 //   warp 0 lane 0  TMA producer: per K block the 128-row box (128 x 128 B)
 //                  and the BN-row box, SWIZZLE_128B, into a ring;
-//   warp 1         allocates tensor memory and, converged, issues the four
-//                  K = 32 MMAs of a block into accumulator g % kAcc, then
-//                  commits that free the stage and publish the accumulator;
+//   warps 1, 2     (warp 1 allocates tensor memory) converged, issue the four
+//                  K = 32 MMAs of a block into accumulator g % kAcc (each
+//                  warp every second block), then the commits that publish
+//                  the accumulator and free the stage;
 //   scale warps    each reads its 32 accumulator lanes (and its half of the
-//                  columns where BN >= 64), adds them, scaled, into
+//                  columns where BN >= 128), adds them, scaled, into
 //                  registers, and stores the finished tile.
 // The scales of 16 K blocks at a time are copied to shared memory
 // (cp.async, any strides) one chunk ahead, across tile boundaries too.
 //
 // The 128-row operand is X (kSwap = false) or W (kSwap = true: few tokens,
 // the tokens on the MMA's N side).
+//
+// What bounds a 128 x 256 tile (cycles per K block, measured): the MMAs alone
+// 512, its 48 KB through the SM's 64 bytes a cycle 750, the scale warps' sums
+// alone 270 (330 with their tensor-memory loads); with two accumulators in
+// flight the hand-overs between the three leave it at about 920.
 #pragma once
 
 #include "common.cuh"
@@ -57,7 +63,7 @@ struct F8Cfg {
   static constexpr bool kFuse = kXq > 0;
   static_assert(kXq <= kF8Chunk, "the scales of all K blocks lie in one chunk");
   static_assert(!kFuse || kSwap, "the kernel quantises a few tokens only");
-  static constexpr int kHalves = BN >= 64 ? 2 : 1;
+  static constexpr int kHalves = BN >= 128 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
   static constexpr int kLd = kCols / 2 < 32 ? kCols / 2 : 32;  // ... per tensor-memory load (an even count of them)
   static constexpr int kScaleWarps = 4 * kHalves;
@@ -65,8 +71,10 @@ struct F8Cfg {
   // registers than an even split of the SM's gives ten warps, so the scale
   // warps take them (setmaxnreg) from a warpgroup that holds warps 0 and 1
   static constexpr bool kMoveRegs = BN >= 256;
-  static constexpr int kFirst = kMoveRegs ? 4 : 2;  // first scale warp
-  static constexpr int kMmaWarps = kMoveRegs ? 2 : 1;
+  // two warps issue MMAs, each into its own accumulators, so that the waits
+  // and the issue of one hide behind the other's MMAs
+  static constexpr int kMmaWarps = 2;
+  static constexpr int kFirst = kMoveRegs ? 4 : 1 + kMmaWarps;  // first scale warp
   static constexpr int kQuantWarps = kFuse ? 4 : 0;  // they help the scale warps quantise, then leave
   static constexpr int kThreads = 32 * (kFirst + kScaleWarps + kQuantWarps);
   static constexpr int kAcc = BN >= 256 ? 2 : 4;
@@ -103,13 +111,22 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// One K = 32 MMA from one elected lane of a converged warp.
-__device__ __forceinline__ void mma_f8_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+// The four K = 32 MMAs of a K block (the first overwrites the accumulator)
+// and the commits behind them, from one elected lane of a converged warp:
+// `done` and `empty` are arrived on when the MMAs are complete.
+__device__ __forceinline__ void mma_f8_block(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint64_t* done, uint64_t* empty) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p, q, e;\n\tsetp.ne.u32 p, %9, %9;\n\tsetp.eq.u32 q, %9, %9;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %5, %9, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %2, %6, %9, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %3, %7, %9, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %4, %8, %9, q;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%10];\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%11];\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(a_desc + 2), "l"(a_desc + 4), "l"(a_desc + 6), "l"(b_desc), "l"(b_desc + 2),
+        "l"(b_desc + 4), "l"(b_desc + 6), "r"(idesc), "r"(smem_u32(done)), "r"(smem_u32(empty))
       : "memory");
 }
 
@@ -471,11 +488,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           const uint64_t da = smem_desc(smem_u32(smem + slot * Cfg::kStageBytes), 16, 1024, kLayoutSW128);
           const uint8_t* bst = kFuse ? xq + s * 1024 : smem + slot * Cfg::kStageBytes + Cfg::kStageA;
           const uint64_t db = smem_desc(smem_u32(bst), 16, 1024, kLayoutSW128);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // K step of 32 = 32 bytes = 2 descriptor units
-            mma_f8_warp(acc, da + 2 * k, db + 2 * k, idesc, k > 0);
-          mma_commit_warp(&empty[slot]);
-          mma_commit_warp(&done[ab]);
+          mma_f8_block(acc, da, db, idesc, &done[ab], &empty[slot]);
         }
       }
     }
@@ -549,14 +562,16 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           // acc += scales * (columns of load j)
           auto add = [&](int j, const uint32_t (&r)[Cfg::kLd]) {
 #pragma unroll
-            for (int i = 0; i < Cfg::kLd / 2; ++i) {
-              uint64_t s = rs2;
-              if (kSwap) {
-                const float2 f =
-                    *reinterpret_cast<const float2*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + Cfg::kLd * j + 2 * i);
-                s = pack2(__float_as_uint(f.x * ws), __float_as_uint(f.y * ws));
+            for (int i = 0; i < Cfg::kLd / 4; ++i) {
+              uint64_t s0 = rs2, s1 = rs2;
+              if (kSwap) {  // a scale per column, four at a time
+                const float4 f =
+                    *reinterpret_cast<const float4*>(xd + kk * Cfg::kXRows + half * Cfg::kCols + Cfg::kLd * j + 4 * i);
+                s0 = pack2(__float_as_uint(f.x * ws), __float_as_uint(f.y * ws));
+                s1 = pack2(__float_as_uint(f.z * ws), __float_as_uint(f.w * ws));
               }
-              fma2(acc[Cfg::kLd / 2 * j + i], pack2(r[2 * i], r[2 * i + 1]), s);
+              fma2(acc[Cfg::kLd / 2 * j + 2 * i], pack2(r[4 * i], r[4 * i + 1]), s0);
+              fma2(acc[Cfg::kLd / 2 * j + 2 * i + 1], pack2(r[4 * i + 2], r[4 * i + 3]), s1);
             }
           };
           if (!warp_wait(&done[ab], (g / NA) & 1, polls)) {

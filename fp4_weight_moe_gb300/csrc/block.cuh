@@ -6,8 +6,9 @@
 
 namespace moe_fp4 {
 
+// `dependent`: launched as its predecessor's dependent (launch_dependent).
 cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,
-                                int64_t s_row, int64_t s_blk, int M, int K, cudaStream_t st);
+                                int64_t s_row, int64_t s_blk, int M, int K, bool dependent, cudaStream_t st);
 // A product's weight scales, addend, output and sizes.
 struct Fp8Product {
   const float* ws;
@@ -19,7 +20,8 @@ struct Fp8Product {
   int out_f32;
   int M, N, K;
 };
-// `after_quantizer`: the stream's last launch is launch_fp8_quantize of x.
+// `after_quantizer`: the stream's last launch is launch_fp8_quantize of x, in
+// plain order.
 cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int64_t xs_row, int64_t xs_blk,
                               const void* w, int64_t w_row, Fp8Product p, bool after_quantizer, cudaStream_t st);
 // BF16 x, where fp8_linear_is_fused(M, K).

@@ -62,7 +62,7 @@ int moe_fp4_fp8_quantize(const void* x_bf16, int64_t x_row, const moe_fp4_activa
   if (!rows_ok(x_row, act ? 2 * (int64_t)K : K, M) || !rows_ok(q_row, K, M) || x_row % 8 != 0 || q_row % 16 != 0)
     return MOE_FP4_EINVAL;
   if (s_row < 0 || s_block < 0) return MOE_FP4_EINVAL;
-  return done(launch_fp8_quantize(x_bf16, x_row, act ? &ap : nullptr, q, q_row, s, s_row, s_block, M, K,
+  return done(launch_fp8_quantize(x_bf16, x_row, act ? &ap : nullptr, q, q_row, s, s_row, s_block, M, K, true,
                                   static_cast<cudaStream_t>(stream)));
 }
 
@@ -103,7 +103,7 @@ int moe_fp4_fp8_linear(const void* x_bf16, int64_t x_row, const void* w, int64_t
   if (fused) return done(launch_fp8_linear_fused(x_bf16, x_row, w, w_row, p, static_cast<cudaStream_t>(stream)));
   float* s = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)M * K));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_fp8_quantize(x_bf16, x_row, nullptr, workspace, K, s, 1, M, M, K, cs);
+  const cudaError_t e = launch_fp8_quantize(x_bf16, x_row, nullptr, workspace, K, s, 1, M, M, K, false, cs);
   if (e != cudaSuccess) return report_cuda_error(e);
   return done(launch_fp8_matmul(workspace, K, s, 1, M, w, w_row, p, true, cs));
 }

@@ -15,9 +15,9 @@ cudaError_t fp8_status_address(void** p) { return cudaGetSymbolAddress(p, g_fp8_
 // ---------------------------------------------------------------- quantiser
 // Per row and 128 columns: s = max|v| / 448 (1 where that is zero), q =
 // e4m3_rn(v / s), each step an IEEE FP32 operation; v is the input, or
-// act(gate) * up of a gated row [gate | up].  HBM bound: a warp takes 1024
-// columns of a row, all its loads (four of 16 bytes per lane) under way
-// before the first block's maximum.
+// act(gate) * up of a gated row [gate | up].  HBM bound: a warp takes up to
+// 1024 columns of a row, all its loads (of 16 bytes per lane) under way before
+// the first block's maximum.
 
 // SiLU in full FP32 precision: the scale of a block follows its largest
 // product, and an element near the middle of two E4M3 values turns on it.
@@ -26,24 +26,24 @@ __device__ __forceinline__ float gated_exact(float g, float u, const ActParams& 
   return gated_act(g, u, act);
 }
 
-constexpr int kQuantCols = 1024;  // columns per warp
-
-template <bool kGated>
+// kChunks chunks of 256 columns per warp
+template <bool kGated, int kChunks>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __restrict__ x, int64_t x_row, ActParams act,
                                                            uint8_t* __restrict__ q, int64_t q_row,
                                                            float* __restrict__ s, int64_t s_row, int64_t s_blk, int M,
                                                            int K) {
+  pdl_wait();
   pdl_launch_dependents();
-  const unsigned groups = (unsigned)(K + kQuantCols - 1) / kQuantCols;
+  const unsigned groups = (unsigned)(K + 256 * kChunks - 1) / (256 * kChunks);
   const unsigned task = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const unsigned m = task / groups;
   if (m >= (unsigned)M) return;
   const int lane = threadIdx.x & 31;
-  const int k0 = (int)(task % groups) * kQuantCols + lane * 8;
+  const int k0 = (int)(task % groups) * (256 * kChunks) + lane * 8;
   const uint16_t* row = x + m * x_row;
-  uint4 raw[4], raw_up[4];
+  uint4 raw[kChunks], raw_up[kChunks];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kChunks; ++i) {
     const int k = k0 + i * 256;
     raw[i] = raw_up[i] = make_uint4(0, 0, 0, 0);
     if (k < K) {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __res
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kChunks; ++i) {
     const int k = k0 + i * 256;
     if ((k & ~255) >= K) break;  // (the whole warp)
     float v[8];
@@ -71,20 +71,36 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __res
   }
 }
 
-cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,
-                                int64_t s_row, int64_t s_blk, int M, int K, cudaStream_t st) {
-  // (tasks fit 32 bits: each stands for up to 1024 values in memory)
-  const int64_t tasks = (int64_t)M * ((K + kQuantCols - 1) / kQuantCols);
-  const unsigned warps = tasks < 1024 ? 2 : 8;  // few tasks: spread over the SMs
+template <bool kGated, int kChunks>
+static cudaError_t launch_quantize(const void* x, int64_t x_row, const ActParams& act, void* q, int64_t q_row, float* s,
+                                   int64_t s_row, int64_t s_blk, int M, int K, unsigned warps, bool dependent,
+                                   cudaStream_t st) {
+  // (tasks fit 32 bits: each stands for 256 values or a whole row in memory)
+  const int64_t tasks = (int64_t)M * ((K + 256 * kChunks - 1) / (256 * kChunks));
   const unsigned grid = (unsigned)((tasks + warps - 1) / warps);
-  const ActParams none = {MOE_FP4_ACT_SILU, 0.f, 0.f, 0.f};
-  if (act)
-    fp8_quantize_kernel<true><<<grid, 32 * warps, 0, st>>>(static_cast<const uint16_t*>(x), x_row, *act,
-                                                           static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
-  else
-    fp8_quantize_kernel<false><<<grid, 32 * warps, 0, st>>>(static_cast<const uint16_t*>(x), x_row, none,
-                                                            static_cast<uint8_t*>(q), q_row, s, s_row, s_blk, M, K);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  uint8_t* qp = static_cast<uint8_t*>(q);
+  if (dependent)
+    return launch_dependent(fp8_quantize_kernel<kGated, kChunks>, grid, 32 * warps, st, xp, x_row, act, qp, q_row, s,
+                            s_row, s_blk, M, K);
+  fp8_quantize_kernel<kGated, kChunks><<<grid, 32 * warps, 0, st>>>(xp, x_row, act, qp, q_row, s, s_row, s_blk, M, K);
   return cudaGetLastError();
+}
+
+cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,
+                                int64_t s_row, int64_t s_blk, int M, int K, bool dependent, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = current_device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  const ActParams none = {MOE_FP4_ACT_SILU, 0.f, 0.f, 0.f};
+  // 1024 columns per warp where that gives every SM its warps, else 256, so
+  // that a few rows spread over the GPU
+  const bool few = (int64_t)M * ((K + 1023) / 1024) < 16 * sms;
+  if (act && few)
+    return launch_quantize<true, 1>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
+  if (act) return launch_quantize<true, 4>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
+  if (few) return launch_quantize<false, 1>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
+  return launch_quantize<false, 4>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
 }
 
 // ------------------------------------------------------------------ product
@@ -132,16 +148,14 @@ static Fp8Args args_of(const Fp8Product& p) {
 struct Operands {
   const void *x, *w;
   int64_t x_row, w_row;
-  bool after_quantizer;  // the launch before this one on the stream is the quantiser of x
 };
 
-// Launch with a cluster of `split` CTAs and, behind our own quantiser, with
-// programmatic dependent launch: the kernel's prologue and its first weight
-// loads then run beside the quantiser, and griddepcontrol.wait comes before
-// everything else it reads.  (The quantiser itself is launched in plain
-// stream order, so whatever wrote the weights has finished.)
+// Launch with a cluster of `split` CTAs, as a dependent of the launch before
+// (see launch_dependent).  Behind our own quantiser (a.early) the first
+// weight loads, too, run beside it, before the wait: the quantiser is then
+// launched in plain stream order, so whatever wrote the weights has finished.
 template <class Kern, class... Args>
-static cudaError_t launch_product(Kern kern, int64_t ctas, int threads, size_t smem, int split, bool dependent,
+static cudaError_t launch_product(Kern kern, int64_t ctas, int threads, size_t smem, int split,
                                   cudaStream_t st, const Args&... args) {
   cudaLaunchAttribute at[2];
   unsigned n = 0;
@@ -151,11 +165,9 @@ static cudaError_t launch_product(Kern kern, int64_t ctas, int threads, size_t s
     at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (dependent) {
-    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)ctas);
   c.blockDim = dim3((unsigned)threads);
@@ -184,8 +196,8 @@ static cudaError_t launch_gemm(const Operands& o, const Fp8Args& a, int sms, cud
   if (e != cudaSuccess) return e;
   const int64_t tiles =
       (int64_t)((a.M + Cfg::kXRows - 1) / Cfg::kXRows) * ((a.N + Cfg::kWRows - 1) / Cfg::kWRows);
-  return launch_product(fp8_gemm_kernel<BN, kSwap>, tiles < sms ? tiles : sms, Cfg::kThreads, Cfg::kSmem, 1,
-                        o.after_quantizer, st, kSwap ? mw : mx, kSwap ? mx : mw, a);
+  return launch_product(fp8_gemm_kernel<BN, kSwap>, tiles < sms ? tiles : sms, Cfg::kThreads, Cfg::kSmem, 1, st,
+                        kSwap ? mw : mx, kSwap ? mx : mw, a);
 }
 
 template <int BN, bool kSwap, bool kTwo>
@@ -196,8 +208,8 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
   static bool seen[64];
   if (e == cudaSuccess) e = allow_smem(fp8_split_kernel<BN, kSwap, kTwo>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
-  return launch_product(fp8_split_kernel<BN, kSwap, kTwo>, (int64_t)tiles * split, Cfg::kThreads, Cfg::kSmem, split,
-                        o.after_quantizer, st, kSwap ? mw : mx, kSwap ? mx : mw, a, split);
+  return launch_product(fp8_split_kernel<BN, kSwap, kTwo>, (int64_t)tiles * split, Cfg::kThreads, Cfg::kSmem, split, st,
+                        kSwap ? mw : mx, kSwap ? mx : mw, a, split);
 }
 
 // Few tiles: K is split over a cluster until the CTAs fill `slots`, with at
@@ -224,8 +236,7 @@ static cudaError_t launch_fused(const CUtensorMap& mw, const Fp8Args& a, int64_t
   static bool seen[64];
   const cudaError_t e = allow_smem(fp8_linear_kernel<kXq>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
-  return launch_product(fp8_linear_kernel<kXq>, tiles * split, Cfg::kThreads, Cfg::kSmem, split, false, st, mw, a,
-                        split);
+  return launch_product(fp8_linear_kernel<kXq>, tiles * split, Cfg::kThreads, Cfg::kSmem, split, st, mw, a, split);
 }
 
 cudaError_t launch_fp8_linear_fused(const void* x, int64_t x_row, const void* w, int64_t w_row, Fp8Product p,
@@ -256,7 +267,8 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   a.xs_row = xs_row;
   a.xs_blk = xs_blk;
   const int M = p.M, N = p.N, K = p.K;
-  const Operands o = {x, w, x_row, w_row, after_quantizer};
+  const Operands o = {x, w, x_row, w_row};
+  a.early = after_quantizer;
   // Up to 32 tokens the weights' 128 rows lie on the MMA's row side and the
   // tokens (16 or 32) on its column side, two CTAs per SM; past that the
   // tokens take the row side, where a scale thread's activation scale is one

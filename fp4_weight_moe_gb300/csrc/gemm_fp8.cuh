@@ -51,6 +51,7 @@ struct Fp8Args {
   void* out;
   int64_t out_row;
   int out_f32;
+  int early;  // the first weight loads may run before the launch before this one is complete
   int vec;  // out (and add) rows start 16-byte aligned
   int M, N, K;
   uint32_t* err;
@@ -391,8 +392,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     }
     mbar_init(xready, Cfg::kScaleWarps + Cfg::kQuantWarps);
     fence_mbar_init();
-    // this thread is the producer: the first stages' weights, which do not
-    // depend on the quantiser before us, set out at once
+    // this thread is the producer: the first stages' weights set out at once
+    if (!a.early) pdl_wait();
     for (int s = 0; s < ahead; ++s) load_w(s, s, (first / m_tiles) * Cfg::kWRows);
     if (!kFuse) tma_prefetch_desc(map_b);
   }
@@ -417,8 +418,16 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     }
   };
   if constexpr (kFuse) {
-    if (warp >= Cfg::kFirst) load_rows(qr);
+    if (warp >= Cfg::kFirst) {
+      pdl_wait();
+      load_rows(qr);
+    }
   }
+  // (This CTA may be resident before the launch before it is complete, and the
+  // allocation waits until the columns are free.  It never holds columns that
+  // a CTA of that launch still needs: CTAs of this library that fit beside a
+  // kTwo CTA in shared memory, its own kind and the decode band's, take at
+  // most 256 columns, and beside the others none fits.)
   if (warp == 1) tmem_alloc(tmem_slot, Cfg::kTmemCols);
   tc_fence_before();
   __syncwarp();
@@ -517,6 +526,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       }
     };
     pdl_wait();
+    pdl_launch_dependents();
     int g = 0, gc = 0;
     uint32_t polls = kWaitPollLimit;  // 1 once a wait gave up: the warp then goes through its barriers without waiting
     if (first < tiles) load_chunk(first, 0, 0);

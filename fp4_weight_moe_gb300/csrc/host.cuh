@@ -47,4 +47,23 @@ cudaError_t allow_smem(Kern kern, size_t bytes, bool (&seen)[64]) {
   return e;
 }
 
+// Launch with programmatic dependent launch: the kernel may become resident
+// while its predecessor on the stream finishes; it waits for that one's
+// completion (griddepcontrol.wait) before it touches global memory, and lets
+// its own successor in only after that wait, so that no kernel ever runs
+// beside one two launches before it.
+template <class Kern, class... Args>
+cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned threads, cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.stream = st;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
+
 }  // namespace moe_fp4

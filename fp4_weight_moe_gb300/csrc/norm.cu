@@ -147,6 +147,8 @@ __device__ __forceinline__ float scalar_of(const void* p, int f32, int64_t i) {
 template <int kCh, int kMaxThreads, bool kVec, bool kF32>
 __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][32];
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t m = blockIdx.x;
   const int H = a.H;
   const float inv_h = 1.0f / (float)H;
@@ -247,16 +249,11 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
 template <int kCh, int kMaxThreads>
 static cudaError_t launch_ch(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {
   const unsigned threads = (unsigned)((a.H + 256 * kCh - 1) / (256 * kCh)) * 32;
-  const unsigned grid = (unsigned)a.M;
-  if (vec && res_f32)
-    block_norm_kernel<kCh, kMaxThreads, true, true><<<grid, threads, 0, st>>>(a);
-  else if (vec)
-    block_norm_kernel<kCh, kMaxThreads, true, false><<<grid, threads, 0, st>>>(a);
-  else if (res_f32)
-    block_norm_kernel<kCh, kMaxThreads, false, true><<<grid, threads, 0, st>>>(a);
-  else
-    block_norm_kernel<kCh, kMaxThreads, false, false><<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  auto* kern = vec ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, true, true>
+                              : block_norm_kernel<kCh, kMaxThreads, true, false>)
+                   : (res_f32 ? block_norm_kernel<kCh, kMaxThreads, false, true>
+                              : block_norm_kernel<kCh, kMaxThreads, false, false>);
+  return launch_dependent(kern, (unsigned)a.M, threads, st, a);
 }
 
 cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {

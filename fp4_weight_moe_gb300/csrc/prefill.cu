@@ -134,7 +134,8 @@ CUresult encode_u8_map_2d(CUtensorMap* m, const void* base, uint64_t inner, uint
                           uint32_t box_rows) {
   EncodeTiledFn enc = encode_tiled();
   if (!enc) return CUDA_ERROR_NOT_FOUND;
-  const cuuint64_t d[2] = {inner, rows}, strides[1] = {stride};
+  // (a single row's stride is never used, but has to be a valid one)
+  const cuuint64_t d[2] = {inner, rows}, strides[1] = {rows == 1 ? (inner + 15) / 16 * 16 : stride};
   const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), d, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -70,6 +70,8 @@ constexpr int kRouteWarps = 8;
 template <int kGroups>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(RouteArgs a, int vec) {
   __shared__ unsigned long long found[kRouteWarps][32];
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t m = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (m >= a.M) return;
@@ -172,6 +174,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_kernel(RouteArgs 
 // Any number of experts: each of the k choices is a pass over the row for the
 // largest key below the last one.
 __global__ void __launch_bounds__(32 * kRouteWarps) route_topk_wide_kernel(RouteArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
   const int64_t m = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
   if (m >= a.M) return;
@@ -217,17 +221,11 @@ cudaError_t launch_route_topk(const RouteArgs& a, cudaStream_t st) {
   const unsigned grid = (unsigned)(((int64_t)a.M + warps - 1) / warps), threads = 32 * warps;
   const unsigned bytes = a.f32 ? 16 : 8;  // of a lane's four logits
   const int vec = ((uintptr_t)a.logits % bytes) == 0 && a.row % 4 == 0;
-  if (a.E <= 128)
-    route_topk_kernel<1><<<grid, threads, 0, st>>>(a, vec);
-  else if (a.E <= 256)
-    route_topk_kernel<2><<<grid, threads, 0, st>>>(a, vec);
-  else if (a.E <= 512)
-    route_topk_kernel<4><<<grid, threads, 0, st>>>(a, vec);
-  else if (a.E <= 1024)
-    route_topk_kernel<8><<<grid, threads, 0, st>>>(a, vec);
-  else
-    route_topk_wide_kernel<<<grid, threads, 0, st>>>(a);
-  return cudaGetLastError();
+  if (a.E <= 128) return launch_dependent(route_topk_kernel<1>, grid, threads, st, a, vec);
+  if (a.E <= 256) return launch_dependent(route_topk_kernel<2>, grid, threads, st, a, vec);
+  if (a.E <= 512) return launch_dependent(route_topk_kernel<4>, grid, threads, st, a, vec);
+  if (a.E <= 1024) return launch_dependent(route_topk_kernel<8>, grid, threads, st, a, vec);
+  return launch_dependent(route_topk_wide_kernel, grid, threads, st, a);
 }
 
 }  // namespace moe_fp4

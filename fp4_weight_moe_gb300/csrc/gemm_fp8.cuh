@@ -23,10 +23,16 @@
 // The 128-row operand is X (kSwap = false) or W (kSwap = true: few tokens,
 // the tokens on the MMA's N side).
 //
-// What bounds a 128 x 256 tile (cycles per K block, measured): the MMAs alone
-// 512, its 48 KB through the SM's 64 bytes a cycle 750, the scale warps' sums
-// alone 270 (330 with their tensor-memory loads); with two accumulators in
-// flight the hand-overs between the three leave it at about 920.
+// What bounds a 128 x 256 tile, in cycles per K block, each measured alone:
+// the MMAs take 512; shared memory moves 128 bytes a cycle, and the MMAs read
+// 48 KB of it and the loads write as much: 768; the scale warps' sums take 270
+// (330 with their tensor-memory loads).  A block in flight takes about 170
+// from the freed accumulator to its MMAs' issue, 830 to their commit's arrival,
+// 400 until it is read out and 230 to be free again, and two are in flight:
+// about 820.  CTA pairs (cta_group::2, 256 x 256 tiles, 64 KB a block and SM)
+// shorten the second bound to 512, but their hand-overs cross SMs: measured
+// 118 us against 110 at M=4096 K=7168 N=4096, and no better with 192, 160 or
+// 128 columns and up to three accumulators.
 #pragma once
 
 #include "common.cuh"

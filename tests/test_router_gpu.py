@@ -115,6 +115,37 @@ def test_ties_and_signed_zeros():
     assert torch.allclose(w, torch.full_like(w, 1 / 16))
 
 
+@pytest.mark.parametrize("E", [100, 600, 1200])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_more_equals_than_the_list_holds(E, sigmoid):
+    """Forty equal scores at the edge of the choice, beside clear ones."""
+    m = _m()
+    g = torch.Generator().manual_seed(E)
+    logits = -1.0 - torch.rand(5, E, generator=g).double().mul(64).round().div(16).float()
+    at = torch.stack([torch.randperm(E, generator=g)[:44] for _ in range(5)])
+    logits.scatter_(1, at[:, :40], torch.full((5, 40), 2.0))
+    logits.scatter_(1, at[:, 40:], torch.tensor([3.0, 4.0, 5.0, 6.0]).repeat(5, 1))
+    check(m, logits, 16, sigmoid=sigmoid)
+
+
+@pytest.mark.parametrize("E", [70, 1100])
+def test_sigmoid_extremes(E):
+    """Scores down to subnormals and zero (logits to -200) order
+    as they are, infinite logits score 1."""
+    m = _m()
+    logits = torch.full((3, E), -200.0)  # 1 / inf: a score of 0, all equal
+    logits[0, 5:10] = torch.tensor([-100.0, -95.0, -90.0, -88.0, -86.0])
+    logits[1, 7] = float("inf")
+    logits[1, 3] = 0.0
+    logits[2, 11] = -80.0
+    ids, w = m.route_topk(logits.cuda(), 8, score=m.SCORE_SIGMOID, renormalize=False)
+    # exp(90) and above overflow FP32: their score is 0, ties to the lowest index
+    assert ids[0].tolist() == [9, 8, 0, 1, 2, 3, 4, 5]
+    assert ids[1].tolist() == [7, 3, 0, 1, 2, 4, 5, 6]
+    assert ids[2].tolist() == [11, 0, 1, 2, 3, 4, 5, 6]
+    assert w[1, :2].tolist() == [1.0, 0.5] and not w[1, 2:].any()
+
+
 def test_strided_logits_and_the_layer():
     """Rows with a stride; the ids and weights go into the layer as they are."""
     m = _m()

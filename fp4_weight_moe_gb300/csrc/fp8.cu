@@ -15,75 +15,124 @@ cudaError_t fp8_status_address(void** p) { return cudaGetSymbolAddress(p, g_fp8_
 // ---------------------------------------------------------------- quantiser
 // Per row and 128 columns: s = max|v| / 448 (1 where that is zero), q =
 // e4m3_rn(v / s), each step an IEEE FP32 operation; v is the input, or
-// act(gate) * up of a gated row [gate | up].  HBM bound: a warp takes up to
-// 1024 columns of a row, all its loads (of 16 bytes per lane) under way before
-// the first block's maximum.
+// act(gate) * up of a gated row [gate | up].  A warp takes 1024 columns of a
+// row, all its loads under way before the first block's maximum.
+//
+// Bound: @@
 
-// SiLU in full FP32 precision: the scale of a block follows its largest
-// product, and an element near the middle of two E4M3 values turns on it.
-__device__ __forceinline__ float gated_exact(float g, float u, const ActParams& act) {
-  if (act.kind == MOE_FP4_ACT_SILU) return g / (1.0f + expf(-g)) * u;
-  return gated_act(g, u, act);
+// SiLU(g) u in full FP32 precision (the scale of a block follows its largest
+// product, and an element near the middle of two E4M3 values turns on it), on
+// the V gates and ups of a lane.
+template <int V>
+__device__ __forceinline__ void silu_gated(const uint4 (&g_raw)[V / 8], const float (&up)[V], float (&v)[V]) {
+  // where the quotients are exact without a division: e^-g below 2^126, g
+  // finite; and not tiny, where 1 + e^-g can have a significand of ones (for
+  // a BF16 g with |g| >= 2^-19 such a divisor leaves the quotient as it is:
+  // g would have to be a power of two, and none of those has one)
+  __nv_bfloat162 least, most, size;
+#pragma unroll
+  for (int i = 0; i < V / 8; ++i) {
+    const uint32_t p[4] = {g_raw[i].x, g_raw[i].y, g_raw[i].z, g_raw[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&p[j]);
+      least = i + j ? __hmin2(least, b) : b;
+      most = i + j ? __hmax2(most, b) : b;
+      size = i + j ? __hmin2(size, __habs2(b)) : __habs2(b);
+    }
+  }
+  const float lo = fminf(__low2float(least), __high2float(least));
+  const float hi = fmaxf(__low2float(most), __high2float(most));
+  const float tiny = fminf(__low2float(size), __high2float(size));
+  if (lo > -80.f && hi < 0x1p100f && tiny >= 0x1p-19f) {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 g = make_float2(v[2 * i], v[2 * i + 1]);
+      const float2 e = make_float2(expf(-g.x), expf(-g.y));
+      const float2 x_neg = ffma2(e, both(-1.f), both(-1.f));
+      const float2 q = fmul2(quotients(g, x_neg, reciprocals(x_neg)), make_float2(up[2 * i], up[2 * i + 1]));
+      v[2 * i] = q.x;
+      v[2 * i + 1] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __fdiv_rn(v[i], 1.0f + expf(-v[i])) * up[i];
+  }
 }
 
-// kChunks chunks of 256 columns per warp
-template <bool kGated, int kChunks>
+// A lane takes V consecutive columns (8 or 16) of each of kChunks chunks.
+template <bool kGated, int V, int kChunks>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __restrict__ x, int64_t x_row, ActParams act,
                                                            uint8_t* __restrict__ q, int64_t q_row,
                                                            float* __restrict__ s, int64_t s_row, int64_t s_blk, int M,
                                                            int K) {
+  constexpr int kCols = 32 * V;
   pdl_wait();
   pdl_launch_dependents();
-  const unsigned groups = (unsigned)(K + 256 * kChunks - 1) / (256 * kChunks);
+  const unsigned groups = (unsigned)(K + kCols * kChunks - 1) / (kCols * kChunks);
   const unsigned task = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const unsigned m = task / groups;
   if (m >= (unsigned)M) return;
   const int lane = threadIdx.x & 31;
-  const int k0 = (int)(task % groups) * (256 * kChunks) + lane * 8;
+  const int k0 = (int)(task % groups) * (kCols * kChunks) + lane * V;
   const uint16_t* row = x + m * x_row;
-  uint4 raw[kChunks], raw_up[kChunks];
+  uint4 raw[kChunks][V / 8], raw_up[kChunks][V / 8];
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int k = k0 + i * 256;
-    raw[i] = raw_up[i] = make_uint4(0, 0, 0, 0);
-    if (k < K) {
-      raw[i] = *reinterpret_cast<const uint4*>(row + k);
-      if (kGated) raw_up[i] = *reinterpret_cast<const uint4*>(row + K + k);
+    const int k = k0 + i * kCols;  // (K % 16 == 0: a lane's columns are there or not)
+#pragma unroll
+    for (int j = 0; j < V / 8; ++j) {
+      raw[i][j] = raw_up[i][j] = make_uint4(0, 0, 0, 0);
+      if (k < K) {
+        raw[i][j] = *reinterpret_cast<const uint4*>(row + k + 8 * j);
+        if (kGated) raw_up[i][j] = *reinterpret_cast<const uint4*>(row + K + k + 8 * j);
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
-    const int k = k0 + i * 256;
-    if ((k & ~255) >= K) break;  // (the whole warp)
-    float v[8];
-    bf16x8_to_float(raw[i], v);
-    if (kGated) {
-      float up[8];
-      bf16x8_to_float(raw_up[i], up);
+    const int k = k0 + i * kCols;
+    float v[V];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = gated_exact(v[j], up[j], act);
+    for (int j = 0; j < V / 8; ++j) bf16x8_to_float(raw[i][j], v + 8 * j);
+    if (kGated) {
+      float up[V];
+#pragma unroll
+      for (int j = 0; j < V / 8; ++j) bf16x8_to_float(raw_up[i][j], up + 8 * j);
+      if (act.kind == MOE_FP4_ACT_SILU) {
+        silu_gated<V>(raw[i], up, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = gated_act(v[j], up[j], act);
+      }
     }
     const float sc = block_scale(block_amax(v));
     if (k < K) {
-      *reinterpret_cast<uint2*>(q + m * q_row + k) = e4m3_quotients(v, sc);
-      if ((lane & 15) == 0) s[m * s_row + (int64_t)(k / 128) * s_blk] = sc;
+      uint32_t w[V / 4];
+      e4m3_quotients(v, sc, w);
+      uint8_t* to = q + m * q_row + k;
+      if constexpr (V == 16)
+        *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      if (lane % (128 / V) == 0) s[m * s_row + (int64_t)(k / 128) * s_blk] = sc;
     }
   }
 }
 
-template <bool kGated, int kChunks>
+template <bool kGated, int V, int kChunks>
 static cudaError_t launch_quantize(const void* x, int64_t x_row, const ActParams& act, void* q, int64_t q_row, float* s,
                                    int64_t s_row, int64_t s_blk, int M, int K, unsigned warps, bool dependent,
                                    cudaStream_t st) {
-  // (tasks fit 32 bits: each stands for 256 values or a whole row in memory)
-  const int64_t tasks = (int64_t)M * ((K + 256 * kChunks - 1) / (256 * kChunks));
+  // (tasks fit 32 bits: each stands for 16 values or a whole row in memory)
+  const int64_t tasks = (int64_t)M * ((K + 32 * V * kChunks - 1) / (32 * V * kChunks));
   const unsigned grid = (unsigned)((tasks + warps - 1) / warps);
   const uint16_t* xp = static_cast<const uint16_t*>(x);
   uint8_t* qp = static_cast<uint8_t*>(q);
   if (dependent)
-    return launch_dependent(fp8_quantize_kernel<kGated, kChunks>, grid, 32 * warps, st, xp, x_row, act, qp, q_row, s,
+    return launch_dependent(fp8_quantize_kernel<kGated, V, kChunks>, grid, 32 * warps, st, xp, x_row, act, qp, q_row, s,
                             s_row, s_blk, M, K);
-  fp8_quantize_kernel<kGated, kChunks><<<grid, 32 * warps, 0, st>>>(xp, x_row, act, qp, q_row, s, s_row, s_blk, M, K);
+  fp8_quantize_kernel<kGated, V, kChunks><<<grid, 32 * warps, 0, st>>>(xp, x_row, act, qp, q_row, s, s_row, s_blk, M, K);
   return cudaGetLastError();
 }
 
@@ -97,10 +146,10 @@ cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* a
   // that a few rows spread over the GPU
   const bool few = (int64_t)M * ((K + 1023) / 1024) < 16 * sms;
   if (act && few)
-    return launch_quantize<true, 1>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
-  if (act) return launch_quantize<true, 4>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
-  if (few) return launch_quantize<false, 1>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
-  return launch_quantize<false, 4>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
+    return launch_quantize<true, 8, 1>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
+  if (act) return launch_quantize<true, 16, 2>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
+  if (few) return launch_quantize<false, 8, 1>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
+  return launch_quantize<false, 16, 2>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
 }
 
 // ------------------------------------------------------------------ product

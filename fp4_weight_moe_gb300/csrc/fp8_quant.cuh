@@ -1,14 +1,14 @@
 // FP8 (E4M3) activations with a scale per 128 columns: the pieces shared by
 // the quantiser, the product kernel that quantises its own tokens, and the
-// norm that hands its output on in FP8.  A block's 128 values lie eight per
-// lane on 16 consecutive lanes.
+// norm that hands its output on in FP8.  A block's 128 values lie V per lane
+// (8 or 16) on 128 / V consecutive lanes.
 #pragma once
 
 #include "common.cuh"
 
 namespace moe_fp4 {
 
-__device__ __forceinline__ void bf16x8_to_float(uint4 u, float (&v)[8]) {
+__device__ __forceinline__ void bf16x8_to_float(uint4 u, float* v) {
   const uint32_t p[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -17,53 +17,80 @@ __device__ __forceinline__ void bf16x8_to_float(uint4 u, float (&v)[8]) {
   }
 }
 
-// Largest magnitude of a block (16 lanes); NaNs are passed over.
-__device__ __forceinline__ float block_amax(const float (&v)[8]) {
+// Largest magnitude of a block; NaNs are passed over.
+template <int V>
+__device__ __forceinline__ float block_amax(const float (&v)[V]) {
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+  for (int i = 0; i < V; ++i) a = fmaxf(a, fabsf(v[i]));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = 64 / V; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
   return a;
+}
+
+// Quotients without branches, and two at a time, from a reciprocal y of the
+// divisor s: q = v y is within two units, and q + (v - q s) y, both steps
+// fused, is the correctly rounded quotient where y is the correctly rounded
+// reciprocal (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): three operations a value, where the
+// kernels here would spend more on divisions than on their memory traffic.
+// Away from FP32's ends only; a zero may lose its sign.
+__device__ __forceinline__ float2 quotients(float2 v, float2 s_neg, float2 y) {
+  const float2 t = fmul2(v, y);
+  return ffma2(ffma2(t, s_neg, v), y, t);
+}
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The reciprocals of -s_neg, 2^-126 < s < 2^126: two steps of y + y (1 - s y)
+// on the hardware's approximation.  The last one rounds correctly but where
+// s's significand is all ones (same source).
+__device__ __forceinline__ float2 reciprocals(float2 s_neg) {
+  float2 y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y.x) : "f"(-s_neg.x));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y.y) : "f"(-s_neg.y));
+  y = ffma2(y, ffma2(s_neg, y, both(1.f)), y);
+  return ffma2(y, ffma2(s_neg, y, both(1.f)), y);
 }
 
 // The block's scale: amax / 448, or 1 where that is zero (an all-zero block,
 // or one below FP32's reach).
 __device__ __forceinline__ float block_scale(float amax) {
+  if (amax > 0x1p-60f && amax < 0x1p60f) {
+    const float y = 1.f / 448.f, t = amax * y;
+    return fmaf(fmaf(t, -448.f, amax), y, t);
+  }
   const float s = __fdiv_rn(amax, 448.f);
   return s == 0.f ? 1.f : s;
 }
 
-// Eight E4M3 bytes of v / s, the quotients correctly rounded to FP32 before
-// they are rounded to E4M3 (to nearest even, saturating).  Away from FP32's
-// ends the quotients come from the correctly rounded reciprocal y of s: q =
-// v y is within two units, and q + (v - q s) y, both steps fused, is the
-// correctly rounded quotient (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990): three operations
-// a value, where the quantiser would spend more on divisions than on its
-// memory traffic.  Quotients too small for the exact remainder are far below
-// half of E4M3's least value and round to zero either way.
-__device__ __forceinline__ uint2 e4m3_quotients(const float (&v)[8], float s) {
-  float q[8];
-  if (s > 0x1p-60f && s < 0x1p60f) {
-    const float y = __frcp_rn(s);
+// E4M3 bytes of v / s, the quotients correctly rounded to FP32 before they
+// are rounded to E4M3 (to nearest even, saturating).  Quotients too small for
+// the exact remainder are far below half of E4M3's least value and round to
+// zero either way.
+template <int V>
+__device__ __forceinline__ void e4m3_quotients(const float (&v)[V], float s, uint32_t (&w)[V / 4]) {
+  float2 q[V / 2];
+  if (s > 0x1p-70f && s < 0x1p60f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu) {
+    const float2 y = both(reciprocals(both(-s)).x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = v[i] * y;
-      q[i] = fmaf(fmaf(-t, s, v[i]), y, t);
-    }
+    for (int i = 0; i < V / 2; ++i) q[i] = quotients(make_float2(v[2 * i], v[2 * i + 1]), both(-s), y);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], s);
+    for (int i = 0; i < V / 2; ++i) q[i] = make_float2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
   }
-  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < V / 4; ++i) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[4 * i + 1]), "f"(q[4 * i]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[4 * i + 3]), "f"(q[4 * i + 2]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(q[2 * i].y), "f"(q[2 * i].x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(q[2 * i + 1].y), "f"(q[2 * i + 1].x));
     w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
   }
+}
+
+__device__ __forceinline__ uint2 e4m3_quotients(const float (&v)[8], float s) {
+  uint32_t w[2];
+  e4m3_quotients(v, s, w);
   return make_uint2(w[0], w[1]);
 }
 

@@ -199,6 +199,45 @@ def test_quantize_gated(M, K, kind):
     assert ((got - v).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("rows", [1024, 65536])
+def test_quantize_silu_bits(rows):
+    """SiLU(g) * 1 of every BF16 g, alone in its row, through its scale: each
+    step an IEEE operation on the GPU's own expf. (1024 rows at a time and all
+    at once take the two forms of the kernel.)"""
+    m = _m()
+    g = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    x = torch.zeros(65536, 32, dtype=torch.bfloat16, device="cuda")
+    x[:, :16] = 2.0 ** -10
+    x[:, 5], x[:, 21] = g, 1.0
+    got = torch.cat([m.fp8_quantize(c, act=m.ACT_SILU)[1] for c in x.split(rows)])[:, 0]
+    f = g.float()
+    v = (f / (1.0 + torch.exp(-f))).abs()
+    want = torch.where(v.isnan(), torch.zeros_like(v), v)  # (NaNs are passed over)
+    want = want / torch.full_like(want, 448.0)
+    want = torch.where(want == 0, torch.ones_like(want), want)
+    assert torch.equal(got, want), (got != want).sum()
+
+
+def test_quantize_every_scale_significand():
+    """v / s with the scale of every BF16 maximum's significand, small and
+    large, and v at every 128th of the maximum."""
+    m = _m()
+    top = (torch.arange(128, dtype=torch.int32) + 128).float()  # every BF16 significand
+    lead = torch.tensor([2.0 ** e for e in (-58, -40, 0, 30, 50)])
+    amax = (top[:, None] * lead[None]).reshape(-1)
+    ratios = torch.arange(1, 129, dtype=torch.float32) / 128
+    x = torch.zeros(amax.numel(), 144)
+    x[:, :128] = amax[:, None] * ratios[None]
+    x = x.to(torch.bfloat16)
+    x[:, 127] = amax.to(torch.bfloat16)
+    want_q, want_s = quantised_32(x.float())
+    for rows in (x, x.repeat(8, 1)):  # (the two forms of the kernel)
+        q, s = m.fp8_quantize(rows.cuda())
+        for c in range(0, rows.shape[0], x.shape[0]):
+            assert torch.equal(s[c:c + x.shape[0]].cpu(), want_s)
+            assert torch.equal(q[c:c + x.shape[0]].cpu().view(torch.uint8), want_q)
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 2560, 300), (4, 272, 640), (16, 7168, 128), (17, 512, 1000), (150, 640, 257)])
 def test_linear_is_quantize_then_matmul(M, K, N):
     """The same bits as the two calls, with and without a workspace."""

@@ -16,35 +16,34 @@ cudaError_t fp8_status_address(void** p) { return cudaGetSymbolAddress(p, g_fp8_
 // Per row and 128 columns: s = max|v| / 448 (1 where that is zero), q =
 // e4m3_rn(v / s), each step an IEEE FP32 operation; v is the input, or
 // act(gate) * up of a gated row [gate | up].  A warp takes 1024 columns of a
-// row, all its loads under way before the first block's maximum.
+// row (512 of a gated one), all its loads under way before the first block's
+// maximum.  Sixteen columns a lane halve what is paid per lane and block (the
+// scale, its reciprocal, the shuffles) against eight: 16384 x 7168 51.5 us
+// against 61.8.
 //
-// Bound: @@
+// Bound: HBM (that size: 6.9 TB/s of a copy's 6.8; 4096 x 7168 14.8 us, 6.0
+// TB/s), with SiLU the instructions of its exact exponential, reciprocal and
+// quotients (16384 x 7168 122 us, 4.8 TB/s; with IEEE divisions 139); up to a
+// few hundred rows the launch (64 x 7168 1.7 us, with SiLU 2.1).
 
 // SiLU(g) u in full FP32 precision (the scale of a block follows its largest
 // product, and an element near the middle of two E4M3 values turns on it), on
 // the V gates and ups of a lane.
 template <int V>
 __device__ __forceinline__ void silu_gated(const uint4 (&g_raw)[V / 8], const float (&up)[V], float (&v)[V]) {
-  // where the quotients are exact without a division: e^-g below 2^126, g
-  // finite; and not tiny, where 1 + e^-g can have a significand of ones (for
-  // a BF16 g with |g| >= 2^-19 such a divisor leaves the quotient as it is:
-  // g would have to be a power of two, and none of those has one)
-  __nv_bfloat162 least, most, size;
+  // Without a division where 1 + e^-g is below 2^126 and g finite.  (A g below
+  // 2^-25 has the divisor 2 exactly, so no remainder is too small.)
+  __nv_bfloat162 most;
 #pragma unroll
   for (int i = 0; i < V / 8; ++i) {
     const uint32_t p[4] = {g_raw[i].x, g_raw[i].y, g_raw[i].z, g_raw[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&p[j]);
-      least = i + j ? __hmin2(least, b) : b;
+      const __nv_bfloat162 b = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&p[j]));
       most = i + j ? __hmax2(most, b) : b;
-      size = i + j ? __hmin2(size, __habs2(b)) : __habs2(b);
     }
   }
-  const float lo = fminf(__low2float(least), __high2float(least));
-  const float hi = fmaxf(__low2float(most), __high2float(most));
-  const float tiny = fminf(__low2float(size), __high2float(size));
-  if (lo > -80.f && hi < 0x1p100f && tiny >= 0x1p-19f) {
+  if (fmaxf(__low2float(most), __high2float(most)) < 80.f) {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       const float2 g = make_float2(v[2 * i], v[2 * i + 1]);
@@ -142,12 +141,13 @@ cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* a
   const cudaError_t e = current_device_sms(&sms);
   if (e != cudaSuccess) return e;
   const ActParams none = {MOE_FP4_ACT_SILU, 0.f, 0.f, 0.f};
-  // 1024 columns per warp where that gives every SM its warps, else 256, so
-  // that a few rows spread over the GPU
+  // 1024 columns per warp where that gives every SM its warps (with SiLU 512:
+  // 16384 x 7168 122 us against 128 with 1024 at fewer warps per SM), else
+  // 256, so that a few rows spread over the GPU
   const bool few = (int64_t)M * ((K + 1023) / 1024) < 16 * sms;
   if (act && few)
     return launch_quantize<true, 8, 1>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
-  if (act) return launch_quantize<true, 16, 2>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
+  if (act) return launch_quantize<true, 16, 1>(x, x_row, *act, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
   if (few) return launch_quantize<false, 8, 1>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 4, dependent, st);
   return launch_quantize<false, 16, 2>(x, x_row, none, q, q_row, s, s_row, s_blk, M, K, 8, dependent, st);
 }

@@ -42,14 +42,13 @@ __device__ __forceinline__ float2 quotients(float2 v, float2 s_neg, float2 y) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The reciprocals of -s_neg, 2^-126 < s < 2^126: two steps of y + y (1 - s y)
-// on the hardware's approximation.  The last one rounds correctly but where
-// s's significand is all ones (same source).
+// The reciprocals of -s_neg, 2^-126 < s < 2^126, correctly rounded: a step of
+// y + y (1 - s y) on the hardware's approximation, which is within a unit
+// (same source; compared with the IEEE reciprocal for all 2^23 significands).
 __device__ __forceinline__ float2 reciprocals(float2 s_neg) {
   float2 y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y.x) : "f"(-s_neg.x));
   asm("rcp.approx.f32 %0, %1;" : "=f"(y.y) : "f"(-s_neg.y));
-  y = ffma2(y, ffma2(s_neg, y, both(1.f)), y);
   return ffma2(y, ffma2(s_neg, y, both(1.f)), y);
 }
 
@@ -71,7 +70,7 @@ __device__ __forceinline__ float block_scale(float amax) {
 template <int V>
 __device__ __forceinline__ void e4m3_quotients(const float (&v)[V], float s, uint32_t (&w)[V / 4]) {
   float2 q[V / 2];
-  if (s > 0x1p-70f && s < 0x1p60f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu) {
+  if (s > 0x1p-70f && s < 0x1p60f) {
     const float2 y = both(reciprocals(both(-s)).x);
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) q[i] = quotients(make_float2(v[2 * i], v[2 * i + 1]), both(-s), y);

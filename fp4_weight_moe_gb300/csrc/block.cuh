@@ -51,9 +51,10 @@ struct NormArgs {
   float* s;
   int64_t s_row, s_blk;
   int M, H;
+  int layout, shift, shift_row, g_smem;  // launch_block_norm's choice
 };
-// `vec`: every row of every array starts 16-byte aligned and H % 8 == 0.
-cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStream_t st);
+// `packed`: every row of every array starts 16-byte aligned and H % 8 == 0.
+cudaError_t launch_block_norm(NormArgs a, int res_f32, bool packed, cudaStream_t st);
 
 struct RouteArgs {
   const void* logits;

@@ -131,6 +131,14 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
+__device__ __forceinline__ void cp_async_16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global)
+               : "memory");
+}
+
+// This thread's own copies have arrived and are visible to it.
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // a * b on two FP32 lanes at once.
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   float2 d;

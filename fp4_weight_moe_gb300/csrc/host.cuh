@@ -53,17 +53,24 @@ cudaError_t allow_smem(Kern kern, size_t bytes, bool (&seen)[64]) {
 // its own successor in only after that wait, so that no kernel ever runs
 // beside one two launches before it.
 template <class Kern, class... Args>
-cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned threads, cudaStream_t st, const Args&... args) {
+cudaError_t launch_dependent_smem(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                                  const Args&... args) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3(grid);
   c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
   c.stream = st;
   c.attrs = at;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, kern, args...);
+}
+
+template <class Kern, class... Args>
+cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned threads, cudaStream_t st, const Args&... args) {
+  return launch_dependent_smem(kern, grid, threads, 0, st, args...);
 }
 
 }  // namespace moe_fp4

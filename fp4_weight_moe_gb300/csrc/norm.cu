@@ -14,13 +14,42 @@
 
 namespace moe_fp4 {
 
-// A thread's eight columns of chunk i.  kVec (rows 16-byte aligned, H % 8 ==
-// 0): eight consecutive ones from 8 (threadIdx.x + i blockDim.x).  Otherwise
-// columns threadIdx.x + (8 i + j) blockDim.x, so that a warp's scalar
-// accesses are consecutive.  Columns past H read as zeros and are not stored.
-template <bool kVec>
-__device__ __forceinline__ int column(int i, int j) {
-  return kVec ? 8 * (threadIdx.x + i * blockDim.x) + j : (int)(threadIdx.x + (8 * i + j) * blockDim.x);
+// How a row's columns lie on its threads (a chunk: eight columns of each):
+//   kPacked   rows 16-byte aligned, H % 8 == 0: columns 8 (t + i T) .. + 7 of
+//             chunk i, in 16-byte accesses;
+//   kShifted  all rows' starts off a 16-byte boundary by the same `shift`
+//             elements (contiguous rows of an odd width): the same, `shift`
+//             columns earlier, so that accesses are aligned; the first and the
+//             last eight are accessed one by one;
+//   kSingle   the rest: columns t + (8 i + j) T, one by one, a warp's next to
+//             each other.
+// T threads to a row, t = 0 .. T - 1.  Columns outside the row read as zeros
+// and are not stored.
+enum Layout { kPacked, kShifted, kSingle };
+
+struct Place {
+  int t, T, shift, H;
+  template <Layout kL>
+  __device__ __forceinline__ int column(int i, int j) const {
+    return kL == kSingle ? t + (8 * i + j) * T : 8 * (t + i * T) + j - (kL == kShifted ? shift : 0);
+  }
+  __device__ __forceinline__ bool holds(int c) const { return (unsigned)c < (unsigned)H; }
+  // all eight of the chunk in the row
+  template <Layout kL>
+  __device__ __forceinline__ bool whole(int i) const {
+    if (kL == kSingle) return false;
+    const int c = column<kL>(i, 0);
+    return kL == kPacked ? c < H : c >= 0 && c + 8 <= H;
+  }
+};
+
+__device__ __forceinline__ uint4 ld_once(const void* p) {  // read once, not worth a line of L1
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p)
+               : "memory");
+  return u;
 }
 
 // Eight bf16 (kF32: f32) values of a row as loaded, packed.
@@ -31,31 +60,23 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < (kF32 ? 8 : 4); ++i) w[i] = 0;
   }
-  // kStream: read once, not worth a line of L1.
-  template <bool kVec, bool kStream>
-  __device__ __forceinline__ void load(const void* row, int i, int H) {
-    if (kVec) {
-      const int k = column<true>(i, 0);
-      if (k >= H) return;
-      const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + (int64_t)k * (kF32 ? 4 : 2));
+  __device__ __forceinline__ void put(int c, uint4 u) { w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w; }
+  // kVector: one of the weights, which start at a 16-byte boundary (if
+  // kPacked) whatever the rows' shift.
+  template <Layout kL, bool kVector>
+  __device__ __forceinline__ void load(const void* row, int i, const Place& p) {
+    if (p.whole<kL>(i) && (kL == kPacked || !kVector)) {
+      const char* q = static_cast<const char*>(row) + (int64_t)p.column<kL>(i, 0) * (kF32 ? 4 : 2);
 #pragma unroll
-      for (int c = 0; c < (kF32 ? 2 : 1); ++c) {
-        uint4 u;
-        if (kStream)
-          asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                       : "l"(q + c)
-                       : "memory");
-        else
-          u = q[c];
-        w[4 * c] = u.x, w[4 * c + 1] = u.y, w[4 * c + 2] = u.z, w[4 * c + 3] = u.w;
-      }
-    } else {
+      for (int c = 0; c < (kF32 ? 2 : 1); ++c)
+        put(c, kVector ? reinterpret_cast<const uint4*>(q)[c] : ld_once(q + 16 * c));
+    } else if (kL != kPacked) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int k = column<false>(i, j);
+        const int k = p.column<kL>(i, j);
         uint32_t u = 0;
-        if (k < H) u = kF32 ? static_cast<const uint32_t*>(row)[k] : (uint32_t) static_cast<const uint16_t*>(row)[k];
+        if (p.holds(k))
+          u = kF32 ? static_cast<const uint32_t*>(row)[k] : (uint32_t) static_cast<const uint16_t*>(row)[k];
         if (kF32)
           w[j] = u;
         else if (j % 2 == 0)
@@ -71,19 +92,19 @@ struct Raw8 {
   }
 };
 
-// The chunk's values of a vector or row of either type.
-template <bool kVec>
-__device__ __forceinline__ void load_pairs(const void* row, int f32, int i, int H, float2 (&v)[4]) {
+// The chunk's values of a weight or a row of either type.
+template <Layout kL, bool kVector>
+__device__ __forceinline__ void load_pairs(const void* row, int f32, int i, const Place& at, float2 (&v)[4]) {
   if (f32) {
     Raw8<true> r;
     r.zero();
-    r.template load<kVec, false>(row, i, H);
+    r.template load<kL, kVector>(row, i, at);
 #pragma unroll
     for (int p = 0; p < 4; ++p) v[p] = r.pair(p);
   } else {
     Raw8<false> r;
     r.zero();
-    r.template load<kVec, false>(row, i, H);
+    r.template load<kL, kVector>(row, i, at);
 #pragma unroll
     for (int p = 0; p < 4; ++p) v[p] = r.pair(p);
   }
@@ -94,11 +115,10 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float2 v) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kVec, bool kF32>
-__device__ __forceinline__ void store_pairs(void* row, int i, int H, const float2 (&v)[4]) {
-  if (kVec) {
-    const int k = column<true>(i, 0);
-    if (k >= H) return;
+template <Layout kL, bool kF32>
+__device__ __forceinline__ void store_pairs(void* row, int i, const Place& at, const float2 (&v)[4]) {
+  if (at.whole<kL>(i)) {
+    const int k = at.column<kL>(i, 0);
     if (kF32) {
       float4* q = reinterpret_cast<float4*>(static_cast<float*>(row) + k);
       q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
@@ -107,12 +127,12 @@ __device__ __forceinline__ void store_pairs(void* row, int i, int H, const float
       *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + k) =
           make_uint4(bf16x2_bits(v[0]), bf16x2_bits(v[1]), bf16x2_bits(v[2]), bf16x2_bits(v[3]));
     }
-  } else {
+  } else if (kL != kPacked) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int k = column<false>(i, j);
+      const int k = at.column<kL>(i, j);
       const float x = j % 2 ? v[j / 2].y : v[j / 2].x;
-      if (k < H) {
+      if (at.holds(k)) {
         if (kF32)
           static_cast<float*>(row)[k] = x;
         else
@@ -122,12 +142,13 @@ __device__ __forceinline__ void store_pairs(void* row, int i, int H, const float
   }
 }
 
-// Sum over the CTA; `part` has a slot per warp.
-__device__ __forceinline__ float block_sum(float v, float* part) {
+// Sum over a row's threads: the warp, or the CTA (`part` has a slot per warp).
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float* part) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
+  if (kWarp || warps == 1) return v;
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = (int)(threadIdx.x & 31) < warps ? part[threadIdx.x & 31] : 0.f;
@@ -142,15 +163,28 @@ __device__ __forceinline__ float scalar_of(const void* p, int f32, int64_t i) {
              : __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16);
 }
 
-// A CTA per row, kCh chunks of eight columns per thread; all of a row's loads
-// are under way before the first sum.
-template <int kCh, int kMaxThreads, bool kVec, bool kF32>
-__global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_constant__ NormArgs a) {
+// A CTA or (kWarp) a warp per row, kCh chunks of eight columns per thread; all
+// of a row's loads are under way before the first sum, those of a gate per
+// value (packed rows, a.g_smem) on their way into shared memory, a thread's
+// own values by itself.
+// (CTAs per SM: as many as the loads in flight need, a bound on the registers)
+constexpr int resident(int chunks, int threads, Layout layout, bool f32, bool warp) {
+  if (threads != 256 || layout == kSingle) return 1;
+  if (chunks == 4) return f32 ? 3 : 4;
+  return chunks == 2 ? (warp || f32 ? 4 : 5) : 6;
+}
+
+template <int kCh, int kMaxThreads, Layout kL, bool kF32, bool kWarp>
+__global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF32, kWarp)) block_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float part[2][32];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t m = blockIdx.x;
+  extern __shared__ uint4 gate_values[];  // [kCh][1 or 2 with f32][blockDim.x]
+  const int64_t m = kWarp ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  if (kWarp && m >= a.M) return;
   const int H = a.H;
+  const Place at = {kWarp ? (int)threadIdx.x & 31 : (int)threadIdx.x, kWarp ? 32 : (int)blockDim.x,
+                    kL == kShifted ? (a.shift + (int)(m & 7) * a.shift_row) & 7 : 0, H};
   const float inv_h = 1.0f / (float)H;
   Raw8<kF32> raw[kCh];
   Raw8<false> rawb[kCh];
@@ -160,8 +194,21 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
   for (int i = 0; i < kCh; ++i) {
     raw[i].zero();
     rawb[i].zero();
-    if (b) rawb[i].template load<kVec, true>(b, i, H);
-    raw[i].template load<kVec, true>(r, i, H);
+    if (b) rawb[i].template load<kL, false>(b, i, at);
+    raw[i].template load<kL, false>(r, i, at);
+  }
+  const char* gate = static_cast<const char*>(a.gate);
+  if (gate && a.g_col) gate += m * a.g_row * (a.g_f32 ? 4 : 2);
+  if (kL == kPacked && a.g_smem) {
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) {
+      const char* q = gate + (int64_t)at.column<kL>(i, 0) * (a.g_f32 ? 4 : 2);
+      uint4* to = gate_values + (a.g_f32 ? 2 * i : i) * blockDim.x + threadIdx.x;
+      if (at.whole<kL>(i)) {
+        cp_async_16(to, q);
+        if (a.g_f32) cp_async_16(to + blockDim.x, q + 16);
+      }
+    }
   }
   float2 v[kCh][4];  // r'
   if (b) {
@@ -175,11 +222,12 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
           const float2 z = rawb[i].pair(p);
           sum = ffma2(z, z, sum);
         }
-      factor *= rsqrtf(block_sum(sum.x + sum.y, part[0]) * inv_h + a.eps);
+      factor *= rsqrtf(row_sum<kWarp>(sum.x + sum.y, part[0]) * inv_h + a.eps);
     }
     if (a.gate && a.g_col == 0) factor *= scalar_of(a.gate, a.g_f32, m * a.g_row);
     const float2 f = make_float2(factor, factor);
     const float2 of = make_float2(a.offset * factor, a.offset * factor);
+    if (kL == kPacked && a.g_smem) cp_async_wait_all();
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
       float2 t[4];  // factor * (offset + w_post) * gate
@@ -187,13 +235,29 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
       for (int p = 0; p < 4; ++p) t[p] = f;
       if (a.w_post) {
         float2 w[4];
-        load_pairs<kVec>(a.w_post, a.w_f32, i, H, w);
+        load_pairs<kL, true>(a.w_post, a.w_f32, i, at, w);
 #pragma unroll
         for (int p = 0; p < 4; ++p) t[p] = ffma2(w[p], f, of);
       }
       if (a.gate && a.g_col) {
         float2 g[4];
-        load_pairs<kVec>(static_cast<const char*>(a.gate) + m * a.g_row * (a.g_f32 ? 4 : 2), a.g_f32, i, H, g);
+        if (kL == kPacked && a.g_smem) {
+          const uint4* from = gate_values + (a.g_f32 ? 2 * i : i) * blockDim.x + threadIdx.x;
+          Raw8<true> u;  // (zeros outside the row: what lies in memory there may be NaN)
+          u.zero();
+          if (at.whole<kL>(i)) {
+            u.put(0, from[0]);
+            if (a.g_f32) u.put(1, from[blockDim.x]);
+          }
+          Raw8<false> h;
+          h.put(0, make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]));
+#pragma unroll
+          for (int p = 0; p < 4; ++p) g[p] = a.g_f32 ? u.pair(p) : h.pair(p);
+        } else if (a.g_row == 0 && kL == kShifted) {  // one gate for all rows, which does not shift with them
+          load_pairs<kL, true>(gate, a.g_f32, i, at, g);
+        } else {
+          load_pairs<kL, false>(gate, a.g_f32, i, at, g);
+        }
 #pragma unroll
         for (int p = 0; p < 4; ++p) t[p] = fmul2(t[p], g[p]);
       }
@@ -209,7 +273,7 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
   if (a.r_out) {
     void* row = static_cast<char*>(a.r_out) + m * a.ro_row * (kF32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < kCh; ++i) store_pairs<kVec, kF32>(row, i, H, v[i]);
+    for (int i = 0; i < kCh; ++i) store_pairs<kL, kF32>(row, i, at, v[i]);
   }
   if (!a.w_pre) return;
   float2 sum = make_float2(0.f, 0.f);
@@ -217,19 +281,19 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
   for (int i = 0; i < kCh; ++i)
 #pragma unroll
     for (int p = 0; p < 4; ++p) sum = ffma2(v[i][p], v[i][p], sum);  // (columns past H are zeros)
-  const float inv = rsqrtf(block_sum(sum.x + sum.y, part[1]) * inv_h + a.eps);
+  const float inv = rsqrtf(row_sum<kWarp>(sum.x + sum.y, part[1]) * inv_h + a.eps);
   const float2 f = make_float2(inv, inv), of = make_float2(a.offset * inv, a.offset * inv);
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
     float2 w[4];
-    load_pairs<kVec>(a.w_pre, a.w_f32, i, H, w);
+    load_pairs<kL, true>(a.w_pre, a.w_f32, i, at, w);
 #pragma unroll
     for (int p = 0; p < 4; ++p) v[i][p] = fmul2(v[i][p], ffma2(w[p], f, of));
-    if (a.n) store_pairs<kVec, false>(a.n + m * a.n_row, i, H, v[i]);
-    if (kVec && a.q) {
+    if (a.n) store_pairs<kL, false>(a.n + m * a.n_row, i, at, v[i]);
+    if (kL == kPacked && a.q) {
       // the BF16 values' FP8 form, so that it is the one a quantiser of n
       // gives; 16 lanes hold a block of 128 columns
-      const int k = column<true>(i, 0);
+      const int k = at.column<kL>(i, 0);
       float x[8];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
@@ -240,28 +304,66 @@ __global__ void __launch_bounds__(kMaxThreads) block_norm_kernel(const __grid_co
       const float sc = block_scale(block_amax(x));
       if (k < H) {
         *reinterpret_cast<uint2*>(a.q + m * a.q_row + k) = e4m3_quotients(x, sc);
-        if ((threadIdx.x & 15) == 0) a.s[m * a.s_row + (int64_t)(k / 128) * a.s_blk] = sc;
+        if ((at.t & 15) == 0) a.s[m * a.s_row + (int64_t)(k / 128) * a.s_blk] = sc;
       }
     }
   }
 }
 
-template <int kCh, int kMaxThreads>
-static cudaError_t launch_ch(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {
-  const unsigned threads = (unsigned)((a.H + 256 * kCh - 1) / (256 * kCh)) * 32;
-  auto* kern = vec ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, true, true>
-                              : block_norm_kernel<kCh, kMaxThreads, true, false>)
-                   : (res_f32 ? block_norm_kernel<kCh, kMaxThreads, false, true>
-                              : block_norm_kernel<kCh, kMaxThreads, false, false>);
-  return launch_dependent(kern, (unsigned)a.M, threads, st, a);
+template <int kCh, int kMaxThreads, bool kWarp>
+static cudaError_t launch_ch(NormArgs a, int res_f32, cudaStream_t st) {
+  const int columns = a.H + (a.layout == kShifted ? 7 : 0);
+  const unsigned threads = kWarp ? kMaxThreads : (unsigned)((columns + 256 * kCh - 1) / (256 * kCh)) * 32;
+  const unsigned grid = kWarp ? (unsigned)(((int64_t)a.M + kMaxThreads / 32 - 1) / (kMaxThreads / 32)) : (unsigned)a.M;
+  size_t smem = 0;
+  if (a.layout == kPacked && a.gate && a.g_col && a.g_row) {
+    smem = (size_t)threads * kCh * (a.g_f32 ? 32 : 16);
+    if (smem > 40 * 1024) smem = 0;  // (a row of that many columns hides its own waits)
+  }
+  a.g_smem = smem != 0;
+  auto* kern = a.layout == kPacked ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, kPacked, true, kWarp>
+                                              : block_norm_kernel<kCh, kMaxThreads, kPacked, false, kWarp>)
+               : a.layout == kShifted ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, kShifted, true, kWarp>
+                                                 : block_norm_kernel<kCh, kMaxThreads, kShifted, false, kWarp>)
+                                      : (res_f32 ? block_norm_kernel<kCh, kMaxThreads, kSingle, true, kWarp>
+                                                 : block_norm_kernel<kCh, kMaxThreads, kSingle, false, kWarp>);
+  return launch_dependent_smem(kern, grid, threads, smem, st, a);
 }
 
-cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStream_t st) {
+// kShifted where every array that is read or written by rows is off a 16-byte
+// boundary by the same elements in every row (of 32-bit types: modulo four).
+// An array with a single row for all tokens would not shift with the others.
+static bool same_shift(const NormArgs& a, int res_f32, int* shift, int* shift_row) {
+  int modulo = 0;  // of the values seen so far: 4, later 8
+  *shift = *shift_row = 0;
+  bool same = true;
+  auto see = [&](const void* p, int64_t row, int f32) {
+    if (!p) return;
+    const int mod = f32 ? 4 : 8, bytes = f32 ? 4 : 2;
+    const int s = (int)((uintptr_t)p / bytes % mod), r = (int)(row % mod);
+    const int low = modulo && modulo < mod ? modulo : mod;
+    same = same && (!modulo || (s % low == *shift % low && r % low == *shift_row % low));
+    if (mod > modulo) modulo = mod, *shift = s, *shift_row = r;
+  };
+  see(a.r, a.r_row, res_f32);
+  see(a.r_out, a.ro_row, res_f32);
+  see(a.b, a.b_row, 0);
+  see(a.n, a.n_row, 0);
+  if (a.gate && a.g_col && a.g_row) see(a.gate, a.g_row, a.g_f32);
+  return same && a.H + 7 <= 32768;  // (the threads hold 32768 columns)
+}
+
+cudaError_t launch_block_norm(NormArgs a, int res_f32, bool packed, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = current_device_sms(&sms);
   if (e != cudaSuccess) return e;
-  if (a.H > 16384) return launch_ch<4, 1024>(a, res_f32, vec, st);
-  if (a.H > 8192) return launch_ch<4, 512>(a, res_f32, vec, st);
+  a.layout = packed ? kPacked : same_shift(a, res_f32, &a.shift, &a.shift_row) ? kShifted : kSingle;
+  const bool many = a.M > 2 * sms;
+  const int columns = a.H + (a.layout == kShifted ? 7 : 0);
+  if (columns > 16384) return launch_ch<4, 1024, false>(a, res_f32, st);
+  if (columns > 8192) return launch_ch<4, 512, false>(a, res_f32, st);
+  if (many && columns <= 256) return launch_ch<1, 256, true>(a, res_f32, st);
+  if (many && columns <= 512) return launch_ch<2, 256, true>(a, res_f32, st);
   // Chunks per thread: one while a row per CTA leaves SMs with one or two
   // rows (latency) and where a row is short or read by scalar loads; beyond,
   // as many as keep a CTA at 256 threads, so that more rows share an SM and
@@ -270,9 +372,9 @@ cudaError_t launch_block_norm(const NormArgs& a, int res_f32, bool vec, cudaStre
   // M=16384 151 / - / 138; H=4096 M=64 2.3 / 2.6 / 3.3, M=16384 81.4 / 80.0 /
   // 80.7; f32 residual with that norm, M=16384: H=7168 365 / - / 221, H=4096
   // 133 / 126 / 129, H=2560 85 / 77 / 81.
-  if (!vec || a.H <= 2048 || a.M <= 2 * sms) return launch_ch<1, 1024>(a, res_f32, vec, st);
-  if (a.H <= 4096) return launch_ch<2, 256>(a, res_f32, vec, st);
-  return launch_ch<4, 256>(a, res_f32, vec, st);
+  if (a.layout == kSingle || columns <= 2048 || !many) return launch_ch<1, 1024, false>(a, res_f32, st);
+  if (columns <= 4096) return launch_ch<2, 256, false>(a, res_f32, st);
+  return launch_ch<4, 256, false>(a, res_f32, st);
 }
 
 }  // namespace moe_fp4

@@ -51,7 +51,7 @@ struct NormArgs {
   float* s;
   int64_t s_row, s_blk;
   int M, H;
-  int layout, shift, shift_row, g_smem;  // launch_block_norm's choice
+  int layout, shift, shift_row, staged;  // launch_block_norm's choice
 };
 // `packed`: every row of every array starts 16-byte aligned and H % 8 == 0.
 cudaError_t launch_block_norm(NormArgs a, int res_f32, bool packed, cudaStream_t st);

@@ -3,11 +3,19 @@
 //   z  = b * rsqrt(mean(b^2) + eps) * (o + w_post)   (z = b without w_post)
 //   r' = r + scale * gate * z
 //   n  = r' * rsqrt(mean(r'^2) + eps) * (o + w_pre)
-// and n's FP8 form (a scale per 128 columns), in one launch.  HBM bound: a
-// CTA holds a row in registers, so b and r are read and r' and n written
-// once; two block sums (of b^2, then of r'^2) are all that separates them.
-// Sums, r' and the norms are FP32; r' enters the second norm before it is
-// rounded to the residual stream's type.
+// and n's FP8 form (a scale per 128 columns), in one launch.  A CTA (a warp)
+// holds a row in registers, so b and r are read and r' and n written once; two
+// sums over the row (of b^2, then of r'^2) are all that separates them.  Sums,
+// r' and the norms are FP32; r' enters the second norm before it is rounded to
+// the residual stream's type.
+//
+// Bound: HBM where rows are many and their starts alike (16384 x 7168, bf16
+// residual, no norm after the block: 136 us, 6.9 TB/s of a copy's 6.8; f32
+// residual, both norms, a gate per value: 244 us, 6.7; 4096 x 4096, both
+// norms: 24 us, 5.6).  Odd widths pay for the weights, which do not shift with
+// the rows and are read one by one (9000 x 5005, bf16: 70 us, 5.1 TB/s; with
+// all rows read one by one 180).  Up to a few hundred rows the launch and the
+// chain of two sums (64 x 7168, f32, both norms: 3.7 us; one row of 2560 2.0).
 #include "block.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"
@@ -157,6 +165,38 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// Weights or a gate on their way to a thread's own slots, slot[c T]: one a
+// chunk, two of 32-bit values.
+enum { kStageGate = 1, kStagePost = 2, kStagePre = 4 };
+
+template <int kCh>
+__device__ __host__ constexpr int staged_slots(int f32) { return f32 ? 2 * kCh : kCh; }
+
+template <int kCh>
+__device__ __forceinline__ void stage_row(uint4* slot, const void* row, int f32, const Place& at) {
+#pragma unroll
+  for (int i = 0; i < kCh; ++i) {
+    const char* q = static_cast<const char*>(row) + (int64_t)at.column<kPacked>(i, 0) * (f32 ? 4 : 2);
+    if (at.whole<kPacked>(i)) {
+      cp_async_16(slot + (f32 ? 2 * i : i) * blockDim.x, q);
+      if (f32) cp_async_16(slot + (2 * i + 1) * blockDim.x, q + 16);
+    }
+  }
+}
+
+__device__ __forceinline__ void staged_pairs(const uint4* slot, int f32, int i, const Place& at, float2 (&v)[4]) {
+  Raw8<true> u;  // (zeros outside the row: what lies in memory there may be NaN)
+  u.zero();
+  if (at.whole<kPacked>(i)) {
+    u.put(0, slot[(f32 ? 2 * i : i) * blockDim.x]);
+    if (f32) u.put(1, slot[(2 * i + 1) * blockDim.x]);
+  }
+  Raw8<false> h;
+  h.put(0, make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]));
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = f32 ? u.pair(p) : h.pair(p);
+}
+
 // Value `m` of a gate or the like, of either type.
 __device__ __forceinline__ float scalar_of(const void* p, int f32, int64_t i) {
   return f32 ? static_cast<const float*>(p)[i]
@@ -164,9 +204,9 @@ __device__ __forceinline__ float scalar_of(const void* p, int f32, int64_t i) {
 }
 
 // A CTA or (kWarp) a warp per row, kCh chunks of eight columns per thread; all
-// of a row's loads are under way before the first sum, those of a gate per
-// value (packed rows, a.g_smem) on their way into shared memory, a thread's
-// own values by itself.
+// of a row's loads are under way before the first sum, those of weights and of
+// a gate per value (packed rows, a.staged) on their way into shared memory, a
+// thread's own values by itself.
 // (CTAs per SM: as many as the loads in flight need, a bound on the registers)
 constexpr int resident(int chunks, int threads, Layout layout, bool f32, bool warp) {
   if (threads != 256 || layout == kSingle) return 1;
@@ -179,7 +219,7 @@ __global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF
   __shared__ float part[2][32];
   pdl_wait();
   pdl_launch_dependents();
-  extern __shared__ uint4 gate_values[];  // [kCh][1 or 2 with f32][blockDim.x]
+  extern __shared__ uint4 stage[];
   const int64_t m = kWarp ? (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   if (kWarp && m >= a.M) return;
   const int H = a.H;
@@ -198,21 +238,24 @@ __global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF
     raw[i].template load<kL, false>(r, i, at);
   }
   const char* gate = static_cast<const char*>(a.gate);
-  if (gate && a.g_col) gate += m * a.g_row * (a.g_f32 ? 4 : 2);
-  if (kL == kPacked && a.g_smem) {
-#pragma unroll
-    for (int i = 0; i < kCh; ++i) {
-      const char* q = gate + (int64_t)at.column<kL>(i, 0) * (a.g_f32 ? 4 : 2);
-      uint4* to = gate_values + (a.g_f32 ? 2 * i : i) * blockDim.x + threadIdx.x;
-      if (at.whole<kL>(i)) {
-        cp_async_16(to, q);
-        if (a.g_f32) cp_async_16(to + blockDim.x, q + 16);
-      }
-    }
+  float factor = a.scale;  // what the row's values of z share
+  if (gate && a.g_col)
+    gate += m * a.g_row * (a.g_f32 ? 4 : 2);
+  else if (gate)
+    factor *= scalar_of(gate, a.g_f32, m * a.g_row);
+  const int staged = kL == kPacked ? a.staged : 0;
+  uint4* const s_gate = stage + threadIdx.x;
+  uint4* const s_post = s_gate + (staged & kStageGate ? staged_slots<kCh>(a.g_f32) * blockDim.x : 0);
+  uint4* const s_pre = s_post + (staged & kStagePost ? staged_slots<kCh>(a.w_f32) * blockDim.x : 0);
+  if (staged) {
+    if (staged & kStageGate) stage_row<kCh>(s_gate, gate, a.g_f32, at);
+    if (staged & kStagePost) stage_row<kCh>(s_post, a.w_post, a.w_f32, at);
+    cp_async_commit();
+    if (staged & kStagePre) stage_row<kCh>(s_pre, a.w_pre, a.w_f32, at);
+    cp_async_commit();
   }
   float2 v[kCh][4];  // r'
   if (b) {
-    float factor = a.scale;  // what the row's values of z share
     if (a.w_post) {
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -224,10 +267,9 @@ __global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF
         }
       factor *= rsqrtf(row_sum<kWarp>(sum.x + sum.y, part[0]) * inv_h + a.eps);
     }
-    if (a.gate && a.g_col == 0) factor *= scalar_of(a.gate, a.g_f32, m * a.g_row);
     const float2 f = make_float2(factor, factor);
     const float2 of = make_float2(a.offset * factor, a.offset * factor);
-    if (kL == kPacked && a.g_smem) cp_async_wait_all();
+    if (staged) cp_async_wait<1>();
 #pragma unroll
     for (int i = 0; i < kCh; ++i) {
       float2 t[4];  // factor * (offset + w_post) * gate
@@ -235,24 +277,17 @@ __global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF
       for (int p = 0; p < 4; ++p) t[p] = f;
       if (a.w_post) {
         float2 w[4];
-        load_pairs<kL, true>(a.w_post, a.w_f32, i, at, w);
+        if (staged & kStagePost)
+          staged_pairs(s_post, a.w_f32, i, at, w);
+        else
+          load_pairs<kL, true>(a.w_post, a.w_f32, i, at, w);
 #pragma unroll
         for (int p = 0; p < 4; ++p) t[p] = ffma2(w[p], f, of);
       }
       if (a.gate && a.g_col) {
         float2 g[4];
-        if (kL == kPacked && a.g_smem) {
-          const uint4* from = gate_values + (a.g_f32 ? 2 * i : i) * blockDim.x + threadIdx.x;
-          Raw8<true> u;  // (zeros outside the row: what lies in memory there may be NaN)
-          u.zero();
-          if (at.whole<kL>(i)) {
-            u.put(0, from[0]);
-            if (a.g_f32) u.put(1, from[blockDim.x]);
-          }
-          Raw8<false> h;
-          h.put(0, make_uint4(u.w[0], u.w[1], u.w[2], u.w[3]));
-#pragma unroll
-          for (int p = 0; p < 4; ++p) g[p] = a.g_f32 ? u.pair(p) : h.pair(p);
+        if (staged & kStageGate) {
+          staged_pairs(s_gate, a.g_f32, i, at, g);
         } else if (a.g_row == 0 && kL == kShifted) {  // one gate for all rows, which does not shift with them
           load_pairs<kL, true>(gate, a.g_f32, i, at, g);
         } else {
@@ -283,10 +318,14 @@ __global__ void __launch_bounds__(kMaxThreads, resident(kCh, kMaxThreads, kL, kF
     for (int p = 0; p < 4; ++p) sum = ffma2(v[i][p], v[i][p], sum);  // (columns past H are zeros)
   const float inv = rsqrtf(row_sum<kWarp>(sum.x + sum.y, part[1]) * inv_h + a.eps);
   const float2 f = make_float2(inv, inv), of = make_float2(a.offset * inv, a.offset * inv);
+  if (staged) cp_async_wait<0>();
 #pragma unroll
   for (int i = 0; i < kCh; ++i) {
     float2 w[4];
-    load_pairs<kL, true>(a.w_pre, a.w_f32, i, at, w);
+    if (staged & kStagePre)
+      staged_pairs(s_pre, a.w_f32, i, at, w);
+    else
+      load_pairs<kL, true>(a.w_pre, a.w_f32, i, at, w);
 #pragma unroll
     for (int p = 0; p < 4; ++p) v[i][p] = fmul2(v[i][p], ffma2(w[p], f, of));
     if (a.n) store_pairs<kL, false>(a.n + m * a.n_row, i, at, v[i]);
@@ -315,12 +354,21 @@ static cudaError_t launch_ch(NormArgs a, int res_f32, cudaStream_t st) {
   const int columns = a.H + (a.layout == kShifted ? 7 : 0);
   const unsigned threads = kWarp ? kMaxThreads : (unsigned)((columns + 256 * kCh - 1) / (256 * kCh)) * 32;
   const unsigned grid = kWarp ? (unsigned)(((int64_t)a.M + kMaxThreads / 32 - 1) / (kMaxThreads / 32)) : (unsigned)a.M;
+  // Staged while 48 KB hold it (what a launch gets unasked), the gate first,
+  // whose values come from memory; not the weights of a warp's row, which the
+  // CTA's other rows leave in L1 (16384 x 264 8.2 us, staged 10.2; a row per
+  // CTA: 9000 x 5120, f32, a gate per value 125 us, staged 98).
   size_t smem = 0;
-  if (a.layout == kPacked && a.gate && a.g_col && a.g_row) {
-    smem = (size_t)threads * kCh * (a.g_f32 ? 32 : 16);
-    if (smem > 40 * 1024) smem = 0;  // (a row of that many columns hides its own waits)
+  a.staged = 0;
+  auto stage = [&](int what, int f32) {
+    const size_t more = (size_t)staged_slots<kCh>(f32) * threads * 16;
+    if (smem + more <= 47 * 1024) smem += more, a.staged |= what;
+  };
+  if (a.layout == kPacked) {
+    if (a.gate && a.g_col) stage(kStageGate, a.g_f32);
+    if (!kWarp && a.w_post) stage(kStagePost, a.w_f32);
+    if (!kWarp && a.w_pre) stage(kStagePre, a.w_f32);
   }
-  a.g_smem = smem != 0;
   auto* kern = a.layout == kPacked ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, kPacked, true, kWarp>
                                               : block_norm_kernel<kCh, kMaxThreads, kPacked, false, kWarp>)
                : a.layout == kShifted ? (res_f32 ? block_norm_kernel<kCh, kMaxThreads, kShifted, true, kWarp>
@@ -362,6 +410,9 @@ cudaError_t launch_block_norm(NormArgs a, int res_f32, bool packed, cudaStream_t
   const int columns = a.H + (a.layout == kShifted ? 7 : 0);
   if (columns > 16384) return launch_ch<4, 1024, false>(a, res_f32, st);
   if (columns > 8192) return launch_ch<4, 512, false>(a, res_f32, st);
+  // A warp per row while two chunks of eight a lane hold it: no barrier, and
+  // short rows leave no threads idle (16384 x 264 17.5 us with a CTA per row,
+  // 8.3; with four chunks 16384 x 1024, f32, a gate per value: 37.9, 55.8).
   if (many && columns <= 256) return launch_ch<1, 256, true>(a, res_f32, st);
   if (many && columns <= 512) return launch_ch<2, 256, true>(a, res_f32, st);
   // Chunks per thread: one while a row per CTA leaves SMs with one or two

@@ -81,6 +81,49 @@ def test_sandwich(M, H, res, gate):
     check(got_n, n, dn, "normed")
 
 
+@pytest.mark.parametrize("M,H", [(333, 1), (333, 200), (333, 256), (334, 264), (1000, 505), (335, 506), (333, 512),
+                                 (333, 513), (333, 2000), (333, 2042), (333, 4097), (333, 5005), (333, 5120),
+                                 (310, 8191), (310, 8192), (2, 32761), (2, 32767)])
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+def test_many_rows(M, H, res, gate):
+    """Enough rows for every arrangement of rows on warps and CTAs, packed and
+    odd ones."""
+    m = _m()
+    r, b, pre, post, g = inputs(M, H, res, gate, M + H)
+    if gate == "full" and H % 3 == 0:
+        g = g.float()
+    rr, dr, n, dn = want_64(r, pre, b, post, g, 0.7, 1e-6, 0.0)
+    got_r, got_n = m.block_norm(r.cuda(), pre.cuda(), b.cuda(), post_weight=post.cuda(), gate=cu(g), scale=0.7)
+    check(got_r, rr, dr, "residual")
+    check(got_n, n, dn, "normed")
+
+
+@pytest.mark.parametrize("M,H", [(5, 83), (400, 83), (400, 700), (400, 2100), (320, 4500)])
+@pytest.mark.parametrize("res", [BF16, F32])
+@pytest.mark.parametrize("at", [(0, 0, 0, 0), (3, 3, 3, 3), (4, 4, 4, 4), (7, 7, 7, 7), (5, 1, 5, 1), (1, 2, 3, 4)])
+def test_rows_off_a_boundary(M, H, res, at):
+    """Residual, block output, gate and output at columns `at` of wider
+    buffers: off a 16-byte boundary alike, alike modulo four (enough for FP32
+    rows beside BF16 ones, not for two BF16 ones), and each its own way. What
+    lies around the rows stays."""
+    m = _m()
+    r, b, pre, post, g = inputs(M, H, res, "full", H)
+    rr, dr, n, dn = want_64(r, pre, b, post, g, 0.7, 1e-6, 0.0)
+
+    def wide(t, k):
+        big = torch.full((M, H + 13), float("nan"), dtype=t.dtype, device="cuda")
+        big[:, k:k + H] = t.cuda()
+        return big[:, k:k + H]
+
+    out = torch.full((M, H + 13), -7.0, dtype=res, device="cuda")
+    got_r, got_n = m.block_norm(wide(r, at[0]), pre.cuda(), wide(b, at[1]), post_weight=post.cuda(),
+                                gate=wide(g, at[2]), scale=0.7, residual_out=out[:, at[3]:at[3] + H])
+    check(got_r, rr, dr, "residual")
+    check(got_n, n, dn, "normed")
+    assert (out[:, :at[3]] == -7).all() and (out[:, at[3] + H:] == -7).all()
+
+
 @pytest.mark.parametrize("H", [256, 1000, 77])
 def test_parts(H):
     """Each part left out; weights as FP32 differences from one; FP32 gates."""

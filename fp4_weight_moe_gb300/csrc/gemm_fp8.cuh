@@ -99,10 +99,15 @@ struct F8Cfg {
   static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
   static constexpr uint32_t kBarBytes = 256;
   static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes - kXqBytes;
-  static constexpr int kStages = kBudget / kStageBytes > 12 ? 12 : (int)(kBudget / kStageBytes);
+  // A multiple of the MMA warps, so that a stage's rounds are all one warp's: a
+  // wait for a round's parity is also met two rounds earlier, and only a warp
+  // that has waited for the round between cannot be early.
+  static constexpr int kFit = kBudget / kStageBytes > 12 ? 12 : (int)(kBudget / kStageBytes);
+  static constexpr int kStages = kFit / kMmaWarps * kMmaWarps;
   static constexpr uint32_t kSmem = kStages * kStageBytes + kXqBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
-  static_assert(kStages >= 3 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
+  static_assert(kAcc % kMmaWarps == 0, "an accumulator's uses, too, are one warp's");
+  static_assert(kStages >= 4 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
   static_assert(!kTwo || kTmemCols <= 256, "tensor memory of two CTAs");
   // a split tile's partial sums lie in the ring: [BN][128] tokens by columns
   // (kSwap) or [128][BN + 4] (padded, so that lanes writing their own rows

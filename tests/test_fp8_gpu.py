@@ -80,6 +80,41 @@ def test_matmul(M, K, N, out):
     assert m.fp8_status() == 0
 
 
+@pytest.mark.parametrize("M", [1, 8, 16, 24, 32, 64, 128])
+def test_long_k_per_cta(M):
+    """Sixteen K blocks and more to a CTA, so that every form's ring of stages
+    goes round several times, many calls in a row; the self-quantising form
+    (up to eight tokens) gives the bits of the two calls."""
+    m = _m()
+    K, N = 16384, 384
+    wq, ws = rand_fp8(N, K, 2), rand_scale(blocks(N), blocks(K), 4)
+    g = torch.Generator().manual_seed(M)
+    x = torch.randn(M, K, generator=g).to(torch.bfloat16).cuda()
+    q, s = m.fp8_quantize(x)
+    want, mag = product_64(q.cpu(), s.cpu(), wq, ws)
+    W, WS = wq.cuda(), ws.cuda()
+    first = m.fp8_matmul(q, s, W, WS, out_dtype=torch.float32)
+    check(first, want, mag, K, torch.float32)
+    for _ in range(20):
+        assert torch.equal(m.fp8_matmul(q, s, W, WS, out_dtype=torch.float32), first)
+        assert torch.equal(m.fp8_linear(x, W, WS, out_dtype=torch.float32), first)
+    assert m.fp8_status() == 0
+
+
+@pytest.mark.parametrize("M,K,N", [(24, 7168, 7168), (17, 5120, 5000), (30, 2048, 20000)])
+def test_many_tiles_few_tokens(M, K, N):
+    m = _m()
+    xq, wq = rand_fp8(M, K, 1), rand_fp8(N, K, 2)
+    xs, ws = rand_scale(M, blocks(K), 3), rand_scale(blocks(N), blocks(K), 4)
+    want, mag = product_64(xq, xs, wq, ws)
+    args = xq.cuda(), xs.cuda(), wq.cuda(), ws.cuda()
+    first = m.fp8_matmul(*args)
+    check(first, want, mag, K, torch.bfloat16)
+    for _ in range(20):
+        assert torch.equal(m.fp8_matmul(*args), first)
+    assert m.fp8_status() == 0
+
+
 @pytest.mark.parametrize("M,K,N", [(1, 7168, 512), (5, 272, 129), (40, 512, 384), (300, 640, 500)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
 def test_matmul_addend_and_strides(M, K, N, out):

@@ -153,11 +153,11 @@ cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* a
 }
 
 // ------------------------------------------------------------------ product
-template <int BN, bool kSwap>
-__global__ void __launch_bounds__(F8Cfg<BN, kSwap>::kThreads, 1)
+template <int BN>
+__global__ void __launch_bounds__(F8Cfg<BN, false>::kThreads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Fp8Args a) {
   a.err = &g_fp8_status;
-  gemm_fp8_persistent<BN, kSwap>(&map_a, &map_b, a);
+  gemm_fp8_persistent<BN, false>(&map_a, &map_b, a);
 }
 
 template <int BN, bool kSwap, bool kTwo>
@@ -191,6 +191,7 @@ static Fp8Args args_of(const Fp8Product& p) {
   a.K = p.K;
   a.vec = ((uintptr_t)p.out & 15u) == 0 && (p.out_row * (p.out_f32 ? 4 : 2)) % 16 == 0 &&
           (!p.add || (((uintptr_t)p.add & 15u) == 0 && p.add_row % 8 == 0));
+  if (a.vec && ((uintptr_t)p.out & 31u) == 0 && (p.out_row * (p.out_f32 ? 4 : 2)) % 32 == 0) a.vec = 2;
   return a;
 }
 
@@ -235,18 +236,18 @@ static cudaError_t encode(CUtensorMap* mx, CUtensorMap* mw, const Operands& o, c
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BN, bool kSwap>
+template <int BN>
 static cudaError_t launch_gemm(const Operands& o, const Fp8Args& a, int sms, cudaStream_t st) {
-  using Cfg = F8Cfg<BN, kSwap>;
+  using Cfg = F8Cfg<BN, false>;
   CUtensorMap mx, mw;
   cudaError_t e = encode(&mx, &mw, o, a, Cfg::kXRows, Cfg::kWRows);
   static bool seen[64];
-  if (e == cudaSuccess) e = allow_smem(fp8_gemm_kernel<BN, kSwap>, Cfg::kSmem, seen);
+  if (e == cudaSuccess) e = allow_smem(fp8_gemm_kernel<BN>, Cfg::kSmem, seen);
   if (e != cudaSuccess) return e;
   const int64_t tiles =
       (int64_t)((a.M + Cfg::kXRows - 1) / Cfg::kXRows) * ((a.N + Cfg::kWRows - 1) / Cfg::kWRows);
-  return launch_product(fp8_gemm_kernel<BN, kSwap>, tiles < sms ? tiles : sms, Cfg::kThreads, Cfg::kSmem, 1, st,
-                        kSwap ? mw : mx, kSwap ? mx : mw, a);
+  return launch_product(fp8_gemm_kernel<BN>, tiles < sms ? tiles : sms, Cfg::kThreads, Cfg::kSmem, 1, st,
+                        mx, mw, a);
 }
 
 template <int BN, bool kSwap, bool kTwo>
@@ -345,8 +346,8 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   const int64_t t256 = (int64_t)((M + 127) / 128) * ((N + 255) / 256);
   const int64_t t128 = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
   const int64_t w256 = (t256 + sms - 1) / sms, w128 = (t128 + sms - 1) / sms;
-  if (10 * w256 <= 9 * w128) return launch_gemm<256, false>(o, a, sms, st);
-  return launch_gemm<128, false>(o, a, sms, st);
+  if (10 * w256 <= 9 * w128) return launch_gemm<256>(o, a, sms, st);
+  return launch_gemm<128>(o, a, sms, st);
 }
 
 }  // namespace moe_fp4

@@ -58,7 +58,7 @@ struct Fp8Args {
   int64_t out_row;
   int out_f32;
   int early;  // the first weight loads may run before the launch before this one is complete
-  int vec;  // out (and add) rows start 16-byte aligned
+  int vec;  // out (and add) rows start 16-byte aligned; 2: out's 32-byte
   int M, N, K;
   uint32_t* err;
 };
@@ -257,6 +257,12 @@ __device__ __forceinline__ void f8_store_one(const Fp8Args& a, int m, int n, flo
     static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(v);
 }
 
+__device__ __forceinline__ void st_32_bytes(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // Eight consecutive columns of one output row.
 __device__ __forceinline__ void f8_store_8(const Fp8Args& a, int m, int n, const float* v) {
   if (!a.vec || n + 8 > a.N) {
@@ -289,6 +295,46 @@ __device__ __forceinline__ void f8_store_8(const Fp8Args& a, int m, int n, const
     }
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)m * a.out_row + n) =
         make_uint4(p[0], p[1], p[2], p[3]);
+  }
+}
+
+// Sixteen consecutive columns of one output row, in 32-byte stores where the
+// rows allow them: lanes hold rows of their own, and a store of less than a
+// sector of each writes the sector twice.
+__device__ __forceinline__ void f8_store_16(const Fp8Args& a, int m, int n, float* v) {
+  if (a.vec < 2 || n + 16 > a.N) {
+    if (n < a.N) f8_store_8(a, m, n, v);
+    if (n + 8 < a.N) f8_store_8(a, m, n + 8, v + 8);
+    return;
+  }
+  if (a.add) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 u = *reinterpret_cast<const uint4*>(a.add + (int64_t)m * a.add_row + n + 8 * h);
+      const uint32_t p[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[8 * h + 2 * i] += __uint_as_float(p[i] << 16);
+        v[8 * h + 2 * i + 1] += __uint_as_float(p[i] & 0xffff0000u);
+      }
+    }
+  }
+  uint32_t w[8];
+  if (a.out_f32) {
+    float* o = static_cast<float*>(a.out) + (int64_t)m * a.out_row + n;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+      st_32_bytes(o + 8 * h, w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    st_32_bytes(static_cast<__nv_bfloat16*>(a.out) + (int64_t)m * a.out_row + n, w);
   }
 }
 
@@ -353,7 +399,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
                                                     const Fp8Args& a, int split = 1) {
   using Cfg = F8Cfg<BN, kSwap, kTwo, kXq>;
   constexpr bool kFuse = Cfg::kFuse;
-  static_assert(!kFuse || kSplit, "one tile per CTA");
+  static_assert(kSplit || !kSwap, "few tokens: one tile per cluster");
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -637,22 +683,14 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         continue;
       }
       if (polls == 1) continue;
-      if (kSwap) {  // lanes along n: 32 consecutive columns of one token per store
-        const int nn = w0 + row;
+      if (x0 + row < a.M) {
 #pragma unroll
-        for (int i = 0; i < Cfg::kCols / 2; ++i) {
-          const int m = x0 + half * Cfg::kCols + 2 * i;
-          if (nn < a.N && m < a.M) f8_store_one(a, m, nn, pair_lo(acc[i]));
-          if (nn < a.N && m + 1 < a.M) f8_store_one(a, m + 1, nn, pair_hi(acc[i]));
-        }
-      } else if (x0 + row < a.M) {
+        for (int i = 0; i < Cfg::kCols / 16; ++i) {
+          const int nn = w0 + half * Cfg::kCols + 16 * i;
+          float v[16];
 #pragma unroll
-        for (int i = 0; i < Cfg::kCols / 8; ++i) {
-          const int nn = w0 + half * Cfg::kCols + 8 * i;
-          float v[8];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) v[2 * p] = pair_lo(acc[4 * i + p]), v[2 * p + 1] = pair_hi(acc[4 * i + p]);
-          if (nn < a.N) f8_store_8(a, x0 + row, nn, v);
+          for (int p = 0; p < 8; ++p) v[2 * p] = pair_lo(acc[8 * i + p]), v[2 * p + 1] = pair_hi(acc[8 * i + p]);
+          if (nn < a.N) f8_store_16(a, x0 + row, nn, v);
         }
       }
     }

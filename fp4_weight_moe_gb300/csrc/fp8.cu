@@ -155,25 +155,24 @@ cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* a
 // ------------------------------------------------------------------ product
 template <int BN>
 __global__ void __launch_bounds__(F8Cfg<BN, false>::kThreads, 1)
-    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Fp8Args a) {
-  a.err = &g_fp8_status;
-  gemm_fp8_persistent<BN, false>(&map_a, &map_b, a);
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ Fp8Args a) {
+  gemm_fp8_persistent<BN, false>(&map_a, &map_b, a, &g_fp8_status);
 }
 
 template <int BN, bool kSwap, bool kTwo>
 __global__ void __launch_bounds__(F8Cfg<BN, kSwap, kTwo>::kThreads, kTwo ? 2 : 1)
-    fp8_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, Fp8Args a,
+    fp8_split_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ Fp8Args a,
                      int split) {
-  a.err = &g_fp8_status;
-  gemm_fp8_persistent<BN, kSwap, kTwo, true>(&map_a, &map_b, a, split);
+  gemm_fp8_persistent<BN, kSwap, kTwo, true>(&map_a, &map_b, a, &g_fp8_status, split);
 }
 
 // The same for at most eight BF16 tokens (a.xb), quantised by the kernel.
 template <int kXq>
 __global__ void __launch_bounds__(F8Cfg<16, true, true, kXq>::kThreads, 2)
-    fp8_linear_kernel(const __grid_constant__ CUtensorMap map_w, Fp8Args a, int split) {
-  a.err = &g_fp8_status;
-  gemm_fp8_persistent<16, true, true, true, kXq>(&map_w, &map_w, a, split);
+    fp8_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ Fp8Args a, int split) {
+  gemm_fp8_persistent<16, true, true, true, kXq>(&map_w, &map_w, a, &g_fp8_status, split);
 }
 
 // The product kernels' arguments but for the activations.
@@ -266,8 +265,12 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
 // least two K blocks each.  Up to 16 tokens a CTA has at most 16 blocks
 // where eight CTAs can manage that: the kernel that quantises its own tokens
 // holds as many (it shares this rule, so that its results are the same).
+// 128-wide tiles, whose partial sums are 64 KB a CTA, only from 16 blocks on
+// (M=300 1024 x 1024, eight blocks, split 1 / 2 / 4: 6.7 / 7.8 / 7.1 us; M=64
+// 2048 x 7168, sixteen, split 1 / 2: 9.6 / 8.5).
 static int k_split(int64_t tiles, int slots, int nk, int bn) {
   int split = 1;
+  if (bn == 128 && nk < 16) return split;
   while (split < 8 && nk >= 4 * split && (tiles * split * 2 <= slots || (bn == 16 && nk > 16 * split && nk <= 128)))
     split *= 2;
   return split;
@@ -340,13 +343,17 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
     }
   }
   // Many tiles: 128 x 256 takes in less per product, 128 x 128 leaves less of
-  // the last wave idle; a wave of the former takes about 1.11 times as long
-  // (M=512 4096 x 4096: 18.0 against 16.2 us, one wave each; M=768: 18.4
-  // against 29.1, one and two).
+  // the last wave idle; a wave of the former takes 1.2 to 1.4 times as long
+  // (256 against 128 wide: M=512 4096 x 4096, one wave each, 17.1 against 14.0
+  // us; M=768, one and two, 17.8 against 24.3; M=700 7168 x 7168, two and
+  // three, 51.1 against 56.9; M=4096 7168 x 4096, four and seven, 97 against
+  // 124).  K split in clusters for the tiles of the last wave, or for 256-wide
+  // tiles, gained at none of these but M=700: a cluster's sums pass through
+  // shared memory at some 15 bytes a cycle and SM.
   const int64_t t256 = (int64_t)((M + 127) / 128) * ((N + 255) / 256);
   const int64_t t128 = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
   const int64_t w256 = (t256 + sms - 1) / sms, w128 = (t128 + sms - 1) / sms;
-  if (10 * w256 <= 9 * w128) return launch_gemm<256>(o, a, sms, st);
+  if (4 * w256 <= 3 * w128) return launch_gemm<256>(o, a, sms, st);
   return launch_gemm<128>(o, a, sms, st);
 }
 

@@ -14,11 +14,14 @@
 //                  K = 32 MMAs of a block into accumulator g % kAcc (each
 //                  warp every second block), then the commits that publish
 //                  the accumulator and free the stage;
+//   warp 3         copies the scales of 16 K blocks at a time to shared memory
+//                  (cp.async, any strides), up to two chunks ahead, across
+//                  tile boundaries too;
 //   scale warps    each reads its 32 accumulator lanes (and its half of the
 //                  columns where BN >= 128), adds them, scaled, into
-//                  registers, and stores the finished tile.
-// The scales of 16 K blocks at a time are copied to shared memory
-// (cp.async, any strides) one chunk ahead, across tile boundaries too.
+//                  registers, and stores the finished tile.  They hold as
+//                  little else as they can: with the scales' copies among
+//                  their work the compiler spilled inside their loop.
 //
 // The 128-row operand is X (kSwap = false) or W (kSwap = true: few tokens,
 // the tokens on the MMA's N side).
@@ -60,7 +63,6 @@ struct Fp8Args {
   int early;  // the first weight loads may run before the launch before this one is complete
   int vec;  // out (and add) rows start 16-byte aligned; 2: out's 32-byte
   int M, N, K;
-  uint32_t* err;
 };
 
 // kTwo: shared memory and tensor memory for two CTAs per SM.  kXq > 0: the
@@ -68,6 +70,7 @@ struct Fp8Args {
 template <int BN, bool kSwap, bool kTwo = false, int kXq = 0>
 struct F8Cfg {
   static constexpr bool kFuse = kXq > 0;
+  static_assert(kF8Chunk * 2 <= 32, "a lane per weight scale of a chunk");
   static_assert(kXq <= kF8Chunk, "the scales of all K blocks lie in one chunk");
   static_assert(!kFuse || kSwap, "the kernel quantises a few tokens only");
   static constexpr int kHalves = BN >= 128 ? 2 : 1;
@@ -75,13 +78,13 @@ struct F8Cfg {
   static constexpr int kLd = kCols / 2 < 32 ? kCols / 2 : 32;  // ... per tensor-memory load (an even count of them)
   static constexpr int kScaleWarps = 4 * kHalves;
   // 256 columns: 128 sums per scale thread and two loads in flight need more
-  // registers than an even split of the SM's gives ten warps, so the scale
-  // warps take them (setmaxnreg) from a warpgroup that holds warps 0 and 1
+  // registers than an even split of the SM's gives twelve warps, so the scale
+  // warps take them (setmaxnreg) from the warpgroup of warps 0 .. 3
   static constexpr bool kMoveRegs = BN >= 256;
   // two warps issue MMAs, each into its own accumulators, so that the waits
   // and the issue of one hide behind the other's MMAs
   static constexpr int kMmaWarps = 2;
-  static constexpr int kFirst = kMoveRegs ? 4 : 1 + kMmaWarps;  // first scale warp
+  static constexpr int kFirst = 2 + kMmaWarps;  // first scale warp
   static constexpr int kQuantWarps = kFuse ? 4 : 0;  // they help the scale warps quantise, then leave
   static constexpr int kThreads = 32 * (kFirst + kScaleWarps + kQuantWarps);
   static constexpr int kAcc = BN >= 256 ? 2 : 4;
@@ -114,7 +117,7 @@ struct F8Cfg {
   // spread over the banks)
   static constexpr uint32_t kPartRow = kSwap ? 128 : BN + 4;
   static_assert(BN > 128 || (kSwap ? BN : 128) * kPartRow * 4u <= kStages * kStageBytes, "partial sums fit the ring");
-  static_assert((2 * kStages + 2 * kAcc + 1) * 8 + 4 <= (int)kBarBytes, "barrier block");
+  static_assert((2 * kStages + 2 * kAcc + 5) * 8 + 4 <= (int)kBarBytes, "barrier block");
 };
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: E4M3 A and B (format
@@ -243,8 +246,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32
 __device__ __forceinline__ void cp_async_4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-__device__ __forceinline__ void named_bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// An arrival on `bar` once this thread's copies so far are complete.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One finished output value (with the addend, if any).
@@ -396,10 +400,11 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t saddr, uint32_t rank) {
 // accumulator columns that are not stored.
 template <int BN, bool kSwap, bool kTwo = false, bool kSplit = false, int kXq = 0>
 __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, const CUtensorMap* map_b,
-                                                    const Fp8Args& a, int split = 1) {
+                                                    const Fp8Args& a, uint32_t* err, int split = 1) {
   using Cfg = F8Cfg<BN, kSwap, kTwo, kXq>;
   constexpr bool kFuse = Cfg::kFuse;
   static_assert(kSplit || !kSwap, "few tokens: one tile per cluster");
+  static_assert(!kSplit || !Cfg::kMoveRegs, "every warp joins the cluster's sums");
   constexpr int S = Cfg::kStages, NA = Cfg::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -411,7 +416,9 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   uint64_t* done = empty + S;     // [NA]
   uint64_t* accfree = done + NA;  // [NA]
   uint64_t* xready = accfree + NA;  // kXq: the tokens are quantised
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xready + 1);
+  uint64_t* sfull = xready + 1;  // [2] a chunk of scales has arrived
+  uint64_t* sempty = sfull + 2;  // [2] ... and was used
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m_tiles = (a.M + Cfg::kXRows - 1) / Cfg::kXRows;
@@ -424,7 +431,6 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   const int nk = (kSplit ? (int)((int64_t)nk_all * (rank + 1) / split) : nk_all) - kb0;
   const int first = kSplit ? (int)(blockIdx.x / split) : (int)blockIdx.x;
   const int step = kSplit ? tiles : (int)gridDim.x;
-  uint32_t* err = a.err;
 
   // the producer's loads of local K block s
   auto load_w = [&](int slot, int s, int w0) {
@@ -447,6 +453,10 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       mbar_init(&accfree[b], Cfg::kScaleWarps);
     }
     mbar_init(xready, Cfg::kScaleWarps + Cfg::kQuantWarps);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sfull[b], 32);
+      mbar_init(&sempty[b], Cfg::kScaleWarps);
+    }
     fence_mbar_init();
     // this thread is the producer: the first stages' weights set out at once
     if (!a.early) pdl_wait();
@@ -511,9 +521,9 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     __syncwarp();
     if (lane == 0) mbar_arrive(xready);
   };
-  // (the registers move: 384 threads x 168 at launch = 128 x 40 + 256 x 232)
+  // (the registers move: 384 threads x 168 at launch = 128 x 88 + 256 x 208)
   if (warp < Cfg::kFirst) {
-    if (Cfg::kMoveRegs) regs_dec<40>();
+    if (Cfg::kMoveRegs) regs_dec<88>();
     if (warp == 0) {
       if (lane == 0) {
         pdl_wait();
@@ -556,36 +566,53 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
           mma_f8_block(acc, da, db, idesc, &done[ab], &empty[slot]);
         }
       }
+    } else {
+      // the scales of this CTA's K blocks [c0, c0 + kF8Chunk) of every tile
+      pdl_wait();
+      int gc = 0;
+      bool ok = true;
+      for (int idx = first; ok && idx < tiles; idx += step) {
+        const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
+        const int last = (a.N - 1) / 128;
+        for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
+          const int buf = gc & 1, round = gc >> 1;
+          if (round > 0 && !warp_wait(&sempty[buf], (round - 1) & 1, kWaitPollLimit)) {
+            if (lane == 0) atomicOr(err, 32u);
+            ok = false;
+            break;
+          }
+          const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
+          float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
+          if (!kFuse) {
+            // (rows past M read the last row's scale; their sums are not stored)
+#pragma unroll
+            for (int r = lane; r < Cfg::kXRows; r += 32) {
+              const int m = x0 + r < a.M ? x0 + r : a.M - 1;
+              const float* from = a.xs + (int64_t)m * a.xs_row + (int64_t)(kb0 + c0) * a.xs_blk;
+              for (int k = 0; k < n; ++k, from += a.xs_blk) cp_async_4(xd + k * Cfg::kXRows + r, from);
+            }
+          }
+          float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
+          if (lane < n * Cfg::kWBlocks) {
+            const int b = wb + lane % Cfg::kWBlocks;
+            cp_async_4(wd + lane, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + kb0 + c0 + lane / Cfg::kWBlocks);
+          }
+          cp_async_arrive(&sfull[buf]);
+        }
+      }
+      cp_async_wait_all();
     }
   } else if (kFuse && warp >= Cfg::kFirst + Cfg::kScaleWarps) {
     if constexpr (kFuse) quantise();
   } else {
-    if (Cfg::kMoveRegs) regs_inc<232>();
-    const int t = threadIdx.x - 32 * Cfg::kFirst;
+    if (Cfg::kMoveRegs) regs_inc<208>();
     const int half = (warp - Cfg::kFirst) / 4;
     const int row = (warp & 3) * 32 + lane;  // row of the 128-row operand (tensor-memory lane)
     const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * Cfg::kCols);
-    // Copy the scales of this CTA's K blocks [c0, c0 + kF8Chunk) of tile idx.
-    auto load_chunk = [&](int idx, int c0, int buf) {
-      const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
-      const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
-      float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
-      for (int i = kFuse ? n * Cfg::kXRows : t; i < n * Cfg::kXRows; i += 32 * Cfg::kScaleWarps) {
-        const int m = x0 + i % Cfg::kXRows;  // rows past M read the last row's scale; their sums are not stored
-        cp_async_4(xd + i, a.xs + (int64_t)(m < a.M ? m : a.M - 1) * a.xs_row + (int64_t)(kb0 + c0 + i / Cfg::kXRows) * a.xs_blk);
-      }
-      float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
-      const int last = (a.N - 1) / 128;
-      if (t < n * Cfg::kWBlocks) {
-        const int b = wb + t % Cfg::kWBlocks;
-        cp_async_4(wd + t, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + kb0 + c0 + t / Cfg::kWBlocks);
-      }
-    };
     pdl_wait();
     pdl_launch_dependents();
     int g = 0, gc = 0;
     uint32_t polls = kWaitPollLimit;  // 1 once a wait gave up: the warp then goes through its barriers without waiting
-    if (first < tiles) load_chunk(first, 0, 0);
     if constexpr (kFuse) {
       quantise();
       // (the scales of the quantiser warps' rows)
@@ -600,15 +627,11 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
 #pragma unroll
       for (int i = 0; i < Cfg::kCols / 2; ++i) acc[i] = 0;
       for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
-        // this chunk's scales have arrived, and every warp is past the chunk
-        // before it, so the other buffer is free for the next chunk
-        cp_async_wait_all();
-        named_bar_sync(1, 32 * Cfg::kScaleWarps);
         const int buf = gc & 1;
-        if (c0 + kF8Chunk < nk)
-          load_chunk(idx, c0 + kF8Chunk, buf ^ 1);
-        else if (idx + step < tiles)
-          load_chunk(idx + step, 0, buf ^ 1);
+        if (!warp_wait(&sfull[buf], (gc >> 1) & 1, polls)) {
+          polls = 1;
+          atomicOr(err, 32u);
+        }
         const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
         const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
         const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
@@ -663,6 +686,8 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
             if (j + 2 < kLoads) TmemLd<Cfg::kLd>::start(src + Cfg::kLd * (j + 3), r1);
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[buf]);
       }
       if (kSplit) {
         // the ring is idle: every load was multiplied, every MMA is done
@@ -694,7 +719,6 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         }
       }
     }
-    cp_async_wait_all();
   }
   if (kSplit) {
     __syncwarp();

@@ -80,10 +80,13 @@ int moe_fp4_fp8_matmul(const void* x_q, int64_t x_row, const float* x_s, int64_t
                                 static_cast<cudaStream_t>(stream)));
 }
 
+// Rows of a K block's scales in the workspace: whole 16 bytes of them.
+static size_t scale_rows(size_t M) { return (M + 3) / 4 * 4; }
+
 size_t moe_fp4_fp8_linear_workspace_bytes(int M_max, int K) {
   if (check_fp8_sizes(M_max, 1, K) != MOE_FP4_OK) return 0;
   const size_t M = M_max < 1 ? 1 : (size_t)M_max;
-  return align256(M * K) + align256(M * blocks128(K) * sizeof(float));
+  return align256(M * K) + align256(scale_rows(M) * blocks128(K) * sizeof(float));
 }
 
 int moe_fp4_fp8_linear(const void* x_bf16, int64_t x_row, const void* w, int64_t w_row, const float* w_s,
@@ -103,9 +106,10 @@ int moe_fp4_fp8_linear(const void* x_bf16, int64_t x_row, const void* w, int64_t
   if (fused) return done(launch_fp8_linear_fused(x_bf16, x_row, w, w_row, p, static_cast<cudaStream_t>(stream)));
   float* s = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256((size_t)M * K));
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_fp8_quantize(x_bf16, x_row, nullptr, workspace, K, s, 1, M, M, K, false, cs);
+  const int64_t block = (int64_t)scale_rows((size_t)M);
+  const cudaError_t e = launch_fp8_quantize(x_bf16, x_row, nullptr, workspace, K, s, 1, block, M, K, false, cs);
   if (e != cudaSuccess) return report_cuda_error(e);
-  return done(launch_fp8_matmul(workspace, K, s, 1, M, w, w_row, p, true, cs));
+  return done(launch_fp8_matmul(workspace, K, s, 1, block, w, w_row, p, true, cs));
 }
 
 int moe_fp4_fp8_status(uint32_t* flags, int clear, void* stream) {

@@ -190,6 +190,7 @@ static Fp8Args args_of(const Fp8Product& p) {
   a.K = p.K;
   a.vec = ((uintptr_t)p.out & 15u) == 0 && (p.out_row * (p.out_f32 ? 4 : 2)) % 16 == 0 &&
           (!p.add || (((uintptr_t)p.add & 15u) == 0 && p.add_row % 8 == 0));
+  a.pairs = ((uintptr_t)p.out % (p.out_f32 ? 8 : 4)) == 0 && p.out_row % 2 == 0;
   if (a.vec && ((uintptr_t)p.out & 31u) == 0 && (p.out_row * (p.out_f32 ? 4 : 2)) % 32 == 0) a.vec = 2;
   return a;
 }
@@ -265,12 +266,8 @@ static cudaError_t launch_split(const Operands& o, const Fp8Args& a, int tiles, 
 // least two K blocks each.  Up to 16 tokens a CTA has at most 16 blocks
 // where eight CTAs can manage that: the kernel that quantises its own tokens
 // holds as many (it shares this rule, so that its results are the same).
-// 128-wide tiles, whose partial sums are 64 KB a CTA, only from 16 blocks on
-// (M=300 1024 x 1024, eight blocks, split 1 / 2 / 4: 6.7 / 7.8 / 7.1 us; M=64
-// 2048 x 7168, sixteen, split 1 / 2: 9.6 / 8.5).
 static int k_split(int64_t tiles, int slots, int nk, int bn) {
   int split = 1;
-  if (bn == 128 && nk < 16) return split;
   while (split < 8 && nk >= 4 * split && (tiles * split * 2 <= slots || (bn == 16 && nk > 16 * split && nk <= 128)))
     split *= 2;
   return split;
@@ -322,6 +319,7 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   const int M = p.M, N = p.N, K = p.K;
   const Operands o = {x, w, x_row, w_row};
   a.early = after_quantizer;
+  a.xs_vec = xs_row == 1 && xs_blk % 4 == 0 && ((uintptr_t)xs & 15u) == 0 && (M % 4 == 0 || after_quantizer);
   // Up to 32 tokens the weights' 128 rows lie on the MMA's row side and the
   // tokens (16 or 32) on its column side, two CTAs per SM; past that the
   // tokens take the row side, where a scale thread's activation scale is one
@@ -334,7 +332,12 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   const int bn = M <= 16 ? 16 : M <= 32 ? 32 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);
   const int slots = bn == 128 ? sms : 2 * sms;
-  if (tiles <= slots / 2 || bn == 16) {
+  // (128 tokens on rows, a CTA's partial sums 64 KB: from 16 K blocks on, M=300
+  // 1024 x 1024, eight blocks, split 1 / 2 / 4 6.7 / 7.8 / 7.1 us, M=64 2048 x
+  // 7168, sixteen, split 1 / 2 9.6 / 8.5; but always where rows allow no vector
+  // stores, which that kernel's last step does not need: M=226 1328 x 999 9.1
+  // us in all, 14.4 without.)
+  if (bn == 16 || (tiles <= slots / 2 && (bn < 128 || nk >= 16 || !a.vec))) {
     const int split = k_split(tiles, slots, nk, bn);
     switch (bn) {
       case 16: return launch_split<16, true, true>(o, a, (int)tiles, split, st);

@@ -14,9 +14,9 @@
 //                  K = 32 MMAs of a block into accumulator g % kAcc (each
 //                  warp every second block), then the commits that publish
 //                  the accumulator and free the stage;
-//   warp 3         copies the scales of 16 K blocks at a time to shared memory
-//                  (cp.async, any strides), up to two chunks ahead, across
-//                  tile boundaries too;
+//   warp 3         copies the scales of 16 K blocks at a time to shared
+//                  memory (cp.async, any strides), a chunk ahead, across tile
+//                  boundaries too;
 //   scale warps    each reads its 32 accumulator lanes (and its half of the
 //                  columns where BN >= 128), adds them, scaled, into
 //                  registers, and stores the finished tile.  They hold as
@@ -46,11 +46,11 @@ namespace moe_fp4 {
 
 constexpr int kF8BM = 128;
 constexpr int kF8BK = 128;     // K elements (= bytes) per stage: one scale block
-constexpr int kF8Chunk = 16;   // K blocks of scales per shared-memory chunk
 
 struct Fp8Args {
   const float* xs;  // activation scales, xs[m * xs_row + b * xs_blk]
   int64_t xs_row, xs_blk;
+  int xs_vec;  // rows lie next to each other, four at a time in 16 bytes (M rounded up to that)
   const uint16_t* xb;  // kXq: the BF16 activations, xb[m * xb_row + k], in place of E4M3 ones and xs
   int64_t xb_row;
   const float* ws;  // weight scales, ws[(n / 128) * ws_row + b]
@@ -61,6 +61,7 @@ struct Fp8Args {
   int64_t out_row;
   int out_f32;
   int early;  // the first weight loads may run before the launch before this one is complete
+  int pairs;  // out rows start at a pair of values' boundary
   int vec;  // out (and add) rows start 16-byte aligned; 2: out's 32-byte
   int M, N, K;
 };
@@ -70,8 +71,9 @@ struct Fp8Args {
 template <int BN, bool kSwap, bool kTwo = false, int kXq = 0>
 struct F8Cfg {
   static constexpr bool kFuse = kXq > 0;
-  static_assert(kF8Chunk * 2 <= 32, "a lane per weight scale of a chunk");
-  static_assert(kXq <= kF8Chunk, "the scales of all K blocks lie in one chunk");
+  // K blocks of scales per shared-memory chunk (kXq: all of the CTA's), and
+  // the chunks (four of four blocks, M=4096 K=7168 N=4096: 100 us, not 96)
+  static constexpr int kChunk = kFuse ? kXq : 16, kChunks = kFuse ? 1 : 2;
   static_assert(!kFuse || kSwap, "the kernel quantises a few tokens only");
   static constexpr int kHalves = BN >= 128 ? 2 : 1;
   static constexpr int kCols = BN / kHalves;  // accumulator columns per scale thread
@@ -99,15 +101,22 @@ struct F8Cfg {
   static constexpr uint32_t kXqBytes = kXq > 0 ? (kXq + 1) * 1024 : 0;
   static_assert(kXq == 0 || BN == 16, "at most eight tokens");
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
-  static constexpr uint32_t kScaleBytes = 2 * kF8Chunk * (kXRows + kWBlocks) * 4;
+  static constexpr uint32_t kScaleBytes = kChunks * kChunk * (kXRows + kWBlocks) * 4;
   static constexpr uint32_t kBarBytes = 256;
-  static constexpr uint32_t kBudget = (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes - kXqBytes;
+  // a scale warp's 32 x 16 values on their way to rows that allow no vector
+  // stores (a word of padding, so that lanes at their own rows spread over the
+  // banks)
+  static constexpr int kOutRow = 17;
+  static constexpr uint32_t kOutBytes = kSwap ? 0 : kScaleWarps * 32 * kOutRow * 4;
+  static constexpr uint32_t kBudget =
+      (kTwo ? 113u : 227u) * 1024u - 1024u - kBarBytes - kScaleBytes - kXqBytes - kOutBytes;
   // A multiple of the MMA warps, so that a stage's rounds are all one warp's: a
   // wait for a round's parity is also met two rounds earlier, and only a warp
   // that has waited for the round between cannot be early.
   static constexpr int kFit = kBudget / kStageBytes > 12 ? 12 : (int)(kBudget / kStageBytes);
   static constexpr int kStages = kFit / kMmaWarps * kMmaWarps;
-  static constexpr uint32_t kSmem = kStages * kStageBytes + kXqBytes + kScaleBytes + kBarBytes + 1024 /*align*/;
+  static constexpr uint32_t kSmem =
+      kStages * kStageBytes + kXqBytes + kScaleBytes + kBarBytes + kOutBytes + 1024 /*align*/;
   static_assert(kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(kAcc % kMmaWarps == 0, "an accumulator's uses, too, are one warp's");
   static_assert(kStages >= 4 && kSmem <= (kTwo ? 113 : 227) * 1024, "shared memory");
@@ -117,7 +126,7 @@ struct F8Cfg {
   // spread over the banks)
   static constexpr uint32_t kPartRow = kSwap ? 128 : BN + 4;
   static_assert(BN > 128 || (kSwap ? BN : 128) * kPartRow * 4u <= kStages * kStageBytes, "partial sums fit the ring");
-  static_assert((2 * kStages + 2 * kAcc + 5) * 8 + 4 <= (int)kBarBytes, "barrier block");
+  static_assert((2 * kStages + 2 * kAcc + 2 * kChunks + 1) * 8 + 4 <= (int)kBarBytes, "barrier block");
 };
 
 // Instruction descriptor of tcgen05.mma kind::f8f6f4: E4M3 A and B (format
@@ -302,6 +311,63 @@ __device__ __forceinline__ void f8_store_8(const Fp8Args& a, int m, int n, const
   }
 }
 
+// kCols columns of the warp's 32 rows m0 .. (lane l holds row m0 + l) where
+// rows allow no vector stores: sixteen at a time through shared memory (`part`,
+// the warp's own), so that a store's lanes lie along a row.  One copy of the
+// storing code, not one per sixteen columns: the loop is short, its
+// instructions are fetched anew for every tile.
+template <int kCols, int kOutRow>
+__device__ __forceinline__ void f8_store_odd(const Fp8Args& a, int m0, int lane, int n0, const uint64_t (&acc)[kCols / 2],
+                                             float* part) {
+  const int each = a.pairs ? 2 : 1;                             // columns of a lane
+  const int c = a.pairs ? 2 * (lane & 7) : lane & 15;           // of sixteen
+  const int row0 = a.pairs ? lane >> 3 : lane >> 4, rows = 2 * each;
+#pragma unroll 1
+  for (int g = 0; g < kCols / 16; ++g) {
+#pragma unroll
+    for (int i = 0; i < kCols / 16; ++i)
+      if (i == g) {
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          part[lane * kOutRow + 2 * p] = pair_lo(acc[8 * i + p]);
+          part[lane * kOutRow + 2 * p + 1] = pair_hi(acc[8 * i + p]);
+        }
+      }
+    __syncwarp();
+    const int n = n0 + 16 * g + c;
+    if (n < a.N) {
+      const bool two = each == 2 && n + 1 < a.N;
+      const int size = a.out_f32 ? 4 : 2;
+      char* o = static_cast<char*>(a.out) + ((int64_t)(m0 + row0) * a.out_row + n) * size;
+      const int64_t step = a.out_row * rows * size;
+      const __nv_bfloat16* add = a.add ? a.add + (int64_t)(m0 + row0) * a.add_row + n : nullptr;
+#pragma unroll 4
+      for (int r = row0; r < 32; r += rows, o += step) {
+        float lo = part[r * kOutRow + c], hi = part[r * kOutRow + c + each - 1];
+        if (m0 + r < a.M) {
+          if (add) {
+            lo += __bfloat162float(add[0]);
+            if (two) hi += __bfloat162float(add[1]);
+            add += a.add_row * rows;
+          }
+          if (a.out_f32) {
+            if (two)
+              *reinterpret_cast<float2*>(o) = make_float2(lo, hi);
+            else
+              *reinterpret_cast<float*>(o) = lo;
+          } else {
+            if (two)
+              *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(lo, hi);
+            else
+              *reinterpret_cast<__nv_bfloat16*>(o) = __float2bfloat16_rn(lo);
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
 // Sixteen consecutive columns of one output row, in 32-byte stores where the
 // rows allow them: lanes hold rows of their own, and a store of less than a
 // sector of each writes the sector twice.
@@ -409,16 +475,18 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* xq = smem + S * Cfg::kStageBytes;                                // [kXq][8][128]
-  float* xsc = reinterpret_cast<float*>(xq + Cfg::kXqBytes);                // [2][kF8Chunk][kXRows]
-  float* wsc = xsc + 2 * kF8Chunk * Cfg::kXRows;                            // [2][kF8Chunk][kWBlocks]
-  uint64_t* full = reinterpret_cast<uint64_t*>(wsc + 2 * kF8Chunk * Cfg::kWBlocks);
+  constexpr int kChunk = Cfg::kChunk, kChunks = Cfg::kChunks;
+  float* xsc = reinterpret_cast<float*>(xq + Cfg::kXqBytes);                // [kChunks][kChunk][kXRows]
+  float* wsc = xsc + kChunks * kChunk * Cfg::kXRows;                        // [kChunks][kChunk][kWBlocks]
+  uint64_t* full = reinterpret_cast<uint64_t*>(wsc + kChunks * kChunk * Cfg::kWBlocks);
   uint64_t* empty = full + S;
   uint64_t* done = empty + S;     // [NA]
   uint64_t* accfree = done + NA;  // [NA]
   uint64_t* xready = accfree + NA;  // kXq: the tokens are quantised
-  uint64_t* sfull = xready + 1;  // [2] a chunk of scales has arrived
-  uint64_t* sempty = sfull + 2;  // [2] ... and was used
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 2);
+  uint64_t* sfull = xready + 1;  // [kChunks] a chunk of scales has arrived
+  uint64_t* sempty = sfull + kChunks;  // [kChunks] ... and was used
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + kChunks);
+  float* outs = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + Cfg::kBarBytes);  // [kScaleWarps][32][kOutRow]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m_tiles = (a.M + Cfg::kXRows - 1) / Cfg::kXRows;
@@ -453,7 +521,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       mbar_init(&accfree[b], Cfg::kScaleWarps);
     }
     mbar_init(xready, Cfg::kScaleWarps + Cfg::kQuantWarps);
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kChunks; ++b) {
       mbar_init(&sfull[b], 32);
       mbar_init(&sempty[b], Cfg::kScaleWarps);
     }
@@ -521,9 +589,9 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
     __syncwarp();
     if (lane == 0) mbar_arrive(xready);
   };
-  // (the registers move: 384 threads x 168 at launch = 128 x 88 + 256 x 208)
+  // (the registers move: 384 threads x 168 at launch = 128 x 104 + 256 x 200)
   if (warp < Cfg::kFirst) {
-    if (Cfg::kMoveRegs) regs_dec<88>();
+    if (Cfg::kMoveRegs) regs_dec<104>();
     if (warp == 0) {
       if (lane == 0) {
         pdl_wait();
@@ -567,23 +635,27 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         }
       }
     } else {
-      // the scales of this CTA's K blocks [c0, c0 + kF8Chunk) of every tile
+      // the scales of this CTA's K blocks [c0, c0 + kChunk) of every tile
       pdl_wait();
       int gc = 0;
       bool ok = true;
       for (int idx = first; ok && idx < tiles; idx += step) {
         const int x0 = (idx % m_tiles) * Cfg::kXRows, wb = (idx / m_tiles) * Cfg::kWRows / 128;
         const int last = (a.N - 1) / 128;
-        for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
-          const int buf = gc & 1, round = gc >> 1;
+        for (int c0 = 0; c0 < nk; c0 += kChunk, ++gc) {
+          const int buf = gc % kChunks, round = gc / kChunks;
           if (round > 0 && !warp_wait(&sempty[buf], (round - 1) & 1, kWaitPollLimit)) {
             if (lane == 0) atomicOr(err, 32u);
             ok = false;
             break;
           }
-          const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
-          float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
-          if (!kFuse) {
+          const int n = nk - c0 < kChunk ? nk - c0 : kChunk;
+          float* xd = xsc + buf * kChunk * Cfg::kXRows;
+          if (!kFuse && !kSwap && a.xs_vec) {  // four rows a lane
+            const int m = x0 + 4 * lane < a.M ? x0 + 4 * lane : 0;
+            const float* from = a.xs + m + (int64_t)(kb0 + c0) * a.xs_blk;
+            for (int k = 0; k < n; ++k, from += a.xs_blk) cp_async_16(xd + k * Cfg::kXRows + 4 * lane, from);
+          } else if (!kFuse) {
             // (rows past M read the last row's scale; their sums are not stored)
 #pragma unroll
             for (int r = lane; r < Cfg::kXRows; r += 32) {
@@ -592,7 +664,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
               for (int k = 0; k < n; ++k, from += a.xs_blk) cp_async_4(xd + k * Cfg::kXRows + r, from);
             }
           }
-          float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
+          float* wd = wsc + buf * kChunk * Cfg::kWBlocks;
           if (lane < n * Cfg::kWBlocks) {
             const int b = wb + lane % Cfg::kWBlocks;
             cp_async_4(wd + lane, a.ws + (int64_t)(b < last ? b : last) * a.ws_row + kb0 + c0 + lane / Cfg::kWBlocks);
@@ -605,7 +677,7 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
   } else if (kFuse && warp >= Cfg::kFirst + Cfg::kScaleWarps) {
     if constexpr (kFuse) quantise();
   } else {
-    if (Cfg::kMoveRegs) regs_inc<208>();
+    if (Cfg::kMoveRegs) regs_inc<200>();
     const int half = (warp - Cfg::kFirst) / 4;
     const int row = (warp & 3) * 32 + lane;  // row of the 128-row operand (tensor-memory lane)
     const uint32_t tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(half * Cfg::kCols);
@@ -626,15 +698,15 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
       uint64_t acc[Cfg::kCols / 2];  // pairs of sums
 #pragma unroll
       for (int i = 0; i < Cfg::kCols / 2; ++i) acc[i] = 0;
-      for (int c0 = 0; c0 < nk; c0 += kF8Chunk, ++gc) {
-        const int buf = gc & 1;
-        if (!warp_wait(&sfull[buf], (gc >> 1) & 1, polls)) {
+      for (int c0 = 0; c0 < nk; c0 += kChunk, ++gc) {
+        const int buf = gc % kChunks;
+        if (!warp_wait(&sfull[buf], (gc / kChunks) & 1, polls)) {
           polls = 1;
           atomicOr(err, 32u);
         }
-        const float* xd = xsc + buf * kF8Chunk * Cfg::kXRows;
-        const float* wd = wsc + buf * kF8Chunk * Cfg::kWBlocks;
-        const int n = nk - c0 < kF8Chunk ? nk - c0 : kF8Chunk;
+        const float* xd = xsc + buf * kChunk * Cfg::kXRows;
+        const float* wd = wsc + buf * kChunk * Cfg::kWBlocks;
+        const int n = nk - c0 < kChunk ? nk - c0 : kChunk;
         // The accumulator's columns pass through two register buffers.  A
         // wait for tensor-memory loads is for all of them, so both buffers'
         // loads fly together, each started as its buffer is used up.  (No
@@ -708,14 +780,20 @@ __device__ __forceinline__ void gemm_fp8_persistent(const CUtensorMap* map_a, co
         continue;
       }
       if (polls == 1) continue;
-      if (x0 + row < a.M) {
+      if constexpr (!kSwap) {
+        __syncwarp();
+        const int m0 = x0 + (warp & 3) * 32;
+        const int n0 = w0 + half * Cfg::kCols;
+        if (a.vec == 0) {
+          f8_store_odd<Cfg::kCols, Cfg::kOutRow>(a, m0, lane, n0, acc, outs + (warp - Cfg::kFirst) * 32 * Cfg::kOutRow);
+        } else if (m0 + lane < a.M) {
 #pragma unroll
-        for (int i = 0; i < Cfg::kCols / 16; ++i) {
-          const int nn = w0 + half * Cfg::kCols + 16 * i;
-          float v[16];
+          for (int i = 0; i < Cfg::kCols / 16; ++i) {
+            float v[16];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) v[2 * p] = pair_lo(acc[8 * i + p]), v[2 * p + 1] = pair_hi(acc[8 * i + p]);
-          if (nn < a.N) f8_store_16(a, x0 + row, nn, v);
+            for (int p = 0; p < 8; ++p) v[2 * p] = pair_lo(acc[8 * i + p]), v[2 * p + 1] = pair_hi(acc[8 * i + p]);
+            if (n0 + 16 * i < a.N) f8_store_16(a, m0 + lane, n0 + 16 * i, v);
+          }
         }
       }
     }

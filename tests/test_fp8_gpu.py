@@ -80,6 +80,25 @@ def test_matmul(M, K, N, out):
     assert m.fp8_status() == 0
 
 
+@pytest.mark.parametrize("M,K,N,at", [(2000, 256, 2101, 0), (2001, 144, 2102, 0), (2002, 272, 2104, 1),
+                                      (2003, 128, 2112, 8), (1999, 256, 2100, 3), (4100, 400, 2816, 0)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("with_add", [False, True])
+def test_many_tiles_any_row_start(M, K, N, at, out, with_add):
+    """More tiles than SMs, rows of the output that start at any value: the
+    stores of whole sectors, of vectors, of pairs and of single values."""
+    m = _m()
+    xq, wq = rand_fp8(M, K, 1), rand_fp8(N, K, 2)
+    xs, ws = rand_scale(M, blocks(K), 3), rand_scale(blocks(N), blocks(K), 4)
+    add = torch.randn(M, N, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16) if with_add else None
+    want, mag = product_64(xq, xs, wq, ws)
+    buf = torch.full((M, N + at), -7.0, dtype=out, device="cuda")
+    s = xs.t().contiguous().cuda().t()
+    m.fp8_matmul(xq.cuda(), s, wq.cuda(), ws.cuda(), out=buf[:, at:], addend=None if add is None else add.cuda())
+    check(buf[:, at:], want, mag, K, out, add)
+    assert (buf[:, :at] == -7).all()
+
+
 @pytest.mark.parametrize("M", [1, 8, 16, 24, 32, 64, 128])
 def test_long_k_per_cta(M):
     """Sixteen K blocks and more to a CTA, so that every form's ring of stages

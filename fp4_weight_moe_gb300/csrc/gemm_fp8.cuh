@@ -29,13 +29,17 @@
 // What bounds a 128 x 256 tile, in cycles per K block, each measured alone:
 // the MMAs take 512; shared memory moves 128 bytes a cycle, and the MMAs read
 // 48 KB of it and the loads write as much: 768; the scale warps' sums take 270
-// (330 with their tensor-memory loads).  A block in flight takes about 170
-// from the freed accumulator to its MMAs' issue, 830 to their commit's arrival,
-// 400 until it is read out and 230 to be free again, and two are in flight:
-// about 820.  CTA pairs (cta_group::2, 256 x 256 tiles, 64 KB a block and SM)
-// shorten the second bound to 512, but their hand-overs cross SMs: measured
-// 118 us against 110 at M=4096 K=7168 N=4096, and no better with 192, 160 or
-// 128 columns and up to three accumulators.
+// (330 with their tensor-memory loads).  In the whole kernel a block takes
+// about 800 (M=4096 K=N=7168, six waves of tiles: 144-147 us, 2.9 PFLOP/s; K=7168
+// N=4096, four waves, the last a third full: 95-98 us, 2.5).  CTA pairs
+// (cta_group::2, 256 x 256 tiles, 64 KB a block and SM) shorten the second
+// bound to 512, but their hand-overs cross SMs: 118 us where this kernel then
+// took 110, and no better with 192, 160 or 128 columns and up to three
+// accumulators.
+//
+// Few tokens are bound by the chain of one CTA (launch and barriers, the first
+// loads, its K blocks, the cluster's sums): M=1 K=7168 N=4096 7.3 us for 29 MB
+// of weights (4.0 TB/s), M=64 10.4, M=64 K=2048 N=7168 8.1.
 #pragma once
 
 #include "common.cuh"

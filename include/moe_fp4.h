@@ -597,7 +597,7 @@ MOE_FP4_API int moe_fp4_debug_quant_mxfp8_rows(const float *in, int rows, int K,
  * FP8 activations: per row and block of 128 columns b = k / 128
  *     s[m][b] = max_{k in b} |v[m][k]| / 448   (1 where that is zero)
  *     q[m][k] = e4m3_rn(v[m][k] / s[m][b])
- * each step an IEEE FP32 operation.  v is x (act == NULL: x [M][K] bf16), or
+ * each step an IEEE FP32 operation (a zero's sign may be lost).  v is x (act == NULL: x [M][K] bf16), or
  * the gated activation of x = [gate | up] [M][2K] bf16 (act: the kinds of
  * moe_fp4_activation but MOE_FP4_ACT_RELU2), computed in FP32 and not rounded
  * before it is quantised.  s[m][b] is written at m * s_row + b *
@@ -636,8 +636,9 @@ MOE_FP4_API int moe_fp4_fp8_matmul(const void *x_q, int64_t x_row, const float *
  * moe_fp4_fp8_linear_workspace_bytes(M, K) bytes (256-byte aligned, needs no
  * initialisation; MOE_FP4_EWORKSPACE if missing or too small).  Up to
  * MOE_FP4_DECODE_MAX_M rows with K <= 16384 the product quantises its own
- * rows, in one launch: the workspace is then not used and may be NULL.  Results are those of the two
- * calls, bitwise.  The size is 0 for invalid arguments.
+ * rows, in one launch: the workspace is then not used and may be NULL.
+ * Results are those of the two calls, bitwise.  The size is 0 for invalid
+ * arguments.
  */
 MOE_FP4_API size_t moe_fp4_fp8_linear_workspace_bytes(int M_max, int K);
 MOE_FP4_API int moe_fp4_fp8_linear(const void *x_bf16, int64_t x_row, const void *w, int64_t w_row, const float *w_s,

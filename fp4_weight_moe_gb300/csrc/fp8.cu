@@ -274,10 +274,9 @@ static int k_split(int64_t tiles, int slots, int nk, int bn) {
 }
 
 // The decode band (M <= MOE_FP4_DECODE_MAX_M) with K <= 16384: one launch, no
-// workspace.  On the GPU the two launches, the product's prologue and first
-// weights beside the quantiser, are a little faster (K x N 7168 x 4096, M=1:
-// 8.6 against 9.4 us in a graph, M=8 9.3 against 10.9), but each launch costs
-// the host about 3 us, which is what calls of this size wait for.
+// workspace (K x N 7168 x 4096, one launch against quantiser and product: M=1
+// 8.4 / 9.3 us in a graph, M=8 9.4 / 9.7, and one launch less for the host,
+// about 3 us of an eager call).
 bool fp8_linear_is_fused(int M, int K) { return M <= MOE_FP4_DECODE_MAX_M && K <= 128 * 128; }
 
 template <int kXq>
@@ -324,10 +323,9 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   // tokens (16 or 32) on its column side, two CTAs per SM; past that the
   // tokens take the row side, where a scale thread's activation scale is one
   // value instead of one per column.  Measured (us, K x N): 7168 x 4096, M=64
-  // tokens on 64 columns 12.4, M=128 on columns 14.5, on rows 11.4; 4096 x
-  // 4096 M=64 on columns 9.6, M=65 on rows 8.8; M=1 7168 x 4096 split 1 / 2 /
-  // 4 / 8: 22.3 / 12.4 / 8.1 / 7.8; M=256 4096 x 4096 split 1 / 2 / 4: 18.4 /
-  // 12.8 / 18.5 (two waves).
+  // tokens on 64 columns 12.4, on rows 10.4, M=128 14.5 and 11.3; split 1 / 2 /
+  // 4 / 8: M=1 7168 x 4096 22.3 / 12.4 / 8.1 / 7.8, M=128 20.4 / 14.5 / 11.4 / -
+  // (two waves), M=256 4096 x 4096 13.7 / 12.0 / - / -.
   const int nk = (K + 127) / 128;
   const int bn = M <= 16 ? 16 : M <= 32 ? 32 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);

@@ -418,11 +418,12 @@ cudaError_t launch_block_norm(NormArgs a, int res_f32, bool packed, cudaStream_t
   // Chunks per thread: one while a row per CTA leaves SMs with one or two
   // rows (latency) and where a row is short or read by scalar loads; beyond,
   // as many as keep a CTA at 256 threads, so that more rows share an SM and
-  // their waits for the two sums overlap.  Measured with 1 / 2 / 4 chunks
-  // (us, bf16 residual, no norm after the block): H=7168 M=64 2.5 / - / 3.3,
-  // M=16384 151 / - / 138; H=4096 M=64 2.3 / 2.6 / 3.3, M=16384 81.4 / 80.0 /
-  // 80.7; f32 residual with that norm, M=16384: H=7168 365 / - / 221, H=4096
-  // 133 / 126 / 129, H=2560 85 / 77 / 81.
+  // their waits for the two sums overlap.  Measured with 1 / 2 / 4 chunks (us;
+  // bf16 residual, no norm after the block): H=7168 M=64 2.5 / 2.5 / 3.0,
+  // M=600 7.8 / 5.6 / 4.9, M=16384 231 / 154 / 136; H=4096 M=64 2.1 / 2.3 /
+  // 2.8, M=16384 90 / 80 / 80; H=2560 M=16384 59 / 51 / 52; f32 residual with
+  // that norm, M=16384: H=7168 383 / 251 / 224, H=4096 169 / 129 / 122, H=2560
+  // 88 / 79 / 81.
   if (a.layout == kSingle || columns <= 2048 || !many) return launch_ch<1, 1024, false>(a, res_f32, st);
   if (columns <= 4096) return launch_ch<2, 256, false>(a, res_f32, st);
   return launch_ch<4, 256, false>(a, res_f32, st);

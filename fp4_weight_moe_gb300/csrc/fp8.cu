@@ -59,6 +59,15 @@ __device__ __forceinline__ void silu_gated(const uint4 (&g_raw)[V / 8], const fl
   }
 }
 
+// SwiGLU-OAI of one gate and up (gated_act's formula), clamped by comparisons:
+// fminf and fmaxf would turn a NaN into a limit, and the block's FP8 form
+// would hide it.
+__device__ __forceinline__ float swiglu_oai(float gate, float up, const ActParams& p) {
+  const float g = gate > p.limit ? p.limit : gate;
+  const float u = up > p.limit ? p.limit : up < -p.limit ? -p.limit : up;
+  return (u + p.beta) * g / (1.0f + __expf(-p.alpha * g));
+}
+
 // A lane takes V consecutive columns (8 or 16) of each of kChunks chunks.
 template <bool kGated, int V, int kChunks>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __restrict__ x, int64_t x_row, ActParams act,
@@ -100,6 +109,9 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __res
       for (int j = 0; j < V / 8; ++j) bf16x8_to_float(raw_up[i][j], up + 8 * j);
       if (act.kind == MOE_FP4_ACT_SILU) {
         silu_gated<V>(raw[i], up, v);
+      } else if (act.kind == MOE_FP4_ACT_SWIGLUOAI) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = swiglu_oai(v[j], up[j], act);
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = gated_act(v[j], up[j], act);

@@ -603,7 +603,8 @@ MOE_FP4_API int moe_fp4_debug_quant_mxfp8_rows(const float *in, int rows, int K,
  * before it is quantised.  s[m][b] is written at m * s_row + b *
  * s_block (the products read s_row = 1 fastest).  A block with a NaN gives
  * NaN at that element; one with an infinity gives NaN there and zeros (whose
- * scale is infinite) elsewhere, so that products of the row are NaN.
+ * scale is infinite) elsewhere, so that products of the row are NaN.  (Of v:
+ * SwiGLU-OAI's limits take an infinite gate or up to the limit, a NaN stays.)
  * K % 16 == 0, x and q 16-byte aligned, x_row % 8 == 0, q_row % 16 == 0
  * (MOE_FP4_EINVAL for misaligned arrays, MOE_FP4_EUNSUPPORTED for K).
  */

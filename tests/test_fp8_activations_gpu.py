@@ -1,0 +1,62 @@
+"""Gated activations in front of the FP8 quantiser: what is not finite stays
+visible, and every step is the operation that its definition names.
+
+Finite values: half an E4M3 step of the value (1/16 of it, or 2^-10 scales
+below the normals) and 2^-12 of the block's largest for the FP32 activation
+and scale."""
+import pytest
+import torch
+
+from tests.gpu_util import ensure_built
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+ALPHA, BETA, LIMIT = 1.702, 1.0, 3.0
+
+
+def _m():
+    ensure_built()
+    import fp4_weight_moe_gb300 as m
+    return m
+
+
+def quantise(m, x, kind):
+    if kind == "oai":
+        return m.fp8_quantize(x, act=m.ACT_SWIGLUOAI, alpha=ALPHA, beta=BETA, limit=LIMIT)
+    return m.fp8_quantize(x, act=m.ACT_SILU if kind == "silu" else m.ACT_GELU_TANH)
+
+
+def activation_64(gate, up, kind):
+    if kind == "silu":
+        return gate * torch.sigmoid(gate) * up
+    if kind == "gelu":
+        return 0.5 * gate * (1 + torch.tanh((2 / torch.pi) ** 0.5 * (gate + 0.044715 * gate ** 3))) * up
+    g, u = gate.clamp(max=LIMIT), up.clamp(-LIMIT, LIMIT)  # (clamp hands NaN on)
+    return (u + BETA) * g * torch.sigmoid(ALPHA * g)
+
+
+@pytest.mark.parametrize("rows", [9, 3000])  # (the two forms of the kernel)
+@pytest.mark.parametrize("kind", ["silu", "gelu", "oai"])
+def test_what_is_not_finite_stays_visible(rows, kind):
+    """One special gate or up a row: NaN wherever the activation is NaN, an
+    infinite scale with NaN and zeros where it is infinite, and no effect on
+    other elements, blocks and rows."""
+    m = _m()
+    K = 272
+    special = [("gate", NAN), ("up", NAN), ("gate", INF), ("gate", -INF), ("up", INF), ("up", -INF)]
+    g = torch.Generator().manual_seed(rows)
+    x = (torch.randn(rows, 2 * K, generator=g) * 2).to(torch.bfloat16)
+    for i, (where, value) in enumerate(special):
+        x[i, 130 + i + (K if where == "up" else 0)] = value
+    q, s = quantise(m, x.cuda(), kind)
+    v = activation_64(x[:, :K].double(), x[:, K:].double(), kind)
+    s64 = s.cpu().double().repeat_interleave(128, 1)[:, :K]
+    got = q.cpu().double()
+    want_nan = torch.isnan(v) | torch.isinf(v)  # (an infinity over an infinite scale)
+    assert torch.equal(torch.isnan(got), want_nan)
+    assert torch.equal(torch.isinf(s.cpu()), torch.nn.functional.pad(torch.isinf(v), (0, 112)).view(rows, 3, 128).any(2))
+    beside = torch.isinf(s64) & ~want_nan
+    assert not got[beside].any()
+    fine = ~want_nan & ~beside
+    err, bound = (got * s64 - v).abs(), v.abs() / 16 + s64 * 2.0 ** -10 + 448 * s64 * 2.0 ** -12
+    assert (err <= bound)[fine].all()

@@ -59,12 +59,23 @@ __device__ __forceinline__ void silu_gated(const uint4 (&g_raw)[V / 8], const fl
   }
 }
 
-// SwiGLU-OAI of one gate and up (gated_act's formula), clamped by comparisons:
-// fminf and fmaxf would turn a NaN into a limit, and the block's FP8 form
-// would hide it.
+// min and max that hand a NaN on (fminf and fmaxf take the other operand).
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// SwiGLU-OAI of one gate and up (gated_act's formula), where a NaN stays: the
+// block's FP8 form would hide one that the limits had replaced.
 __device__ __forceinline__ float swiglu_oai(float gate, float up, const ActParams& p) {
-  const float g = gate > p.limit ? p.limit : gate;
-  const float u = up > p.limit ? p.limit : up < -p.limit ? -p.limit : up;
+  const float g = min_nan(gate, p.limit);
+  const float u = min_nan(max_nan(up, -p.limit), p.limit);
   return (u + p.beta) * g / (1.0f + __expf(-p.alpha * g));
 }
 

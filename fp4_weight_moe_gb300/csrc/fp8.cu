@@ -72,7 +72,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // SwiGLU-OAI of one gate and up (gated_act's formula), where a NaN stays: the
-// block's FP8 form would hide one that the limits had replaced.
+// block's FP8 form would hide one that the limits had replaced.  The hardware's
+// exponential: its error grows with |alpha g| as that of the rounded product
+// alpha g does, and is about twice it (expf: 16384 x 7168 150 us for 140).
 __device__ __forceinline__ float swiglu_oai(float gate, float up, const ActParams& p) {
   const float g = min_nan(gate, p.limit);
   const float u = min_nan(max_nan(up, -p.limit), p.limit);

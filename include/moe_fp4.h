@@ -597,11 +597,15 @@ MOE_FP4_API int moe_fp4_debug_quant_mxfp8_rows(const float *in, int rows, int K,
  * FP8 activations: per row and block of 128 columns b = k / 128
  *     s[m][b] = max_{k in b} |v[m][k]| / 448   (1 where that is zero)
  *     q[m][k] = e4m3_rn(v[m][k] / s[m][b])
- * each step an IEEE FP32 operation (a zero's sign may be lost).  v is x (act == NULL: x [M][K] bf16), or
- * the gated activation of x = [gate | up] [M][2K] bf16 (act: the kinds of
- * moe_fp4_activation but MOE_FP4_ACT_RELU2), computed in FP32 and not rounded
- * before it is quantised.  s[m][b] is written at m * s_row + b *
- * s_block (the products read s_row = 1 fastest).  A block with a NaN gives
+ * each step an IEEE FP32 operation (a zero's sign may be lost).  v is x (act
+ * == NULL: x [M][K] bf16), or the gated activation of x = [gate | up] [M][2K]
+ * bf16 (act: the kinds of moe_fp4_activation but MOE_FP4_ACT_RELU2), computed
+ * in FP32 and not rounded before it is quantised: SiLU in IEEE operations and
+ * expf; the tanh form of GELU with tanhf; SwiGLU-OAI, as in the layer, with
+ * the hardware's exponential, off by at most 2 + 1.173 |alpha gate'| units of
+ * 2^-23 (the product alpha gate' itself leaves |alpha gate'| half units).
+ * s[m][b] is written at m * s_row + b * s_block (the products read s_row = 1
+ * fastest).  A block with a NaN gives
  * NaN at that element; one with an infinity gives NaN there and zeros (whose
  * scale is infinite) elsewhere, so that products of the row are NaN.  (Of v:
  * SwiGLU-OAI's limits take an infinite gate or up to the limit, a NaN stays.)

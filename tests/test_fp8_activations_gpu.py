@@ -60,3 +60,28 @@ def test_what_is_not_finite_stays_visible(rows, kind):
     fine = ~want_nan & ~beside
     err, bound = (got * s64 - v).abs(), v.abs() / 16 + s64 * 2.0 ** -10 + 448 * s64 * 2.0 ** -12
     assert (err <= bound)[fine].all()
+
+
+@pytest.mark.parametrize("rows", [1024, 65536])
+@pytest.mark.parametrize("alpha,limit", [(1.702, 7.0), (0.25, 256.0)])
+def test_swiglu_oai_precision(rows, alpha, limit):
+    """The clamped SwiGLU of every BF16 gate, alone in its row, through its
+    scale. With x = alpha g: the product is off by 2^-24 of itself, which the
+    exponential turns into |x| 2^-24, and the hardware's exponential is
+    documented to be off by at most 2 + 1.173 |x| units of 2^-23; the sum, the
+    product, the quotient and the scale add less than 2^-21. Where e^-x leaves
+    FP32 (|x| > 85) or the value does, there is nothing to compare."""
+    m = _m()
+    g = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).cuda()
+    x = torch.zeros(65536, 32, dtype=torch.bfloat16, device="cuda")
+    x[:, 5], x[:, 21] = g, 0.75
+    got = torch.cat([m.fp8_quantize(c, act=m.ACT_SWIGLUOAI, alpha=alpha, beta=BETA, limit=limit)[1]
+                     for c in x.split(rows)])[:, 0].double()
+    f = g.double().clamp(max=limit)
+    alpha = torch.tensor(alpha, dtype=torch.float32).double().item()
+    e = alpha * f
+    want = (1.75 * f * torch.sigmoid(e)).abs() / 448
+    fine = (e.abs() <= 85) & (want > 2.0 ** -125)
+    assert fine.sum() > 30000
+    bound = ((2 + 1.173 * e.abs()) * 2.0 ** -23 + e.abs() * 2.0 ** -24 + 2.0 ** -21) * want
+    assert ((got - want).abs() <= bound)[fine].all()

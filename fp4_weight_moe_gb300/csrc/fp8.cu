@@ -81,12 +81,13 @@ __device__ __forceinline__ float swiglu_oai(float gate, float up, const ActParam
   return (u + p.beta) * g / (1.0f + __expf(-p.alpha * g));
 }
 
-// A lane takes V consecutive columns (8 or 16) of each of kChunks chunks.
+// A lane takes V consecutive columns (8 or 16) of each of kChunks chunks.  (No
+// __restrict__: it would let the compiler read x as data that no kernel
+// writes, even before pdl_wait, while the launch before may still write it.)
 template <bool kGated, int V, int kChunks>
-__global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* __restrict__ x, int64_t x_row, ActParams act,
-                                                           uint8_t* __restrict__ q, int64_t q_row,
-                                                           float* __restrict__ s, int64_t s_row, int64_t s_blk, int M,
-                                                           int K) {
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const uint16_t* x, int64_t x_row, ActParams act, uint8_t* q,
+                                                           int64_t q_row, float* s, int64_t s_row, int64_t s_blk,
+                                                           int M, int K) {
   constexpr int kCols = 32 * V;
   pdl_wait();
   pdl_launch_dependents();

@@ -154,11 +154,8 @@ static cudaError_t launch_quantize(const void* x, int64_t x_row, const ActParams
   const unsigned grid = (unsigned)((tasks + warps - 1) / warps);
   const uint16_t* xp = static_cast<const uint16_t*>(x);
   uint8_t* qp = static_cast<uint8_t*>(q);
-  if (dependent)
-    return launch_dependent(fp8_quantize_kernel<kGated, V, kChunks>, grid, 32 * warps, st, xp, x_row, act, qp, q_row, s,
-                            s_row, s_blk, M, K);
-  fp8_quantize_kernel<kGated, V, kChunks><<<grid, 32 * warps, 0, st>>>(xp, x_row, act, qp, q_row, s, s_row, s_blk, M, K);
-  return cudaGetLastError();
+  return launch_smem(fp8_quantize_kernel<kGated, V, kChunks>, grid, 32 * warps, 0, dependent, st, xp, x_row, act, qp,
+                     q_row, s, s_row, s_blk, M, K);
 }
 
 cudaError_t launch_fp8_quantize(const void* x, int64_t x_row, const ActParams* act, void* q, int64_t q_row, float* s,

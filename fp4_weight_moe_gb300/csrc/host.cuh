@@ -47,14 +47,16 @@ cudaError_t allow_smem(Kern kern, size_t bytes, bool (&seen)[64]) {
   return e;
 }
 
-// Launch with programmatic dependent launch: the kernel may become resident
-// while its predecessor on the stream finishes; it waits for that one's
-// completion (griddepcontrol.wait) before it touches global memory, and lets
-// its own successor in only after that wait, so that no kernel ever runs
-// beside one two launches before it.
+// A launch in plain stream order, or (`dependent`) with programmatic dependent
+// launch: the kernel may become resident while its predecessor on the stream
+// finishes; it waits for that one's completion (griddepcontrol.wait) before it
+// touches global memory, and lets its own successor in only after that wait,
+// so that no kernel ever runs beside one two launches before it.  The status
+// is the launch's own: cudaGetLastError would also report, and clear, an
+// error that an earlier call has reported already.
 template <class Kern, class... Args>
-cudaError_t launch_dependent_smem(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
-                                  const Args&... args) {
+cudaError_t launch_smem(Kern kern, unsigned grid, unsigned threads, size_t smem, bool dependent, cudaStream_t st,
+                        const Args&... args) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -64,8 +66,14 @@ cudaError_t launch_dependent_smem(Kern kern, unsigned grid, unsigned threads, si
   c.dynamicSmemBytes = smem;
   c.stream = st;
   c.attrs = at;
-  c.numAttrs = 1;
+  c.numAttrs = dependent ? 1 : 0;
   return cudaLaunchKernelEx(&c, kern, args...);
+}
+
+template <class Kern, class... Args>
+cudaError_t launch_dependent_smem(Kern kern, unsigned grid, unsigned threads, size_t smem, cudaStream_t st,
+                                  const Args&... args) {
+  return launch_smem(kern, grid, threads, smem, true, st, args...);
 }
 
 template <class Kern, class... Args>

@@ -365,48 +365,14 @@ def moe_fp4_debug_decode_plan(M, E, H, I, top_k):
     return tuple(v)
 
 
-def moe_fp4_fp8_quantize(x, x_row, act, q, q_row, s, s_row, s_block, M, K, stream):
-    """``act``: None (x itself) or a MoeFp4Activation (x = [gate | up])."""
-    return _check("moe_fp4_fp8_quantize",
-                  lib().moe_fp4_fp8_quantize(x, x_row, None if act is None else ctypes.byref(act), q, q_row, s, s_row,
-                                             s_block, M, K, stream))
-
-
-def moe_fp4_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32,
-                       M, N, K, stream):
-    return _check("moe_fp4_fp8_matmul",
-                  lib().moe_fp4_fp8_matmul(x_q, x_row, x_s, xs_row, xs_block, w, w_row, w_s, ws_row, add, add_row,
-                                           out, out_row, out_f32, M, N, K, stream))
-
-
 def moe_fp4_fp8_linear_workspace_bytes(M_max, K) -> int:
     return int(lib().moe_fp4_fp8_linear_workspace_bytes(M_max, K))
-
-
-def moe_fp4_fp8_linear(x, x_row, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32, M, N, K, ws, ws_bytes,
-                       stream):
-    return _check("moe_fp4_fp8_linear",
-                  lib().moe_fp4_fp8_linear(x, x_row, w, w_row, w_s, ws_row, add, add_row, out, out_row, out_f32, M, N,
-                                           K, ws, ws_bytes, stream))
 
 
 def moe_fp4_fp8_status(clear: bool, stream) -> int:
     v = ctypes.c_uint32(0)
     _check("moe_fp4_fp8_status", lib().moe_fp4_fp8_status(ctypes.byref(v), int(bool(clear)), stream))
     return v.value
-
-
-def moe_fp4_block_norm(args: bytes, stream):
-    """``args``: a struct moe_fp4_block_norm_args (MoeFp4BlockNormArgs.PACK.pack
-    of its fields, or bytes of an instance)."""
-    return _check("moe_fp4_block_norm", lib().moe_fp4_block_norm(args, stream))
-
-
-def moe_fp4_route_topk(logits, logits_row, logits_f32, bias, score, renormalize, scale, ids, weights, M, E, top_k,
-                       stream):
-    return _check("moe_fp4_route_topk",
-                  lib().moe_fp4_route_topk(logits, logits_row, logits_f32, bias, score, renormalize, scale, ids,
-                                           weights, M, E, top_k, stream))
 
 
 def raw_status(name: str, *args) -> int:

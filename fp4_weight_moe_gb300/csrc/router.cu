@@ -1,7 +1,8 @@
 // The router's choice of experts (moe_fp4_route_topk): per token the top_k
 // experts by logit (softmax) or by sigmoid(logit) + bias, ties to the lowest
 // index, and their weights.  Experts with a logit of -inf or NaN are never
-// chosen; a row that runs out of experts ends in id -1 with weight 0.
+// chosen; a row that runs out of experts ends in id -1 with weight 0.  With
+// the softmax +inf comes first, and its row's weights are NaN (inf - inf).
 //
 // A warp per token.  A bound cuts the scores, as sortable integers, to a few
 // candidates: the top_k-th largest of the lanes' two best each is no larger

@@ -714,7 +714,9 @@ MOE_FP4_API int moe_fp4_block_norm(const moe_fp4_block_norm_args *args, void *st
  * Order: descending, equal scores by ascending index.  Experts with a logit
  * of -inf or NaN (or a NaN score) are never chosen; where a row has fewer
  * than top_k others, its last ids are -1 with weight 0, which the layer takes
- * as no expert.  1 <= top_k <= 16, top_k <= E <= 65536
+ * as no expert.  A logit of +inf has the sigmoid one; with the softmax it
+ * comes first, and the weights of all experts chosen in its row are NaN (that
+ * softmax is not defined).  1 <= top_k <= 16, top_k <= E <= 65536
  * (MOE_FP4_EUNSUPPORTED); bias with the softmax score is MOE_FP4_EINVAL.
  */
 #define MOE_FP4_SCORE_SOFTMAX 0

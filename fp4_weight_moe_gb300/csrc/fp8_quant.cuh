@@ -1,7 +1,7 @@
 // FP8 (E4M3) activations with a scale per 128 columns: the pieces shared by
 // the quantiser, the product kernel that quantises its own tokens, and the
-// norm that hands its output on in FP8.  A block's 128 values lie V per lane
-// (8 or 16) on 128 / V consecutive lanes.
+// norm that hands its output on in FP8 (the reciprocal by the router, too).  A
+// block's 128 values lie V per lane (8 or 16) on 128 / V consecutive lanes.
 #pragma once
 
 #include "common.cuh"
@@ -29,12 +29,16 @@ __device__ __forceinline__ float block_amax(const float (&v)[V]) {
 }
 
 // Quotients without branches, and two at a time, from a reciprocal y of the
-// divisor s: q = v y is within two units, and q + (v - q s) y, both steps
-// fused, is the correctly rounded quotient where y is the correctly rounded
+// divisor s: q + (v - q s) y, both steps fused, is the correctly rounded
+// quotient where q is within a unit of it and y is the correctly rounded
 // reciprocal (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990): three operations a value, where the
 // kernels here would spend more on divisions than on their memory traffic.
-// Away from FP32's ends only; a zero may lose its sign.
+// q = v y itself may be off by up to a unit and a half, exclusive (v times
+// the half unit of y, and its own half), but the last step can only go wrong
+// for quotients next to a midpoint of two values, which are half a unit or a
+// unit and a half from q, and the latter is out of reach.  Away from FP32's
+// ends only; a zero may lose its sign.
 __device__ __forceinline__ float2 quotients(float2 v, float2 s_neg, float2 y) {
   const float2 t = fmul2(v, y);
   return ffma2(ffma2(t, s_neg, v), y, t);
@@ -42,9 +46,16 @@ __device__ __forceinline__ float2 quotients(float2 v, float2 s_neg, float2 y) {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// The reciprocals of -s_neg, 2^-126 < s < 2^126, correctly rounded: a step of
-// y + y (1 - s y) on the hardware's approximation, which is within a unit
-// (same source; compared with the IEEE reciprocal for all 2^23 significands).
+// 1 / x, 2^-126 < x < 2^126, correctly rounded, without branches: a step of y
+// + y (1 - x y) on the hardware's approximation, which is within a unit (same
+// source; compared with the IEEE reciprocal for all 2^23 significands).
+__device__ __forceinline__ float recip_rn(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return fmaf(y, fmaf(-x, y, 1.0f), y);
+}
+
+// The same of -s_neg, two at a time.
 __device__ __forceinline__ float2 reciprocals(float2 s_neg) {
   float2 y;
   asm("rcp.approx.f32 %0, %1;" : "=f"(y.x) : "f"(-s_neg.x));

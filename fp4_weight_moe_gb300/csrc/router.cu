@@ -22,6 +22,7 @@
 // are 10; sigmoid 42). An IEEE reciprocal for every sigmoid, a branch each,
 // took 4.8 us at M = 4, E = 288 where the one below takes 3.5.
 #include "block.cuh"
+#include "fp8_quant.cuh"
 #include "host.cuh"
 
 namespace moe_fp4 {
@@ -34,18 +35,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 
 // 1 / (1 + e^-v), each step rounded (the reciprocal correctly: the quotient).
 __device__ __forceinline__ float sigmoid_exact(float v) { return __frcp_rn(1.0f + expf(-v)); }
-
-// 1 / x, correctly rounded, for 1 <= x < 2^126, without branches, so that the
-// scores of a lane overlap: a step of y + y (1 - x y), fused, on the
-// hardware's approximation, which is within a unit (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990; compared with the IEEE reciprocal for all 2^23
-// significands).
-__device__ __forceinline__ float recip_rn(float x) {
-  float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return fmaf(y, fmaf(-x, y, 1.0f), y);
-}
 
 __device__ __forceinline__ float route_logit(const RouteArgs& a, int64_t m, int e) {
   return a.f32 ? static_cast<const float*>(a.logits)[m * a.row + e]

@@ -336,9 +336,9 @@ def route_topk(logits: torch.Tensor, top_k: int, score: int = SCORE_SOFTMAX, bia
     sigmoid(logit) + ``bias`` (float32 ``[E]`` or None) and weighs by
     sigmoid(logit).  Equal scores go to the lowest index; experts with a logit
     of -inf or NaN are never chosen, and a row that runs out of experts ends
-    in id -1 with weight 0.  With the softmax a logit of +inf comes first
-    and makes its row's weights NaN, as torch.softmax does.  ``renormalize`` divides by the chosen weights'
-    sum; ``scale`` multiplies the weights."""
+    in id -1 with weight 0.  With the softmax a logit of +inf comes first and
+    makes its row's weights NaN, as torch.softmax does.  ``renormalize``
+    divides by the chosen weights' sum; ``scale`` multiplies the weights."""
     if stream is not None:
         with _on(stream, logits):
             return route_topk(logits, top_k, score, bias, renormalize, scale)

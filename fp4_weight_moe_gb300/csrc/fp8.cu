@@ -23,8 +23,9 @@ cudaError_t fp8_status_address(void** p) { return cudaGetSymbolAddress(p, g_fp8_
 //
 // Bound: HBM (that size: 6.9 TB/s of a copy's 6.8; 4096 x 7168 14.8 us, 6.0
 // TB/s), with SiLU the instructions of its exact exponential, reciprocal and
-// quotients (16384 x 7168 122 us, 4.8 TB/s; with IEEE divisions 139); up to a
-// few hundred rows the launch (64 x 7168 1.7 us, with SiLU 2.1).
+// quotients (16384 x 7168 122 us, 4.8 TB/s; with IEEE divisions 139; GELU 128,
+// SwiGLU-OAI 140); up to a few hundred rows the launch (64 x 7168 1.7 us, 64 x
+// 2048 with SiLU or GELU 2.0, with SwiGLU-OAI 2.4).
 
 // SiLU(g) u in full FP32 precision (the scale of a block follows its largest
 // product, and an element near the middle of two E4M3 values turns on it), on
@@ -297,9 +298,10 @@ static int k_split(int64_t tiles, int slots, int nk, int bn) {
 }
 
 // The decode band (M <= MOE_FP4_DECODE_MAX_M) with K <= 16384: one launch, no
-// workspace (K x N 7168 x 4096, one launch against quantiser and product: M=1
-// 8.4 / 9.3 us in a graph, M=8 9.4 / 9.7, and one launch less for the host,
-// about 3 us of an eager call).
+// workspace (K x N 7168 x 4096, one launch against quantiser and product, in a
+// graph: M=1 8.0 / 9.2 us, M=8 9.2 / 9.4 with the weights in L2, 8.9 / 11.4 and
+// 9.7 / 11.7 with weights from memory; and one launch less for the host, about
+// 3 us of an eager call).
 bool fp8_linear_is_fused(int M, int K) { return M <= MOE_FP4_DECODE_MAX_M && K <= 128 * 128; }
 
 template <int kXq>
@@ -345,10 +347,12 @@ cudaError_t launch_fp8_matmul(const void* x, int64_t x_row, const float* xs, int
   // Up to 32 tokens the weights' 128 rows lie on the MMA's row side and the
   // tokens (16 or 32) on its column side, two CTAs per SM; past that the
   // tokens take the row side, where a scale thread's activation scale is one
-  // value instead of one per column.  Measured (us, K x N): 7168 x 4096, M=64
-  // tokens on 64 columns 12.4, on rows 10.4, M=128 14.5 and 11.3; split 1 / 2 /
-  // 4 / 8: M=1 7168 x 4096 22.3 / 12.4 / 8.1 / 7.8, M=128 20.4 / 14.5 / 11.4 / -
-  // (two waves), M=256 4096 x 4096 13.7 / 12.0 / - / -.
+  // value instead of one per column.  Measured (us, K x N, weights in L2): 7168 x
+  // 4096, M=64 tokens on 64 columns 12.4, on rows 10.4, M=128 14.5 and 11.3;
+  // split 1 / 2 / 4 / 8: M=1 7168 x 4096 15.5 / 9.8 / 6.9 / 7.0, M=128 21.3 /
+  // 14.6 / 11.1 / 26.7, M=256 4096 x 4096 14.6 / 11.2 / 17.3 / 38.9; with weights
+  // from memory 15.9 / 10.5 / 8.9 / 8.8, 21.6 / 15.0 / 12.2 / 28.8 and 15.1 / 11.9
+  // / 18.4 / 40.5.
   const int nk = (K + 127) / 128;
   const int bn = M <= 16 ? 16 : M <= 32 ? 32 : 128;
   const int64_t tiles = (int64_t)((M + bn - 1) / bn) * ((N + 127) / 128);

@@ -30,16 +30,18 @@
 // the MMAs take 512; shared memory moves 128 bytes a cycle, and the MMAs read
 // 48 KB of it and the loads write as much: 768; the scale warps' sums take 270
 // (330 with their tensor-memory loads).  In the whole kernel a block takes
-// about 800 (M=4096 K=N=7168, six waves of tiles: 144-147 us, 2.9 PFLOP/s; K=7168
-// N=4096, four waves, the last a third full: 95-98 us, 2.5).  CTA pairs
+// about 800 (M=4096 K=N=7168, six waves of tiles: 144-151 us, 2.9 PFLOP/s; K=7168
+// N=4096, four waves, the last a third full: 95-99 us, 2.5).  CTA pairs
 // (cta_group::2, 256 x 256 tiles, 64 KB a block and SM) shorten the second
 // bound to 512, but their hand-overs cross SMs: 118 us where this kernel then
 // took 110, and no better with 192, 160 or 128 columns and up to three
 // accumulators.
 //
 // Few tokens are bound by the chain of one CTA (launch and barriers, the first
-// loads, its K blocks, the cluster's sums): M=1 K=7168 N=4096 7.3 us for 29 MB
-// of weights (4.0 TB/s), M=64 10.4, M=64 K=2048 N=7168 8.1.
+// loads, its K blocks, the cluster's sums).  With the weights in L2, and with
+// weights from memory, as a model's layers find theirs: M=1 K=7168 N=4096 7.0
+// and 8.8 us for 29 MB (3.3 TB/s of HBM), M=64 10.1 and 11.3, M=64 K=2048 N=7168
+// 7.7 and 8.7.
 #pragma once
 
 #include "common.cuh"

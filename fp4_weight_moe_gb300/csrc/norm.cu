@@ -12,10 +12,14 @@
 // Bound: HBM where rows are many and their starts alike (16384 x 7168, bf16
 // residual, no norm after the block: 136 us, 6.9 TB/s of a copy's 6.8; f32
 // residual, both norms, a gate per value: 244 us, 6.7; 4096 x 4096, both
-// norms: 24 us, 5.6).  Odd widths pay for the weights, which do not shift with
-// the rows and are read one by one (9000 x 5005, bf16: 70 us, 5.1 TB/s; with
-// all rows read one by one 180).  Up to a few hundred rows the launch and the
-// chain of two sums (64 x 7168, f32, both norms: 3.7 us; one row of 2560 2.0).
+// norms: 24 us, 5.6, with the FP8 form 29).  Odd widths pay for the weights,
+// which do not shift with the rows and are read one by one (9000 x 5005, bf16,
+// no norm after the block: 70 us, 5.1 TB/s, with it 90; with all rows read one
+// by one 180).  Past 16384 columns one CTA of 1024 threads fills an SM's
+// registers, so nothing runs beside a row's sums, and the odd forms and the FP32
+// one spill some (1000 x 32768, both norms: 61 us, 4.3 TB/s, f32 97; 1000 x
+// 32767 144).  Up to a few hundred rows the launch and the chain of two sums (64
+// x 7168, f32, both norms: 3.7 us; one row of 2560 2.0).
 #include "block.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"

@@ -17,10 +17,12 @@
 // top_k = 10, where the list held: 4.9 us at M = 4096, now 5.1).
 //
 // Bound: few tokens, the chain of one row (2.4 us at M = 4, 3.5 with 288
-// sigmoids, from a graph); many, the integer and special-function work of the
-// scores (M = 32768, 512 experts in FP32: 27 us of which the logits' bytes
-// are 10; sigmoid 42). An IEEE reciprocal for every sigmoid, a branch each,
-// took 4.8 us at M = 4, E = 288 where the one below takes 3.5.
+// sigmoids, from a graph), and so up to a wave of CTAs (M = 4096, 512 experts:
+// 512 CTAs for 608 places, 5.1 us, sigmoid 7.5; issue slots 30 and 39 % busy
+// over the whole launch); many, the instructions of the scores (M = 32768, 512
+// experts in FP32: 27 us of which the logits' bytes are 10; sigmoid 42; issue
+// slots 81 and 83 % busy while SMs are).  An IEEE reciprocal for every sigmoid,
+// a branch each, took 4.8 us at M = 4, E = 288 where recip_rn takes 3.5.
 #include "block.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"

@@ -24,6 +24,7 @@ from . import _capi
 SCORE_SOFTMAX, SCORE_SIGMOID = _capi.MOE_FP4_SCORE_SOFTMAX, _capi.MOE_FP4_SCORE_SIGMOID
 FP8 = torch.float8_e4m3fn
 _BF16, _F32 = torch.bfloat16, torch.float32
+_INT_MAX = 2 ** 31 - 1
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -72,7 +73,10 @@ def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -
 def _sizes(t: torch.Tensor, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, not {list(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if shape[0] > _INT_MAX or shape[1] > _INT_MAX:  # (ctypes would pass the low 32 bits on)
+        raise ValueError(f"{name} must have fewer than 2^31 rows and columns, not {list(shape)}")
+    return shape
 
 
 def _float_type(t: torch.Tensor, name: str):

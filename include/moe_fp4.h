@@ -624,8 +624,10 @@ MOE_FP4_API int moe_fp4_fp8_quantize(const void *x_bf16, int64_t x_row, const mo
  * NULL, out bf16 (out_f32 = 0) or f32 [M][N]: the sums are FP32 and rounded
  * once, after add.  Products of a block are summed on the tensor cores, the
  * scaled blocks in FP32 registers, both in a fixed order: results are
- * bitwise deterministic for given sizes and device.  out may be add itself;
- * it must not overlap the other inputs.
+ * bitwise deterministic for given sizes, alignment of out and add, and
+ * device.  (Where rows of out or add start off a 16-byte boundary, a product
+ * of few tiles may split K where it otherwise does not.)  out may be add
+ * itself; it must not overlap the other inputs.
  * K % 16 == 0 (MOE_FP4_EUNSUPPORTED), x_q and w 16-byte aligned with row
  * strides that are multiples of 16 (MOE_FP4_EINVAL); any M and N, last
  * blocks of K and N may be short.

@@ -9,9 +9,9 @@ CAPI = os.path.join(ROOT, "fp4_weight_moe_gb300", "_capi.py")
 
 
 def python_files():
-    for base, dirs, files in os.walk(ROOT):
-        dirs[:] = [d for d in dirs if not d.startswith((".", "_")) and d not in ("gpurun_out", "baseline")]
-        yield from (os.path.join(base, f) for f in files if f.endswith(".py"))
+    for folder in ("fp4_weight_moe_gb300", "tests", "examples"):
+        for base, _, files in os.walk(os.path.join(ROOT, folder)):
+            yield from (os.path.join(base, f) for f in files if f.endswith(".py"))
 
 
 def test_every_wrapper_is_called():

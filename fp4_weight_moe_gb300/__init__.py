@@ -320,3 +320,14 @@ from .ops import (  # noqa: E402,F401
     fp8_status,
     route_topk,
 )
+from .attention import (  # noqa: E402,F401
+    CacheStep,
+    alloc_fp4_attention_workspace,
+    alloc_fp4_cache,
+    cache_step,
+    fp4_attention,
+    fp4_attention_status,
+    fp4_cache_read,
+    qk_norm_rope,
+    rotary_table,
+)

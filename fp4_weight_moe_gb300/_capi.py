@@ -64,6 +64,40 @@ class MoeFp4BlockNormArgs(ctypes.Structure):
 assert MoeFp4BlockNormArgs.PACK.size == ctypes.sizeof(MoeFp4BlockNormArgs)
 
 
+def _struct(*fields):
+    """(ctypes fields, native struct format) of a C structure given as "names: type code" lines."""
+    kinds = {"P": ctypes.c_void_p, "q": ctypes.c_int64, "N": ctypes.c_size_t, "f": ctypes.c_float, "i": ctypes.c_int}
+    pairs = [(name, kind) for line in fields for names, kind in [line.split(": ")] for name in names.split()]
+    return [(name, kinds[kind]) for name, kind in pairs], struct.Struct("@" + "".join(kind for _, kind in pairs) + "0q")
+
+
+class MoeFp4CacheStepArgs(ctypes.Structure):
+    """struct moe_fp4_cache_step_args."""
+    _fields_, PACK = _struct("lengths new_tokens finished tables: P", "table_row: q",
+                             "free_pages free_count offsets positions slots lengths_out free_count_out accepted: P",
+                             "table_width free_capacity page_size R tokens: i")
+
+
+class MoeFp4QkNormRopeArgs(ctypes.Structure):
+    """struct moe_fp4_qk_norm_rope_args."""
+    _fields_, PACK = _struct("q_in k_in v_in: P", "q_row q_head k_row k_head v_row v_head: q",
+                             "w_q w_k rotary positions q_out k_out: P", "q_out_row q_out_head k_out_row k_out_head: q",
+                             "cache slots: P", "eps offset k_scale v_scale: f",
+                             "weights_f32 interleaved positions_i64 positions_max T Hq Hkv D rot pages page_size: i")
+
+
+class MoeFp4AttentionArgs(ctypes.Structure):
+    """struct moe_fp4_attention_args."""
+    _fields_, PACK = _struct("q: P", "q_row q_head: q", "cache tables: P", "table_row: q",
+                             "lengths offsets sinks out: P", "out_row out_head: q", "lse workspace: P",
+                             "workspace_bytes: N", "scale k_scale v_scale: f",
+                             "window T R Hq Hkv D pages page_size table_width: i")
+
+
+for _s in (MoeFp4CacheStepArgs, MoeFp4QkNormRopeArgs, MoeFp4AttentionArgs):
+    assert _s.PACK.size == ctypes.sizeof(_s)
+
+
 # (name, restype, argtypes) for every symbol declared in include/moe_fp4.h
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -121,6 +155,12 @@ SIGNATURES = {
     "moe_fp4_fp8_status": (_I, [ctypes.POINTER(ctypes.c_uint32), _I, _P]),
     "moe_fp4_block_norm": (_I, [_P, _P]),
     "moe_fp4_route_topk": (_I, [_P, _L, _I, _P, _I, _I, _F, _P, _P, _I, _I, _I, _P]),
+    "moe_fp4_cache_step": (_I, [_P, _P]),
+    "moe_fp4_qk_norm_rope": (_I, [_P, _P]),
+    "moe_fp4_cache_read": (_I, [_P, _I, _I, _I, _I, _P, _F, _F, _P, _P, _I, _P]),
+    "moe_fp4_attention_workspace_bytes": (_Z, [_I, _I, _I, _I]),
+    "moe_fp4_attention": (_I, [_P, _P]),
+    "moe_fp4_attention_status": (_I, [ctypes.POINTER(ctypes.c_uint32), _I, _P]),
     "moe_fp4_debug_decode_plan": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int)]),
 }
 
@@ -372,6 +412,16 @@ def moe_fp4_fp8_linear_workspace_bytes(M_max, K) -> int:
 def moe_fp4_fp8_status(clear: bool, stream) -> int:
     v = ctypes.c_uint32(0)
     _check("moe_fp4_fp8_status", lib().moe_fp4_fp8_status(ctypes.byref(v), int(bool(clear)), stream))
+    return v.value
+
+
+def moe_fp4_attention_workspace_bytes(R_max, Hq, Hkv, D) -> int:
+    return int(lib().moe_fp4_attention_workspace_bytes(R_max, Hq, Hkv, D))
+
+
+def moe_fp4_attention_status(clear: bool, stream) -> int:
+    v = ctypes.c_uint32(0)
+    _check("moe_fp4_attention_status", lib().moe_fp4_attention_status(ctypes.byref(v), int(bool(clear)), stream))
     return v.value
 
 

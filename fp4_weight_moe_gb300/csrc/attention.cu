@@ -1,0 +1,643 @@
+// Attention over the paged cache of 4 bits (moe_fp4_attention): a few rows to
+// a key head, as in decoding, and the join of what workers share.
+//
+//   x_j = scale k_scale q . k_j,  out = v_scale sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
+//
+// in one pass over the cache with a running maximum m (in units of log 2).
+//
+// Every warp streams blocks of 16 tokens of its own (keys and values of a head
+// lie together: one bulk copy of 18 D bytes each) through a ring in shared
+// memory, decodes them in registers (E2M1 by the hardware's conversion, times
+// the E4M3 scale, exact in FP16) straight into the operands of
+// mma.m16n8k16: the 16 tokens are the rows of K q^T, whose columns are the
+// heads that share the key head, so that eight heads fill the product, and
+// the columns of V^T p^T.  Between the two, p is a transposition away
+// (movmatrix) from the second product's operand.  Tokens are dealt to the
+// products' rows as (0, 4, 1, 5, 2, 6, 3, 7), and the same 8 later, so that
+// the lanes that read the values of their two tokens at once lie on other
+// banks.  q is scaled by a power of two per row into FP16's range.
+#include "attention_work.cuh"
+#include "host.cuh"
+#include "tcgen05.cuh"
+
+namespace moe_fp4 {
+
+static __device__ uint32_t g_attention_status;
+
+cudaError_t attention_status_address(void** p) { return cudaGetSymbolAddress(p, g_attention_status); }
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kUnit = kWarps * kCacheBlock;  // tokens that the warps of a worker take in one go
+constexpr uint32_t kWaitCode = 1u;
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two E4M3 scales as an FP16 pair, NaN as 0.
+__device__ __forceinline__ uint32_t value_scales(uint32_t lo, uint32_t hi) {
+  if ((lo & 0x7fu) == 0x7fu) lo = 0;
+  if ((hi & 0x7fu) == 0x7fu) hi = 0;
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(lo | (hi << 8))));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t key_scale(uint32_t b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(b | (b << 8))));
+  return r;
+}
+
+// The exponent that brings a row's largest |q| to [2^14, 2^15), as 2^-e, 2^e.
+__device__ __forceinline__ float row_scale(float top, float& back) {
+  const int e = min(max((int)((__float_as_uint(top) >> 23) & 0xff) - 127 - 14, -100), 100);
+  back = __uint_as_float((uint32_t)(127 + e) << 23);
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// The token of a block that row i of its 16 stands for.
+__device__ __forceinline__ int row_token(int i) { return (i & 8) + ((i & 7) >> 1) + 4 * (i & 1); }
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStages = 4;
+  static constexpr int kBlockBytes = cache_block_bytes(D);
+  static constexpr int kRing = kStages * kBlockBytes;  // a warp's
+  static constexpr int kRow = D + 4;                   // floats of a row of sums (padded: rows start on other banks)
+  static_assert(kRows * kRow * 4 <= kRing, "a warp's sums lie in its ring");
+  static constexpr int kBarriers = kWarps * kStages * 8;
+  static constexpr int kStats = kWarps * kRows * 2 * 4;
+  static constexpr int kSmem = kWarps * kRing + kBarriers + kStats + 128;
+  static constexpr int kCtas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;  // per SM
+};
+
+// A worker's place in the line of units.
+struct Place {
+  int r;
+  int64_t rest;  // units of the request before the worker's first
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_kernel(AttnArgs p) {
+  using C = Cfg<D, NT>;
+  constexpr int kRows = C::kRows, S = C::kStages;
+  constexpr int kSteps = D / 16;  // K steps of q . k, row tiles of V^T
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * C::kRing);
+  float* stats = reinterpret_cast<float*>(smem + kWarps * C::kRing + C::kBarriers);
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + kWarps * C::kRing + C::kBarriers + C::kStats);
+  __shared__ Place s_place;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * C::kRing;
+  uint64_t* full = bars + warp * S;
+
+  if (lane == 0)
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+  fence_mbar_init();
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // the line of units, and this worker's stretch
+  const int each = ceil_div(max(p.a.R, 1), kThreads);
+  const int r0 = min((int)threadIdx.x * each, p.a.R), r1 = min(r0 + each, p.a.R);
+  int64_t mine = 0, units;
+  for (int r = r0; r < r1; ++r) mine += attn_units<kRows, kUnit>(p, r);
+  const int64_t before = block_before<kThreads>(mine, &units, scan);
+  if (blockIdx.x == 0) {
+    int64_t at = before;
+    for (int r = r0; r < r1; ++r) {
+      p.prefix[r] = at;
+      at += attn_units<kRows, kUnit>(p, r);
+    }
+    if (threadIdx.x == 0) p.prefix[p.a.R] = units;
+  }
+  const int workers = attn_workers(p, units);
+  if (units == 0 || (int)blockIdx.x >= workers) return;
+  int64_t u = attn_start(blockIdx.x, units, workers);
+  const int64_t u_end = attn_start(blockIdx.x + 1, units, workers);
+  if (before <= u && u < before + mine) {
+    int64_t at = before;
+    for (int r = r0; r < r1; ++r) {
+      const int64_t n = attn_units<kRows, kUnit>(p, r);
+      if (u < at + n) {
+        s_place = {r, u - at};
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int r = s_place.r;
+  int64_t rest = s_place.rest;
+
+  const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
+  const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);  // blocks of a page
+  const float to_log2 = 1.4426950408889634f;
+  int round = 0;  // copies of this warp so far: stage round % S, phase round / S
+  bool alive = true;
+
+  while (u < u_end) {
+    // the item
+    const AttnRequest q = attn_request(p, r);
+    const int tiles = attn_tiles<kRows>(p, q);
+    int tile = 0;
+    AttnSpan span = {0, 0, 0, 0};
+    for (; tile < tiles; ++tile) {
+      span = attn_span<kUnit>(p, q, tile * kRows, kRows);
+      if (rest < (int64_t)span.units * p.a.Hkv) break;
+      rest -= (int64_t)span.units * p.a.Hkv;
+    }
+    if (tile == tiles) {  // (nothing is left of this request)
+      ++r;
+      rest = 0;
+      continue;
+    }
+    const int head = (int)(rest / span.units), from = (int)(rest - (int64_t)head * span.units);
+    const int to = (int)min((int64_t)span.units, from + u_end - u);
+    u += to - from;
+
+    // q, in the operand's order, and the rows' factors
+    uint32_t qf[NT][kSteps][2];
+    float fac[NT][2];
+    int last[NT][2];  // position of the columns' queries, -1: no row
+    const int base_pos = q.length - q.n;
+    const int rows = min((int64_t)kRows, (int64_t)q.n * p.group - (int64_t)tile * kRows);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int row = tile * kRows + 8 * n + g;
+      float v[D / 4], top = 0.f;
+      const bool real = 8 * n + g < rows;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(q.row0 + row / p.group) * p.a.q_row +
+                                 (int64_t)(head * p.group + row % p.group) * p.a.q_head + t * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const uint4 w = real ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
+        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] = __uint_as_float(b[j] << 16);
+          v[8 * i + 2 * j + 1] = __uint_as_float(b[j] & 0xffff0000u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float back;
+      const float by = row_scale(top, back);
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) {
+        qf[n][j][0] = pack_f16x2(v[4 * j] * by, v[4 * j + 1] * by);
+        qf[n][j][1] = pack_f16x2(v[4 * j + 2] * by, v[4 * j + 3] * by);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        fac[n][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c)) * (p.a.scale * p.a.k_scale * to_log2);
+        const int col = 8 * n + 2 * t + c;
+        last[n][c] = col < rows ? base_pos + (tile * kRows + col) / p.group : -1;
+      }
+    }
+    // blocks that every row sees whole
+    const int pos_first = base_pos + tile * kRows / p.group;
+    const int pos_last = base_pos + (tile * kRows + rows - 1) / p.group;
+    const int all_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
+
+    float o[NT][kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    // this warp's blocks: first, first + kWarps, ...
+    const int end_block = min((span.first + to) * kWarps, (span.hi + kCacheBlock - 1) / kCacheBlock);
+    const int first = (span.first + from) * kWarps + warp;
+    const int count = alive && first < end_block ? (end_block - first + kWarps - 1) / kWarps : 0;
+    int page_reg = 0;  // pages of 32 blocks: lane i's that of block first + (i + 32 k) kWarps
+    auto page_of = [&](int i) {
+      if ((i & 31) == 0) {
+        const int b = first + (i + lane) * kWarps;
+        page_reg = b < end_block ? p.a.tables[(int64_t)r * p.a.table_row + (b >> blocks_log)] : 0;
+      }
+      return __shfl_sync(0xffffffffu, page_reg, i & 31);
+    };
+    unsigned bad_pages = 0;  // of the copies in flight, by stage
+    auto load = [&](int i) {
+      const int page = page_of(i), b = first + i * kWarps, stage = (round + i) % S;
+      const bool bad = page < 0 || page >= p.a.pages;
+      bad_pages = (bad_pages & ~(1u << stage)) | ((bad ? 1u : 0u) << stage);
+      if (lane == 0) {
+        const int64_t block = (((int64_t)(bad ? 0 : page) * p.a.Hkv + head) << blocks_log) + (b & ((1 << blocks_log) - 1));
+        mbar_arrive_expect_tx(&full[stage], C::kBlockBytes);
+        bulk_load(ring + stage * C::kBlockBytes, cache + block * C::kBlockBytes, C::kBlockBytes, &full[stage]);
+      }
+    };
+    int loaded = 0;
+    for (; loaded < min(S - 1, count); ++loaded) load(loaded);
+
+    for (int i = 0; i < count; ++i) {
+      if (loaded < count) load(loaded++);  // (into the stage of block i - 1)
+      const int stage = (round + i) % S;
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], ((round + i) / S) & 1, &g_attention_status, kWaitCode))) {
+        alive = false;
+        break;
+      }
+      const uint8_t* kb = ring + stage * C::kBlockBytes;
+      const uint8_t* vb = kb + cache_half_bytes(D);
+      const int tok0 = (first + i * kWarps) * kCacheBlock;
+
+      // S^T = K q^T: rows g, g + 8
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+      {
+        constexpr int kWords = D / 32;  // words of codes per lane and row
+        uint32_t w[2][kWords];
+        uint32_t sc[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int tok = row_token(g + 8 * h);
+          const uint8_t* row = kb + tok * (D / 2) + t * (D / 8);
+#pragma unroll
+          for (int j = 0; j < kWords; j += 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(row + 4 * j);
+            w[h][j] = x.x;
+            w[h][j + 1] = x.y;
+          }
+          const uint8_t* sr = kb + 8 * D + tok * (D / 16) + t * (D / 64);
+          if constexpr (D == 64)
+            sc[h] = *sr;
+          else if constexpr (D == 128)
+            sc[h] = *reinterpret_cast<const uint16_t*>(sr);
+          else
+            sc[h] = *reinterpret_cast<const uint32_t*>(sr);
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          uint32_t x[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t by = key_scale((sc[h] >> (8 * (j / 2))) & 0xffu);
+            e2m1x8_to_half2x4(w[h][j], x[h]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[h][k] = mul_f16x2(x[h][k], by);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t af[4] = {x[0][2 * k], x[1][2 * k], x[0][2 * k + 1], x[1][2 * k + 1]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
+          }
+        }
+      }
+
+      // scores in units of log 2, masked; the running maximum
+      const bool whole = tok0 >= all_lo && tok0 + kCacheBlock - 1 <= pos_first;
+      const bool bad = (bad_pages >> stage) & 1u;
+      float top[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = e & 1, j = tok0 + row_token(g + 8 * (e >> 1));
+          float x = s[n][e] * fac[n][c];
+          if (bad) x = NAN;
+          if (!whole) {
+            const bool sees = j <= last[n][c] && (p.a.window == 0 || j > last[n][c] - p.a.window);
+            if (!sees) x = -INFINITY;
+          }
+          s[n][e] = x;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) top[n][c] = fmaxf(s[n][c], s[n][c + 2]);
+      }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
+      bool grows = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) grows = grows || top[n][c] > m[n][c];
+      if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float next = fmaxf(m[n][c], top[n][c]);
+            const float by = next == -INFINITY ? 1.f : exp2_approx(m[n][c] - next);
+            m[n][c] = next;
+            l[n][c] *= by;
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j) {
+              o[n][j][c] *= by;
+              o[n][j][c + 2] *= by;
+            }
+          }
+        }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float e[4];
+#pragma unroll
+        for (int i4 = 0; i4 < 4; ++i4) {
+          const float from_m = m[n][i4 & 1] == -INFINITY ? 0.f : m[n][i4 & 1];
+          e[i4] = exp2_approx(s[n][i4] - from_m);
+          l[n][i4 & 1] += e[i4];
+        }
+        pf[n][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+        pf[n][1] = transpose8x8(pack_f16x2(e[2], e[3]));
+      }
+
+      // O^T += V^T p^T: columns g D / 8 .. of the values, tokens t, t + 4, t + 8, t + 12 of the block
+      {
+        constexpr int kWords = D / 64;  // words of codes per lane and token
+        uint32_t w[4][kWords];
+        uint32_t sc[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint8_t* row = vb + (t + 4 * k) * (D / 2) + g * (D / 16);
+          const uint8_t* sr = vb + 8 * D + (t + 4 * k) * (D / 16) + g * (D / 8) / 16;
+          if constexpr (D == 64) {
+            w[k][0] = *reinterpret_cast<const uint32_t*>(row);
+            sc[k] = *sr;
+          } else if constexpr (D == 128) {
+            const uint2 x = *reinterpret_cast<const uint2*>(row);
+            w[k][0] = x.x;
+            w[k][1] = x.y;
+            sc[k] = *sr;
+          } else {
+            const uint4 x = *reinterpret_cast<const uint4*>(row);
+            w[k][0] = x.x;
+            w[k][1] = x.y;
+            w[k][2] = x.z;
+            w[k][3] = x.w;
+            sc[k] = *reinterpret_cast<const uint16_t*>(sr);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          uint32_t x[4][4];  // rows of even and odd columns, tokens (t, t + 4); the same, tokens (t + 8, t + 12)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t a = w[2 * k][j], b = w[2 * k + 1][j];
+            const uint32_t even = (a & 0x0f0f0f0fu) | ((b & 0x0f0f0f0fu) << 4);
+            const uint32_t odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+            const uint32_t by = value_scales((sc[2 * k] >> (8 * (j / 2))) & 0xffu, (sc[2 * k + 1] >> (8 * (j / 2))) & 0xffu);
+            e2m1x8_to_half2x4(even, x[2 * k]);
+            e2m1x8_to_half2x4(odd, x[2 * k + 1]);
+#pragma unroll
+            for (int i4 = 0; i4 < 4; ++i4) {
+              x[2 * k][i4] = mul_f16x2(x[2 * k][i4], by);
+              x[2 * k + 1][i4] = mul_f16x2(x[2 * k + 1][i4], by);
+            }
+          }
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            const uint32_t af[4] = {x[0][i4], x[1][i4], x[2][i4], x[3][i4]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i4], af, pf[n][0], pf[n][1]);
+          }
+        }
+      }
+      __syncwarp();  // the block is read: its stage may be loaded anew
+    }
+    round += count;
+
+    // the warps' sums, joined
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
+    float* sums = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float* row = sums + (8 * n + 2 * t + c) * C::kRow + g * (D / 8);
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) *reinterpret_cast<float2*>(row + 2 * j) = make_float2(o[n][j][c], o[n][j][c + 2]);
+        if (g == 0) {
+          stats[(warp * kRows + 8 * n + 2 * t + c) * 2] = m[n][c];
+          stats[(warp * kRows + 8 * n + 2 * t + c) * 2 + 1] = l[n][c];
+        }
+      }
+    __syncthreads();
+    const bool is_whole = from == 0 && to == span.units;
+    const int part = 2 * (int)blockIdx.x + (from == 0 ? 1 : 0);
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = 4 * (i % (D / 4));
+      if (row >= rows) break;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[(w * kRows + row) * 2]);
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = stats[(w * kRows + row) * 2];
+        const float by = mw == -INFINITY ? (top == -INFINITY ? 1.f : 0.f) : exp2_approx(mw - top);
+        // (a warp whose maximum is -inf has sums of zero, or NaN from NaN scores)
+        const float lw = stats[(w * kRows + row) * 2 + 1];
+        const float4 v = *reinterpret_cast<const float4*>(smem + w * C::kRing + (row * C::kRow + d) * 4);
+        sum += lw * by;
+        acc.x += v.x * by;
+        acc.y += v.y * by;
+        acc.z += v.z * by;
+        acc.w += v.w * by;
+      }
+      if (!is_whole) {
+        float* dst = p.parts + ((int64_t)part * kRows + row) * D + d;
+        *reinterpret_cast<float4*>(dst) = acc;
+        if (d == 0) {
+          float* st = p.parts + (int64_t)2 * p.workers * kRows * D + ((int64_t)part * kRows + row) * 2;
+          st[0] = top;
+          st[1] = sum;
+        }
+        continue;
+      }
+      const int rr = tile * kRows + row, token = q.row0 + rr / p.group, hq = head * p.group + rr % p.group;
+      float scale_up = 1.f;
+      if (p.a.sinks) {
+        const float sink = p.a.sinks[hq] * to_log2, next = fmaxf(top, sink);
+        if (next != -INFINITY) {
+          scale_up = top == -INFINITY ? (sum == sum ? 0.f : 1.f) : exp2_approx(top - next);
+          sum = sum * scale_up + exp2_approx(sink - next);
+          top = next;
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : p.a.v_scale * scale_up / sum;
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)token * p.a.out_row + (int64_t)hq * p.a.out_head + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      if (p.a.lse && d == 0)
+        p.a.lse[(int64_t)token * p.a.Hq + hq] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.6931471805599453f + logf(sum);
+    }
+    fence_proxy_async_smem();  // the sums lie where the next copies go
+    __syncthreads();
+    rest = (int64_t)head * span.units + to;
+    for (int i = 0; i < tile; ++i) rest += (int64_t)attn_span<kUnit>(p, q, i * kRows, kRows).units * p.a.Hkv;
+  }
+}
+
+// Joins the parts of the items that workers share, in the workers' order, and
+// writes the rows that no worker has: queries that see no key, and rows
+// behind the last sequence.  A warp per row (token, head).
+template <int D, int kRows, int kUnits>
+__global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p) {
+  constexpr int kCols = D / 32;  // of a lane
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+  if (id >= (int64_t)p.a.T * p.a.Hq) return;
+  const int token = (int)(id / p.a.Hq), hq = (int)(id % p.a.Hq), head = hq / p.group;
+  const int64_t units = p.prefix[p.a.R];
+  float acc[kCols] = {}, top = -INFINITY, sum = 0.f;
+  if (p.a.R > 0 && token >= p.a.offsets[0] && token < p.a.offsets[p.a.R]) {
+    int lo = 0, hi = p.a.R;  // offsets[lo] <= token < offsets[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.a.offsets[mid] <= token)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const AttnRequest q = attn_request(p, lo);
+    const int rr = (token - q.row0) * p.group + hq % p.group, tile = rr / kRows, row = rr % kRows;
+    int64_t u0 = p.prefix[lo];
+    for (int i = 0; i < tile; ++i) u0 += (int64_t)attn_span<kUnits>(p, q, i * kRows, kRows).units * p.a.Hkv;
+    const AttnSpan span = attn_span<kUnits>(p, q, tile * kRows, kRows);
+    u0 += (int64_t)head * span.units;
+    if (span.units > 0) {
+      const int workers = attn_workers(p, units);
+      const int w0 = attn_owner(u0, units, workers), w1 = attn_owner(u0 + span.units - 1, units, workers);
+      if (w0 == w1) return;  // that worker has written it
+      const float* st = p.parts + (int64_t)2 * p.workers * kRows * D;
+      for (int w = w0; w <= w1; ++w) {
+        const int64_t at = ((int64_t)2 * w + (w == w0 ? 1 : 0)) * kRows + row;
+        const float mw = st[2 * at], lw = st[2 * at + 1], next = fmaxf(top, mw);
+        const float old_by = top == next ? 1.f : exp2_approx(top - next);
+        const float new_by = mw == next ? 1.f : exp2_approx(mw - next);
+        top = next;
+        sum = sum * old_by + lw * new_by;
+        const float* src = p.parts + at * D + lane * kCols;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) acc[c] = acc[c] * old_by + src[c] * new_by;
+      }
+    }
+  }
+  const bool in_batch = p.a.R > 0 && token >= p.a.offsets[0] && token < p.a.offsets[p.a.R];
+  float scale_up = 1.f;
+  if (p.a.sinks && in_batch) {
+    const float sink = p.a.sinks[hq] * 1.4426950408889634f, next = fmaxf(top, sink);
+    if (next != -INFINITY) {
+      scale_up = top == -INFINITY ? (sum == sum ? 0.f : 1.f) : exp2_approx(top - next);
+      sum = sum * scale_up + exp2_approx(sink - next);
+      top = next;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : p.a.v_scale * scale_up / sum;
+  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)token * p.a.out_row +
+                                                          (int64_t)hq * p.a.out_head + lane * kCols);
+#pragma unroll
+  for (int c = 0; c < kCols / 2; ++c) out[c] = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  if (p.a.lse && lane == 0)
+    p.a.lse[id] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.6931471805599453f + logf(sum);
+}
+
+int max_workers(int sms, int D, int NT) { return sms * (D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2); }
+
+template <int D, int NT>
+cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
+  using C = Cfg<D, NT>;
+  static bool seen[64];
+  cudaError_t e = allow_smem(attention_rows_kernel<D, NT>, C::kSmem, seen);
+  if (e != cudaSuccess) return e;
+  p.workers = max_workers(sms, D, NT);
+  p.least = 2;
+  e = launch_dependent_smem(attention_rows_kernel<D, NT>, (unsigned)p.workers, kThreads, C::kSmem, st, p);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)p.a.T * p.a.Hq;
+  return launch_dependent(attention_join_kernel<D, C::kRows, kUnit>, (unsigned)((rows + 7) / 8), 256, st, p);
+}
+
+template <int D>
+cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
+  // rows that an average request has to a key head
+  const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
+  return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);
+}
+
+size_t prefix_bytes(int R) { return (((size_t)R + 1) * 8 + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attention_workspace_bytes(int R, int, int, int D) {
+  int sms = 0;
+  if (current_device_sms(&sms) != cudaSuccess) sms = 152;
+  size_t parts = 0;
+  for (int NT = 1; NT <= 2; ++NT) {
+    const size_t n = (size_t)2 * max_workers(sms, D, NT) * 8 * NT * (D + 2) * 4;
+    parts = n > parts ? n : parts;
+  }
+  return prefix_bytes(R) + (parts + 255) / 256 * 256;
+}
+
+cudaError_t launch_attention(const moe_fp4_attention_args& a, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = current_device_sms(&sms);
+  if (e != cudaSuccess) return e;
+  AttnArgs p = {};
+  p.a = a;
+  p.group = a.Hq / a.Hkv;
+  p.capacity = a.table_width * a.page_size;
+  p.prefix = static_cast<int64_t*>(a.workspace);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + prefix_bytes(a.R));
+  switch (a.D) {
+    case 64: return launch_dim<64>(p, sms, st);
+    case 128: return launch_dim<128>(p, sms, st);
+    default: return launch_dim<256>(p, sms, st);
+  }
+}
+
+}  // namespace moe_fp4

@@ -8,6 +8,8 @@ residual stream and ``forward``:
   ``fp8_matmul``    128 x 128 block (the always-on expert, projections), from
   ``fp8_quantize``  BF16 or already quantised activations.
 
+Those of the attention over a paged cache in 4 bits are in ``attention``.
+
 Thin wrappers of the C entry points of include/moe_fp4.h: they check types and
 shapes, allocate outputs, and launch on the current stream (or ``stream``).
 """

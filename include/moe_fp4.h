@@ -727,6 +727,166 @@ MOE_FP4_API int moe_fp4_route_topk(const void *logits, int64_t logits_row, int l
                                    int score, int renormalize, float scale, int32_t *topk_ids, float *topk_weights,
                                    int M, int E, int top_k, void *stream);
 
+/*
+ * ---- The attention's side of a block: a cache in 4 bits ------------------
+ *
+ * What a served block does between its projections and its attention's
+ * output.  The cache is paged: pages of page_size tokens (16, 32, 64 or 128)
+ * hold, for each key head and each 16 tokens, first their keys, then their
+ * values, each as 16 rows of D / 2 bytes (E2M1, the even column in the low
+ * nibble) and then 16 rows of D / 16 scales (E4M3, one per 16 columns):
+ *     cache [pages][kv_heads][page_size / 16][2][9 D] bytes
+ * An element's value is e2m1 * e4m3 * (k_scale or v_scale), these two FP32
+ * numbers of the caller's.  A slot is page * page_size + the token's place in
+ * the page.  Head dimensions D are 64, 128 and 256 (MOE_FP4_EUNSUPPORTED
+ * otherwise, as for other page sizes).  As above: strides in elements,
+ * columns contiguous, device pointers, no allocation, capturable.  Inference
+ * only, like the layer.  The pages have no counterpart of these.
+ */
+
+/*
+ * One step of a batch whose rows are requests: pages for the new tokens and
+ * where each of them goes.  Request r has lengths[r] tokens in the cache, on
+ * the pages tables[r][0 .. ceil(lengths[r] / page_size)), and new_tokens[r]
+ * more to come; free_pages[0 .. free_count) is a stack of free pages.
+ *   1. The pages of each request r with finished[r] (finished: a byte per
+ *      request, or NULL) are pushed on the stack, in the order of r and of
+ *      the table; its length counts as 0 from there on.
+ *   2. In the order of r, each request takes the pages that its new tokens
+ *      need from the stack's top and appends them to its table row.  A
+ *      request whose pages the stack does not hold any more (its own and
+ *      those that the requests before it asked for exceed what is there), or
+ *      whose tokens exceed its table row, is refused: it takes none.
+ * Out: offsets [R + 1], the sums of new_tokens before each request (of
+ * refused ones too); for each token t < tokens, positions[t] (its place in
+ * its sequence) and slots[t] (-1 where its request was refused); both for
+ * tokens behind offsets[R] 0 and -1; accepted[r], new_tokens[r] or 0;
+ * lengths_out[r], the length with the accepted tokens; free_count_out.
+ * tables and free_pages are updated in place; lengths_out and free_count_out
+ * may be lengths and free_count.  Negative lengths and counts are taken as 0,
+ * free_count at most as free_capacity, the size of free_pages (pages pushed
+ * past it are lost).  tokens < offsets[R] leaves the others out.  Sums must
+ * be below 2^31.  R, tokens >= 0; R <= 65536 (MOE_FP4_EUNSUPPORTED).
+ */
+typedef struct moe_fp4_cache_step_args {
+  const int32_t *lengths, *new_tokens;
+  const uint8_t *finished;
+  int32_t *tables;
+  int64_t table_row;
+  int32_t *free_pages;
+  const int32_t *free_count;
+  int32_t *offsets, *positions;
+  int64_t *slots;
+  int32_t *lengths_out, *free_count_out, *accepted;
+  int table_width, free_capacity, page_size, R, tokens;
+} moe_fp4_cache_step_args;
+MOE_FP4_API int moe_fp4_cache_step(const moe_fp4_cache_step_args *args, void *stream);
+
+/*
+ * The norms of queries and keys for each head, and the rotation of their
+ * first rot columns by the angles of the token's position:
+ *     y = x * rsqrt(mean(x^2) + eps) * (offset + w)      (w NULL: y = x)
+ *     a' = a c - b s,  b' = b c + a s
+ * with c = rotary[position][i], s = rotary[position][rot / 2 + i] (FP32) for
+ * i < rot / 2, and (a, b) the columns i and i + rot / 2, or 2i and 2i + 1
+ * (interleaved).  rotary NULL: no rotation.  A position outside [0,
+ * positions_max) makes its token's rotated columns NaN.
+ * q_in [T][Hq][D] and k_in, v_in [T][Hkv][D] are bf16 with strides per token
+ * and per head; q_out is bf16 [T][Hq][D] with its own.  Then either
+ *   cache NULL: k_out, bf16 [T][Hkv][D]; v_in is not read; or
+ *   the keys' results and the values as they are go into the cache at
+ *   slots[t] (a slot that is negative or past the cache: not stored; two
+ *   tokens must not name one slot), each 16 columns v by
+ *     u = v / (k_scale or v_scale),  s = e4m3_rn(min(max|u| / 6, 448)),
+ *     code = e2m1_rn(u / s)  (0 where s is 0),
+ *   each step an IEEE FP32 operation.  A block of values with an infinity or
+ *   a NaN gets the scale NaN, and so does every block of a token's key where
+ *   its key or its values of that head have one.  k_out is not written.
+ * Arithmetic is FP32 with one rounding to bf16; the keys on their way to the
+ * cache carry twice that, so that what is quantised is the FP32 number next
+ * to the formula's (of offset + w, rounded to FP32) and its codes do not
+ * depend on the order of sums.
+ * w_q, w_k [D] bf16, or f32 (weights_f32).  positions int32 or int64
+ * (positions_i64), slots int64.  rot % 16 == 0, rot <= D
+ * (MOE_FP4_EUNSUPPORTED).  16-byte aligned arrays, strides that are
+ * multiples of 8 elements; k_scale, v_scale positive and finite; eps >= 0
+ * (MOE_FP4_EINVAL).  q_out may be q_in, k_out k_in (same strides).
+ */
+typedef struct moe_fp4_qk_norm_rope_args {
+  const void *q_in, *k_in, *v_in;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  const void *w_q, *w_k;
+  const float *rotary;
+  const void *positions;
+  void *q_out, *k_out;
+  int64_t q_out_row, q_out_head, k_out_row, k_out_head;
+  void *cache;
+  const int64_t *slots;
+  float eps, offset, k_scale, v_scale;
+  int weights_f32, interleaved, positions_i64, positions_max;
+  int T, Hq, Hkv, D, rot, pages, page_size;
+} moe_fp4_qk_norm_rope_args;
+MOE_FP4_API int moe_fp4_qk_norm_rope(const moe_fp4_qk_norm_rope_args *args, void *stream);
+
+/*
+ * What the cache holds at slots[0 .. T): k_out and v_out bf16 [T][Hkv][D]
+ * dense, the FP32 product e2m1 * e4m3 * scale rounded to bf16; zeros for a slot that is negative
+ * or past the cache.  16-byte aligned outputs (MOE_FP4_EINVAL).
+ */
+MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, int Hkv, int D, const int64_t *slots,
+                                   float k_scale, float v_scale, void *k_out, void *v_out, int T, void *stream);
+
+/*
+ * Attention of new tokens over the cache.  Request r has lengths[r] tokens
+ * there (its new ones among them) on the pages of tables[r]; its queries are
+ * the rows offsets[r] .. offsets[r + 1) of q, n of them, for its last n
+ * tokens.  Query i stands at p = lengths[r] - n + i and sees the keys j with
+ * p - window < j <= p (window 0: all j <= p).  Head h reads key head h / (Hq
+ * / Hkv).
+ *     x_j = scale * k_scale * q . k_j,
+ *     out = v_scale * sum_j e^x_j v_j / (sum_j e^x_j + e^sinks[h])
+ * over the keys it sees (sinks f32 [Hq], or NULL: without that term), lse =
+ * log of that divisor (f32 [T][Hq] dense, or NULL).  A query that sees no key
+ * (p < 0) gets out 0 and lse sinks[h], or -inf.  Rows of q behind
+ * offsets[R] get 0 and -inf.  What lies in the cache outside the keys a query
+ * sees does not touch its output, NaN included.  A key with a NaN scale makes
+ * the queries that see it NaN; NaN scales of values count as 0 (the store
+ * above marks the keys of a token with non-finite values, too).  A page
+ * number outside [0, pages) reads as NaN keys.  Tokens past table_width *
+ * page_size are not looked for.
+ * Queries, 4-bit keys and values enter the products exactly (q in FP16
+ * scaled by a power of two per row: exact to 2^-39 of the row's largest),
+ * the probabilities in FP16; sums, maxima and divisors are FP32.  Results are
+ * deterministic for given inputs and device.
+ * q and out: bf16 [T][Hq][D], 16-byte aligned, strides multiples of 8
+ * elements (MOE_FP4_EINVAL); Hq % Hkv == 0, Hq / Hkv <= 64, R <= 65536
+ * (MOE_FP4_EUNSUPPORTED).  workspace: moe_fp4_attention_workspace_bytes
+ * bytes, 256-byte aligned, no initialisation needed; calls that may run at
+ * the same time need workspaces of their own.
+ */
+typedef struct moe_fp4_attention_args {
+  const void *q;
+  int64_t q_row, q_head;
+  const void *cache;
+  const int32_t *tables;
+  int64_t table_row;
+  const int32_t *lengths, *offsets;
+  const float *sinks;
+  void *out;
+  int64_t out_row, out_head;
+  float *lse;
+  void *workspace;
+  size_t workspace_bytes;
+  float scale, k_scale, v_scale;
+  int window;
+  int T, R, Hq, Hkv, D, pages, page_size, table_width;
+} moe_fp4_attention_args;
+MOE_FP4_API size_t moe_fp4_attention_workspace_bytes(int R_max, int Hq, int Hkv, int D);
+MOE_FP4_API int moe_fp4_attention(const moe_fp4_attention_args *args, void *stream);
+/* Status word of the attention kernels' bounded waits on the current device
+ * (as moe_fp4_fp8_status). */
+MOE_FP4_API int moe_fp4_attention_status(uint32_t *flags, int clear, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -45,24 +45,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // Two E4M3 scales as an FP16 pair, NaN as 0.
 __device__ __forceinline__ uint32_t value_scales(uint32_t lo, uint32_t hi) {
   if ((lo & 0x7fu) == 0x7fu) lo = 0;
@@ -78,13 +60,6 @@ __device__ __forceinline__ uint32_t key_scale(uint32_t b) {
   return r;
 }
 
-// The exponent that brings a row's largest |q| to [2^14, 2^15), as 2^-e, 2^e.
-__device__ __forceinline__ float row_scale(float top, float& back) {
-  const int e = min(max((int)((__float_as_uint(top) >> 23) & 0xff) - 127 - 14, -100), 100);
-  back = __uint_as_float((uint32_t)(127 + e) << 23);
-  return __uint_as_float((uint32_t)(127 - e) << 23);
-}
-
 // The token of a block that row i of its 16 stands for.
 __device__ __forceinline__ int row_token(int i) { return (i & 8) + ((i & 7) >> 1) + 4 * (i & 1); }
 
@@ -98,14 +73,8 @@ struct Cfg {
   static_assert(kRows * kRow * 4 <= kRing, "a warp's sums lie in its ring");
   static constexpr int kBarriers = kWarps * kStages * 8;
   static constexpr int kStats = kWarps * kRows * 2 * 4;
-  static constexpr int kSmem = kWarps * kRing + kBarriers + kStats + 128;
+  static constexpr int kSmem = kWarps * kRing + kBarriers + kStats;
   static constexpr int kCtas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;  // per SM
-};
-
-// A worker's place in the line of units.
-struct Place {
-  int r;
-  int64_t rest;  // units of the request before the worker's first
 };
 
 template <int D, int NT>
@@ -116,8 +85,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * C::kRing);
   float* stats = reinterpret_cast<float*>(smem + kWarps * C::kRing + C::kBarriers);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + kWarps * C::kRing + C::kBarriers + C::kStats);
-  __shared__ Place s_place;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * C::kRing;
   uint64_t* full = bars + warp * S;
@@ -128,62 +95,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   pdl_wait();
   pdl_launch_dependents();
 
-  // the line of units, and this worker's stretch
-  const int each = ceil_div(max(p.a.R, 1), kThreads);
-  const int r0 = min((int)threadIdx.x * each, p.a.R), r1 = min(r0 + each, p.a.R);
-  int64_t mine = 0, units;
-  for (int r = r0; r < r1; ++r) mine += attn_units<kRows, kUnit>(p, r);
-  const int64_t before = block_before<kThreads>(mine, &units, scan);
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int r = r0; r < r1; ++r) {
-      p.prefix[r] = at;
-      at += attn_units<kRows, kUnit>(p, r);
-    }
-    if (threadIdx.x == 0) p.prefix[p.a.R] = units;
-  }
-  const int workers = attn_workers(p, units);
-  if (units == 0 || (int)blockIdx.x >= workers) return;
-  int64_t u = attn_start(blockIdx.x, units, workers);
-  const int64_t u_end = attn_start(blockIdx.x + 1, units, workers);
-  if (before <= u && u < before + mine) {
-    int64_t at = before;
-    for (int r = r0; r < r1; ++r) {
-      const int64_t n = attn_units<kRows, kUnit>(p, r);
-      if (u < at + n) {
-        s_place = {r, u - at};
-        break;
-      }
-      at += n;
-    }
-  }
-  __syncthreads();
-  int r = s_place.r;
-  int64_t rest = s_place.rest;
+  AttnCursor<kRows, kUnit> c;
+  int64_t u, u_end;
+  if (!attn_stretch<kRows, kUnit, kThreads>(p, c, u, u_end)) return;
 
   const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
   const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);  // blocks of a page
-  const float to_log2 = 1.4426950408889634f;
   int round = 0;  // copies of this warp so far: stage round % S, phase round / S
   bool alive = true;
 
   while (u < u_end) {
-    // the item
-    const AttnRequest q = attn_request(p, r);
-    const int tiles = attn_tiles<kRows>(p, q);
-    int tile = 0;
-    AttnSpan span = {0, 0, 0, 0};
-    for (; tile < tiles; ++tile) {
-      span = attn_span<kUnit>(p, q, tile * kRows, kRows);
-      if (rest < (int64_t)span.units * p.a.Hkv) break;
-      rest -= (int64_t)span.units * p.a.Hkv;
-    }
-    if (tile == tiles) {  // (nothing is left of this request)
-      ++r;
-      rest = 0;
-      continue;
-    }
-    const int head = (int)(rest / span.units), from = (int)(rest - (int64_t)head * span.units);
+    const AttnRequest q = c.q;
+    const AttnSpan span = c.span;
+    const int r = c.r, tile = c.tile, head = c.head, from = c.from;
     const int to = (int)min((int64_t)span.units, from + u_end - u);
     u += to - from;
 
@@ -192,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     float fac[NT][2];
     int last[NT][2];  // position of the columns' queries, -1: no row
     const int base_pos = q.length - q.n;
-    const int rows = min((int64_t)kRows, (int64_t)q.n * p.group - (int64_t)tile * kRows);
+    const int rows = c.rows(p);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int row = tile * kRows + 8 * n + g;
@@ -223,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        fac[n][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c)) * (p.a.scale * p.a.k_scale * to_log2);
+        fac[n][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c)) * (p.a.scale * p.a.k_scale * kLog2e);
         const int col = 8 * n + 2 * t + c;
         last[n][c] = col < rows ? base_pos + (tile * kRows + col) / p.group : -1;
       }
@@ -486,103 +410,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         acc.w += v.w * by;
       }
       if (!is_whole) {
-        float* dst = p.parts + ((int64_t)part * kRows + row) * D + d;
-        *reinterpret_cast<float4*>(dst) = acc;
-        if (d == 0) {
-          float* st = p.parts + (int64_t)2 * p.workers * kRows * D + ((int64_t)part * kRows + row) * 2;
-          st[0] = top;
-          st[1] = sum;
-        }
+        *reinterpret_cast<float4*>(p.parts + ((int64_t)part * kRows + row) * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(attn_stats<D, kRows>(p, part, row)) = make_float2(top, sum);
         continue;
       }
       const int rr = tile * kRows + row, token = q.row0 + rr / p.group, hq = head * p.group + rr % p.group;
-      float scale_up = 1.f;
-      if (p.a.sinks) {
-        const float sink = p.a.sinks[hq] * to_log2, next = fmaxf(top, sink);
-        if (next != -INFINITY) {
-          scale_up = top == -INFINITY ? (sum == sum ? 0.f : 1.f) : exp2_approx(top - next);
-          sum = sum * scale_up + exp2_approx(sink - next);
-          top = next;
-        }
-      }
-      const float inv = sum == 0.f ? 0.f : p.a.v_scale * scale_up / sum;
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)token * p.a.out_row + (int64_t)hq * p.a.out_head + d) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      if (p.a.lse && d == 0)
-        p.a.lse[(int64_t)token * p.a.Hq + hq] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.6931471805599453f + logf(sum);
+      float lse;
+      const float inv = attn_finish(p, hq, top, sum, lse);
+      *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (p.a.lse && d == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
     }
     fence_proxy_async_smem();  // the sums lie where the next copies go
     __syncthreads();
-    rest = (int64_t)head * span.units + to;
-    for (int i = 0; i < tile; ++i) rest += (int64_t)attn_span<kUnit>(p, q, i * kRows, kRows).units * p.a.Hkv;
+    if (u < u_end) c.next(p);
   }
-}
-
-// Joins the parts of the items that workers share, in the workers' order, and
-// writes the rows that no worker has: queries that see no key, and rows
-// behind the last sequence.  A warp per row (token, head).
-template <int D, int kRows, int kUnits>
-__global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p) {
-  constexpr int kCols = D / 32;  // of a lane
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t id = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
-  if (id >= (int64_t)p.a.T * p.a.Hq) return;
-  const int token = (int)(id / p.a.Hq), hq = (int)(id % p.a.Hq), head = hq / p.group;
-  const int64_t units = p.prefix[p.a.R];
-  float acc[kCols] = {}, top = -INFINITY, sum = 0.f;
-  if (p.a.R > 0 && token >= p.a.offsets[0] && token < p.a.offsets[p.a.R]) {
-    int lo = 0, hi = p.a.R;  // offsets[lo] <= token < offsets[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.a.offsets[mid] <= token)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const AttnRequest q = attn_request(p, lo);
-    const int rr = (token - q.row0) * p.group + hq % p.group, tile = rr / kRows, row = rr % kRows;
-    int64_t u0 = p.prefix[lo];
-    for (int i = 0; i < tile; ++i) u0 += (int64_t)attn_span<kUnits>(p, q, i * kRows, kRows).units * p.a.Hkv;
-    const AttnSpan span = attn_span<kUnits>(p, q, tile * kRows, kRows);
-    u0 += (int64_t)head * span.units;
-    if (span.units > 0) {
-      const int workers = attn_workers(p, units);
-      const int w0 = attn_owner(u0, units, workers), w1 = attn_owner(u0 + span.units - 1, units, workers);
-      if (w0 == w1) return;  // that worker has written it
-      const float* st = p.parts + (int64_t)2 * p.workers * kRows * D;
-      for (int w = w0; w <= w1; ++w) {
-        const int64_t at = ((int64_t)2 * w + (w == w0 ? 1 : 0)) * kRows + row;
-        const float mw = st[2 * at], lw = st[2 * at + 1], next = fmaxf(top, mw);
-        const float old_by = top == next ? 1.f : exp2_approx(top - next);
-        const float new_by = mw == next ? 1.f : exp2_approx(mw - next);
-        top = next;
-        sum = sum * old_by + lw * new_by;
-        const float* src = p.parts + at * D + lane * kCols;
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) acc[c] = acc[c] * old_by + src[c] * new_by;
-      }
-    }
-  }
-  const bool in_batch = p.a.R > 0 && token >= p.a.offsets[0] && token < p.a.offsets[p.a.R];
-  float scale_up = 1.f;
-  if (p.a.sinks && in_batch) {
-    const float sink = p.a.sinks[hq] * 1.4426950408889634f, next = fmaxf(top, sink);
-    if (next != -INFINITY) {
-      scale_up = top == -INFINITY ? (sum == sum ? 0.f : 1.f) : exp2_approx(top - next);
-      sum = sum * scale_up + exp2_approx(sink - next);
-      top = next;
-    }
-  }
-  const float inv = sum == 0.f ? 0.f : p.a.v_scale * scale_up / sum;
-  __nv_bfloat162* out = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)token * p.a.out_row +
-                                                          (int64_t)hq * p.a.out_head + lane * kCols);
-#pragma unroll
-  for (int c = 0; c < kCols / 2; ++c) out[c] = __floats2bfloat162_rn(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-  if (p.a.lse && lane == 0)
-    p.a.lse[id] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * 0.6931471805599453f + logf(sum);
 }
 
 int max_workers(int sms, int D, int NT) { return sms * (D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2); }
@@ -597,14 +439,14 @@ cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
   p.least = 2;
   e = launch_dependent_smem(attention_rows_kernel<D, NT>, (unsigned)p.workers, kThreads, C::kSmem, st, p);
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)p.a.T * p.a.Hq;
-  return launch_dependent(attention_join_kernel<D, C::kRows, kUnit>, (unsigned)((rows + 7) / 8), 256, st, p);
+  return launch_attention_join<D, C::kRows, kUnit>(p, st);
 }
 
 template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
   // rows that an average request has to a key head
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
+  if (rows > 32) return launch_attention_tc(p, sms, st);
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);
 }
 
@@ -615,7 +457,7 @@ size_t prefix_bytes(int R) { return (((size_t)R + 1) * 8 + 255) / 256 * 256; }
 size_t attention_workspace_bytes(int R, int, int, int D) {
   int sms = 0;
   if (current_device_sms(&sms) != cudaSuccess) sms = 152;
-  size_t parts = 0;
+  size_t parts = attention_tc_parts_bytes(D, sms);
   for (int NT = 1; NT <= 2; ++NT) {
     const size_t n = (size_t)2 * max_workers(sms, D, NT) * 8 * NT * (D + 2) * 4;
     parts = n > parts ? n : parts;

@@ -1,0 +1,530 @@
+// Attention over the paged cache of 4 bits for many rows to a key head
+// (prompts and their chunks), on the 5th-generation tensor cores (sm_103a).
+//
+// A CTA takes kTiles tiles of 128 rows (query and head of a group each) over a
+// key head's tokens, kTok at a time (a step):
+//   softmax warps  (four per tile of rows, or of one tile) own a row per
+//                  thread: they bring q to shared memory as FP16, scaled by a
+//                  power of two per row; read a step's scores from tensor
+//                  memory, take the running maximum, and put p = 2^(x - m)
+//                  back over them in FP16, the second product's A operand;
+//                  at the end they read the sums and write the rows out;
+//   decode warps   turn the cache's codes into FP16 (exact: at most six
+//                  significant bits in [2^-10, 2688]) in shared memory, in the
+//                  128-byte-swizzled layout that the products read: keys
+//                  K-major, values as they lie, N-major;
+//   MMA warp       converged, issues S = Q K^T into tensor memory and O += P V
+//                  (P from tensor memory) as their operands come;
+//   load warp      a block's half (keys or values of 16 tokens) to a bulk
+//                  copy, a lane each, into a ring of half steps.
+// With two tiles each has its scores; while one's softmax runs, the other's
+// products do.  With one (D = 256, whose sums take half of tensor memory) two
+// buffers of scores alternate between steps.
+//
+// The maximum follows the scores only when they outgrow it by 2^8 (p stays
+// within FP16, sums and divisor are taken against the same m), so that the
+// sums in tensor memory are hardly ever rescaled.
+#include "attention_work.cuh"
+#include "gemm_f16w4.cuh"
+#include "gemm_fp8.cuh"
+
+namespace moe_fp4 {
+
+namespace {
+
+template <int D>
+struct TcCfg {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kTok = D <= 128 ? 128 : 64;
+  static constexpr int kBlocks = kTok / kCacheBlock;
+  static constexpr uint32_t kQTile = 128 * D * 2;
+  static constexpr uint32_t kKv = kTok * D * 2;  // decoded keys or values of a step
+  static constexpr uint32_t kPanel = kTok * 128;    // 64 columns of them: swizzled rows of 128 bytes
+  static constexpr uint32_t kHalf = kBlocks * cache_half_bytes(D);
+  static constexpr int kRaw = D == 64 ? 6 : 3;   // half steps in flight
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kDecWarps = kTiles == 2 ? 4 : 8;
+  static constexpr int kThreads = 32 * 16;       // (whole warpgroups, for the split of registers)
+  static constexpr int kMmaWarp = 12, kLoadWarp = 13;
+  static constexpr uint32_t kTmemO = 2 * 128;    // the sums lie behind two buffers of scores
+  static constexpr uint32_t kBytes = kTiles * kQTile + 4 * kKv + kRaw * kHalf;
+  static constexpr uint32_t kBarBytes = 512;
+  static constexpr uint32_t kSmem = kBytes + kBarBytes + 1024 /*align*/;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kTmemO + kTiles * D <= 512, "tensor memory");
+  static_assert(kSoftWarps + kDecWarps == 12, "three warpgroups, then MMA and loads");
+};
+
+// Shared-memory descriptor of an operand whose rows of 128 bytes are its
+// N direction (64 values) and go along K: 8 rows to a swizzled group of 1024
+// bytes, `panel` bytes to the next 64 values.
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t panel) {
+  return smem_desc(saddr, panel, 1024, kLayoutSW128);
+}
+
+// D (+)= A B with A (FP16, a row per lane, two values a column) in tensor
+// memory, from a converged warp.
+__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2,%3};\n\tmov.b64 rb, {%4,%5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0,%1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+constexpr uint32_t kTcWait = 2u;
+
+template <int D>
+__global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(AttnArgs p, uint32_t* err) {
+  using C = TcCfg<D>;
+  constexpr int kTok = C::kTok, kTiles = C::kTiles;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* q_smem = smem;
+  uint8_t* k_smem = q_smem + kTiles * C::kQTile;  // two buffers
+  uint8_t* v_smem = k_smem + 2 * C::kKv;          // two buffers
+  uint8_t* raw = v_smem + 2 * C::kKv;
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw + C::kRaw * C::kHalf);
+  uint64_t* raw_empty = raw_full + C::kRaw;
+  uint64_t* kv_full = raw_empty + C::kRaw;  // [keys 0, keys 1, values 0, values 1]
+  uint64_t* kv_empty = kv_full + 4;
+  uint64_t* s_full = kv_empty + 4;  // [2] scores of a buffer are there
+  uint64_t* p_full = s_full + 2;    // [2] probabilities are
+  uint64_t* pv_done = p_full + 2;   // [2] sums of a tile are
+  uint64_t* q_full = pv_done + 2;   // [2] a tile's queries are there, and its sums read
+  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(q_full + 2);  // [kRaw]
+  uint32_t* tmem_slot = bad_blocks + C::kRaw;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], C::kDecWarps);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&kv_full[i], C::kDecWarps);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&q_full[i], 4);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  AttnCursor<C::kRows, kTok> c;
+  int64_t u, u_end;
+  if (!attn_stretch<C::kRows, kTok, C::kThreads>(p, c, u, u_end)) return;
+
+  if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, err, kTcWait));
+  };
+
+  if (warp >= C::kSoftWarps + C::kDecWarps) {
+    regs_dec<64>();
+    if (warp == C::kLoadWarp) {
+      const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
+      const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);
+      uint32_t half = 0;
+      bool ok = true;
+      while (ok && u < u_end) {
+        const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+        const int end_block = (c.span.hi + kCacheBlock - 1) / kCacheBlock;
+        const int32_t* table = p.a.tables + (int64_t)c.r * p.a.table_row;
+        int b = (c.span.first + c.from) * C::kBlocks + lane;
+        auto page_of = [&](int block) { return lane < C::kBlocks && block < end_block ? table[block >> blocks_log] : 0; };
+        int page = page_of(b);
+        for (int i = 0; i < steps; ++i, b += C::kBlocks) {
+          const bool mine = lane < C::kBlocks && b < end_block;
+          const bool bad = mine && (page < 0 || page >= p.a.pages);
+          const int64_t at = ((((int64_t)(bad ? 0 : page) * p.a.Hkv + c.head) << blocks_log) + (b & ((1 << blocks_log) - 1))) *
+                             cache_block_bytes(D);
+          const unsigned real = __ballot_sync(0xffffffffu, mine), wrong = __ballot_sync(0xffffffffu, bad);
+          page = i + 1 < steps ? page_of(b + C::kBlocks) : 0;
+          for (int kind = 0; ok && kind < 2; ++kind, ++half) {
+            const uint32_t s = half % C::kRaw, round = half / C::kRaw;
+            if (round > 0 && !wait(&raw_empty[s], round - 1)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              bad_blocks[s] = wrong;
+              mbar_arrive_expect_tx(&raw_full[s], __popc(real) * cache_half_bytes(D));
+            }
+            __syncwarp();
+            if (mine)
+              bulk_load(raw + s * C::kHalf + lane * cache_half_bytes(D), cache + at + kind * cache_half_bytes(D),
+                        cache_half_bytes(D), &raw_full[s]);
+          }
+          if (!ok) break;
+        }
+        u += steps;
+        if (u < u_end) c.next(p);
+      }
+    } else if (warp == C::kMmaWarp) {
+      const uint32_t idesc_s = idesc_f16(128, kTok), idesc_o = idesc_f16(128, D) | (1u << 16);
+      uint32_t step = 0;         // over all items
+      uint32_t item = 0;
+      bool ok = true;
+      auto scores = [&](int tile, uint32_t at, int buffer) {  // S = Q K^T of step `at` into a buffer
+        const uint32_t q0 = smem_u32(q_smem) + tile * C::kQTile, k0 = smem_u32(k_smem) + (at & 1) * C::kKv;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_f16_warp(tmem + buffer * 128, smem_desc(q0 + (k / 4) * 16384 + (k % 4) * 32, 16, 1024, kLayoutSW128),
+                       smem_desc(k0 + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024, kLayoutSW128), idesc_s, k > 0);
+        mma_commit_warp(&s_full[buffer]);
+      };
+      auto sums = [&](int tile, uint32_t at, int buffer, bool first) {  // O += P V
+        const uint32_t v0 = smem_u32(v_smem) + (at & 1) * C::kKv;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_f16_ts_warp(tmem + C::kTmemO + tile * D, tmem + buffer * 128 + 8 * k, desc_n_major(v0 + k * 2048, C::kPanel),
+                          idesc_o, !first || k > 0);
+        mma_commit_warp(&pv_done[tile]);
+      };
+      uint32_t p_seen[2] = {0, 0};
+      while (ok && u < u_end) {
+        const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+        if constexpr (kTiles == 2) {
+          ok = wait(&kv_full[step & 1], step >> 1);
+          for (int n = 0; ok && n < 2; ++n) {
+            ok = wait(&q_full[n], item);
+            if (ok) scores(n, step, n);
+          }
+          if (!ok) break;
+          mma_commit_warp(&kv_empty[step & 1]);
+          for (int i = 0; ok && i < steps; ++i, ++step) {
+            const uint32_t next = step + 1;
+            for (int n = 0; ok && n < 2; ++n) {
+              ok = wait(&p_full[n], p_seen[n]++);
+              if (ok && n == 0) ok = wait(&kv_full[2 + (step & 1)], step >> 1);
+              if (!ok) break;
+              sums(n, step, n, i == 0);
+              if (n == 1) mma_commit_warp(&kv_empty[2 + (step & 1)]);
+              if (i + 1 < steps) {
+                if (n == 0) ok = wait(&kv_full[next & 1], next >> 1);
+                if (!ok) break;
+                scores(n, next, n);
+                if (n == 1) mma_commit_warp(&kv_empty[next & 1]);
+              }
+            }
+          }
+        } else {
+          ok = wait(&q_full[0], item);
+          for (int j = 0; ok && j < min(steps, 2); ++j) {
+            const uint32_t at = step + j;
+            ok = wait(&kv_full[at & 1], at >> 1);
+            if (!ok) break;
+            scores(0, at, at & 1);
+            mma_commit_warp(&kv_empty[at & 1]);
+          }
+          for (int i = 0; ok && i < steps; ++i, ++step) {
+            const int buffer = step & 1;
+            ok = wait(&p_full[buffer], p_seen[buffer]++);
+            if (ok) ok = wait(&kv_full[2 + (step & 1)], step >> 1);
+            if (!ok) break;
+            sums(0, step, buffer, i == 0);
+            mma_commit_warp(&kv_empty[2 + (step & 1)]);
+            if (i + 2 < steps) {
+              const uint32_t at = step + 2;
+              ok = wait(&kv_full[at & 1], at >> 1);
+              if (!ok) break;
+              scores(0, at, at & 1);
+              mma_commit_warp(&kv_empty[at & 1]);
+            }
+          }
+        }
+        ++item;
+        u += steps;
+        if (ok && u < u_end) c.next(p);
+      }
+    }
+  } else if (warp >= C::kSoftWarps) {
+    // decode: a unit is 32 values of a token
+    regs_dec<80>();
+    constexpr int kParts = D / 32, kUnits = kTok * kParts, kDecThreads = 32 * C::kDecWarps;
+    const int tid = threadIdx.x - 32 * C::kSoftWarps;
+    uint32_t half = 0;
+    bool ok = true;
+    while (ok && u < u_end) {
+      const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+      for (int i = 0; ok && i < 2 * steps; ++i, ++half) {
+        const uint32_t s = half % C::kRaw, step = half >> 1, kind = half & 1, buf = 2 * kind + (step & 1), round = step >> 1;
+        ok = wait(&raw_full[s], half / C::kRaw);
+        if (ok && round > 0) ok = wait(&kv_empty[buf], round - 1);
+        if (!ok) break;
+        const uint8_t* src = raw + s * C::kHalf;
+        uint8_t* dst = (kind ? v_smem : k_smem) + (step & 1) * C::kKv;
+        const uint32_t wrong = kind ? 0 : bad_blocks[s];
+#pragma unroll
+        for (int x = 0; x < kUnits / kDecThreads; ++x) {
+          const int unit = tid + x * kDecThreads, tok = unit / kParts, part = unit % kParts;
+          const uint8_t* block = src + (tok / 16) * cache_half_bytes(D);
+          uint4 w = *reinterpret_cast<const uint4*>(block + (tok % 16) * (D / 2) + part * 16);
+          uint32_t sb = *reinterpret_cast<const uint16_t*>(block + 8 * D + (tok % 16) * (D / 16) + part * 2);
+          if (kind) {  // a value's NaN scale counts as 0
+            if ((sb & 0x7fu) == 0x7fu) sb &= 0xff00u;
+            if ((sb & 0x7f00u) == 0x7f00u) sb &= 0xffu;
+          } else if (wrong >> (tok / 16) & 1u) {
+            sb = 0x7f7fu;
+          }
+          uint32_t s2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)sb));
+          uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
+          // the chunks in an order that puts a quarter warp's on banks of their own
+          const int turn = D == 64 ? 0 : D == 128 ? 2 * (part / 2) : part / 2;
+          if (turn & 2) {
+            uint32_t t = w.x;
+            w.x = w.z, w.z = t, t = w.y, w.y = w.w, w.w = t, t = s0, s0 = s1, s1 = t;
+          }
+          if (turn & 1) {
+            uint32_t t = w.x;
+            w.x = w.y, w.y = t, t = w.z, w.z = w.w, w.w = t;
+          }
+          uint8_t* row = dst + (part / 2) * C::kPanel + tok * 128;
+          const int chunk = (4 * (part % 2)) ^ turn ^ (tok & 7);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 0) << 4)) = e2m1x8_scaled_f16(w.x, s0);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 1) << 4)) = e2m1x8_scaled_f16(w.y, s0);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 2) << 4)) = e2m1x8_scaled_f16(w.z, s1);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 3) << 4)) = e2m1x8_scaled_f16(w.w, s1);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&raw_empty[s]);
+          mbar_arrive(&kv_full[buf]);
+        }
+      }
+      u += steps;
+      if (ok && u < u_end) c.next(p);
+    }
+  } else {
+    regs_inc<kTiles == 2 ? 176 : 208>();
+    const int n = warp / 4, row_in_tile = threadIdx.x & 127, tile_row = 128 * n + row_in_tile;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t o_tmem = tmem + lanes + C::kTmemO + n * D;
+    uint32_t step = 0;  // over all items
+    uint32_t item = 0;
+    bool ok = true;
+    while (ok && u < u_end) {
+      const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+      const int rows = c.rows(p), row = c.tile * C::kRows + tile_row;
+      const bool real = tile_row < rows;
+      const int token = c.q.row0 + row / p.group, hq = c.head * p.group + row % p.group;
+      const int base_pos = c.q.length - c.q.n;
+      const int pos = real ? base_pos + row / p.group : -1;
+      float fac;
+      {
+        // q in FP16, the sign of the scale with it
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                                          (int64_t)token * p.a.q_row + (int64_t)hq * p.a.q_head);
+        float top = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = real ? src[i] : make_uint4(0, 0, 0, 0);
+          float v[8];
+          bf16x8_to_float(x, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+        }
+        float back;
+        float by = row_scale(top, back);
+        fac = fmaxf(back * fabsf(p.a.scale) * p.a.k_scale * kLog2e, 0x1p-120f);  // (above 0: masked scores stay -inf)
+        by = p.a.scale < 0.f ? -by : p.a.scale == 0.f ? 0.f : by;
+        uint8_t* dst = q_smem + n * C::kQTile + row_in_tile * 128;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 x = real ? src[i] : make_uint4(0, 0, 0, 0);
+          float v[8];
+          bf16x8_to_float(x, v);
+          const uint4 h = make_uint4(pack_f16x2(v[0] * by, v[1] * by), pack_f16x2(v[2] * by, v[3] * by),
+                                     pack_f16x2(v[4] * by, v[5] * by), pack_f16x2(v[6] * by, v[7] * by));
+          *reinterpret_cast<uint4*>(dst + (i / 8) * 16384 + (((i % 8) ^ (row_in_tile & 7)) << 4)) = h;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[n]);
+      }
+      // steps that every row of the tile sees whole
+      const int pos_first = base_pos + (c.tile * C::kRows + 128 * n) / p.group;
+      const int pos_last = base_pos + (c.tile * C::kRows + min(128 * n + 128, rows) - 1) / p.group;
+      const int all_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
+      const int lowest = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;  // first token that the row sees
+
+      float m = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
+      int tok0 = (c.span.first + c.from) * kTok;
+      for (int i = 0; i < steps; ++i, ++step, tok0 += kTok) {
+        const int buffer = kTiles == 2 ? n : (int)(step & 1);
+        if (!wait(&s_full[buffer], kTiles == 2 ? step : step >> 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t s_tmem = tmem + lanes + buffer * 128;
+        uint32_t s[kTok / 32][32];
+#pragma unroll
+        for (int x = 0; x < kTok / 32; ++x) TmemLd<32>::start(s_tmem + 32 * x, s[x]);
+#pragma unroll
+        for (int x = 0; x < kTok / 32; ++x) TmemLd<32>::wait(s[x]);
+        if (!(tok0 >= all_lo && tok0 + kTok - 1 <= pos_first)) {
+          const int hi = pos - tok0, lo = lowest - tok0;
+#pragma unroll
+          for (int x = 0; x < kTok / 32; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (32 * x + y > hi || 32 * x + y < lo) s[x][y] = 0xff800000u;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kTok / 32; ++x)
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
+        top *= fac;
+        const bool grows = top > m + 8.f || (m == -INFINITY && top > m);
+        if (__any_sync(0xffffffffu, grows)) {
+          const float by = grows ? exp2_approx(m - top) : 1.f;
+          if (grows) m = top;
+          l.x *= by;
+          l.y *= by;
+          if (i > 0) {
+            if (!wait(&pv_done[n], step - 1)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D / 16; ++x) {
+              uint32_t o[16];
+              tmem_ld16(o_tmem + 16 * x, o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * by);
+              tmem_st16(o_tmem + 16 * x, o);
+            }
+          }
+        }
+        const float from_m = m == -INFINITY ? 0.f : m;
+        const float2 fac2 = make_float2(fac, fac), minus = make_float2(-from_m, -from_m);
+#pragma unroll
+        for (int x = 0; x < kTok / 32; ++x) {
+          uint32_t h[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            float2 e = ffma2(make_float2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])), fac2, minus);
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            l = fadd2(l, e);
+            h[y] = pack_f16x2(e.x, e.y);
+          }
+          tmem_st16(s_tmem + 16 * x, h);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buffer]);
+      }
+      // (the last scores come before the last two sums where buffers alternate,
+      // and a wait for a phase is met by the one two before it: both, in order)
+      if (kTiles == 1 && steps > 1 && ok) ok = wait(&pv_done[n], step - 2);
+      if (!ok || !wait(&pv_done[n], step - 1)) break;
+      tc_fence_after();
+      const float sum = l.x + l.y;
+      const bool whole = c.from == 0 && steps == c.span.units;
+      float lse = 0.f, inv = 0.f;
+      float* part = nullptr;
+      if (whole) {
+        if (real) inv = attn_finish(p, hq, m, sum, lse);
+        if (real && p.a.lse) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
+      } else {
+        const int64_t at = 2 * (int64_t)blockIdx.x + (c.from == 0 ? 1 : 0);
+        part = p.parts + (at * C::kRows + tile_row) * D;
+        if (real) *reinterpret_cast<float2*>(attn_stats<D, C::kRows>(p, at, tile_row)) = make_float2(m, sum);
+      }
+      __nv_bfloat16* out = attn_out(p, token, hq);
+#pragma unroll 1
+      for (int x = 0; x < D / 16; ++x) {
+        uint32_t o[16];
+        tmem_ld16(o_tmem + 16 * x, o);
+        if (real && whole) {
+          uint32_t w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+          *reinterpret_cast<uint4*>(out + 16 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(out + 16 * x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        } else if (real) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<uint4*>(part + 16 * x + 4 * y) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        }
+        __syncwarp();
+      }
+      ++item;
+      u += steps;
+      if (u < u_end) c.next(p);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  __syncthreads();
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch_tc_dim(AttnArgs p, int sms, cudaStream_t st) {
+  using C = TcCfg<D>;
+  static bool seen[64];
+  cudaError_t e = allow_smem(attention_tc_kernel<D>, C::kSmem, seen);
+  if (e != cudaSuccess) return e;
+  void* err = nullptr;
+  e = attention_status_address(&err);
+  if (e != cudaSuccess) return e;
+  p.workers = sms;
+  p.least = 4;
+  e = launch_dependent_smem(attention_tc_kernel<D>, (unsigned)sms, C::kThreads, C::kSmem, st, p, static_cast<uint32_t*>(err));
+  if (e != cudaSuccess) return e;
+  return launch_attention_join<D, C::kRows, C::kTok>(p, st);
+}
+
+template <int D>
+size_t parts_bytes(int sms) {
+  return (size_t)2 * sms * TcCfg<D>::kRows * (D + 2) * 4;
+}
+
+}  // namespace
+
+size_t attention_tc_parts_bytes(int D, int sms) {
+  return D == 64 ? parts_bytes<64>(sms) : D == 128 ? parts_bytes<128>(sms) : parts_bytes<256>(sms);
+}
+
+cudaError_t launch_attention_tc(const AttnArgs& p, int sms, cudaStream_t st) {
+  switch (p.a.D) {
+    case 64: return launch_tc_dim<64>(p, sms, st);
+    case 128: return launch_tc_dim<128>(p, sms, st);
+    default: return launch_tc_dim<256>(p, sms, st);
+  }
+}
+
+}  // namespace moe_fp4

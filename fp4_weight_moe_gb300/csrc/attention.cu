@@ -29,7 +29,10 @@ cudaError_t attention_status_address(void** p) { return cudaGetSymbolAddress(p, 
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kUnit = kWarps * kCacheBlock;  // tokens that the warps of a worker take in one go
+constexpr int kPair = 2 * kCacheBlock;  // tokens that a warp takes in one go: two blocks
+// Items of fewer pairs on average go to a warp each (64 key heads' windows of
+// 128 tokens of 128 requests: @WIN@; with the four warps of a CTA @WIN4@).
+constexpr int kTeamSpan = 64;
 constexpr uint32_t kWaitCode = 1u;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -45,18 +48,17 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   return r;
 }
 
-// Two E4M3 scales as an FP16 pair, NaN as 0.
-__device__ __forceinline__ uint32_t value_scales(uint32_t lo, uint32_t hi) {
-  if ((lo & 0x7fu) == 0x7fu) lo = 0;
-  if ((hi & 0x7fu) == 0x7fu) hi = 0;
+// Two E4M3 scales as an FP16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t two) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(lo | (hi << 8))));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
   return r;
 }
 
-__device__ __forceinline__ uint32_t key_scale(uint32_t b) {
+// The same with NaN as 448 (the minimum of a number and a NaN is the number).
+__device__ __forceinline__ uint32_t finite_scale_pair(uint32_t two) {
   uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)(b | (b << 8))));
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(scale_pair(two)), "r"(0x5f005f00u));
   return r;
 }
 
@@ -66,9 +68,9 @@ __device__ __forceinline__ int row_token(int i) { return (i & 8) + ((i & 7) >> 1
 template <int D, int NT>
 struct Cfg {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kStages = 4;
-  static constexpr int kBlockBytes = cache_block_bytes(D);
-  static constexpr int kRing = kStages * kBlockBytes;  // a warp's
+  static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kStageBytes = 2 * cache_block_bytes(D);
+  static constexpr int kRing = kStages * kStageBytes;  // a warp's
   static constexpr int kRow = D + 4;                   // floats of a row of sums (padded: rows start on other banks)
   static_assert(kRows * kRow * 4 <= kRing, "a warp's sums lie in its ring");
   static constexpr int kBarriers = kWarps * kStages * 8;
@@ -95,9 +97,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   pdl_wait();
   pdl_launch_dependents();
 
-  AttnCursor<kRows, kUnit> c;
+  AttnCursor<kRows, kPair> c;
   int64_t u, u_end;
-  if (!attn_stretch<kRows, kUnit, kThreads>(p, c, u, u_end)) return;
+  int team;
+  if (!attn_stretch<kRows, kPair, kThreads, kWarps, kTeamSpan>(p, c, u, u_end, team)) return;
+  const int member = team == 1 ? 0 : warp, worker = team == 1 ? (int)blockIdx.x * kWarps + warp : (int)blockIdx.x;
 
   const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
   const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);  // blocks of a page
@@ -110,6 +114,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     const int r = c.r, tile = c.tile, head = c.head, from = c.from;
     const int to = (int)min((int64_t)span.units, from + u_end - u);
     u += to - from;
+
+    // this warp's pairs of blocks: first, first + team, ...; their copies
+    // start before anything else
+    const int end_block = (min((span.first + to) * kPair, span.hi) + kCacheBlock - 1) / kCacheBlock;
+    const int first = span.first + from + member, end_pair = span.first + to;
+    const int count = alive && first < end_pair ? (end_pair - first + team - 1) / team : 0;
+    const int32_t* table = p.a.tables + (int64_t)r * p.a.table_row;
+    int page_even = 0, page_odd = 0;  // of 32 pairs' blocks: lane i's those of pair first + (i + 32 k) team
+    unsigned bad_blocks = 0;          // of the copies in flight: two bits per stage
+    auto load = [&](int i) {
+      if ((i & 31) == 0) {
+        const int b = 2 * (first + (i + lane) * team);
+        page_even = b < end_block ? table[b >> blocks_log] : 0;
+        page_odd = blocks_log == 0 && b + 1 < end_block ? table[b + 1] : page_even;
+      }
+      const int pair = first + i * team, stage = (round + i) % S;
+      const int even = __shfl_sync(0xffffffffu, page_even, i & 31), odd = __shfl_sync(0xffffffffu, page_odd, i & 31);
+      const bool bad0 = (unsigned)even >= (unsigned)p.a.pages, bad1 = (unsigned)odd >= (unsigned)p.a.pages;
+      bad_blocks = (bad_blocks & ~(3u << (2 * stage))) | (((bad0 ? 1u : 0u) | (bad1 ? 2u : 0u)) << (2 * stage));
+      if (lane == 0) {
+        uint8_t* dst = ring + stage * C::kStageBytes;
+        const int64_t heads = p.a.Hkv;
+        const int in_page = (2 * pair) & ((1 << blocks_log) - 1);
+        const uint8_t* src = cache + ((((bad0 ? 0 : (int64_t)even) * heads + head) << blocks_log) + in_page) * cache_block_bytes(D);
+        const int blocks = min(end_block - 2 * pair, 2);
+        mbar_arrive_expect_tx(&full[stage], blocks * cache_block_bytes(D));
+        if (blocks_log > 0) {  // the two lie together
+          bulk_load(dst, src, blocks * cache_block_bytes(D), &full[stage]);
+        } else {
+          bulk_load(dst, src, cache_block_bytes(D), &full[stage]);
+          if (blocks == 2)
+            bulk_load(dst + cache_block_bytes(D), cache + ((bad1 ? 0 : (int64_t)odd) * heads + head) * cache_block_bytes(D),
+                      cache_block_bytes(D), &full[stage]);
+        }
+      }
+    };
+    int loaded = 0;
+    for (; loaded < min(S - 1, count); ++loaded) load(loaded);
 
     // q, in the operand's order, and the rows' factors
     uint32_t qf[NT][kSteps][2];
@@ -157,161 +199,150 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     const int pos_last = base_pos + (tile * kRows + rows - 1) / p.group;
     const int all_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
 
-    float o[NT][kSteps][4], m[NT][2], l[NT][2];
+    float o[NT][kSteps][4], m[NT][2], minus[NT][2], l[NT][2];  // (minus: -m, or 0 while that is -inf)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
       m[n][0] = m[n][1] = -INFINITY;
+      minus[n][0] = minus[n][1] = 0.f;
       l[n][0] = l[n][1] = 0.f;
     }
 
-    // this warp's blocks: first, first + kWarps, ...
-    const int end_block = min((span.first + to) * kWarps, (span.hi + kCacheBlock - 1) / kCacheBlock);
-    const int first = (span.first + from) * kWarps + warp;
-    const int count = alive && first < end_block ? (end_block - first + kWarps - 1) / kWarps : 0;
-    int page_reg = 0;  // pages of 32 blocks: lane i's that of block first + (i + 32 k) kWarps
-    auto page_of = [&](int i) {
-      if ((i & 31) == 0) {
-        const int b = first + (i + lane) * kWarps;
-        page_reg = b < end_block ? p.a.tables[(int64_t)r * p.a.table_row + (b >> blocks_log)] : 0;
-      }
-      return __shfl_sync(0xffffffffu, page_reg, i & 31);
-    };
-    unsigned bad_pages = 0;  // of the copies in flight, by stage
-    auto load = [&](int i) {
-      const int page = page_of(i), b = first + i * kWarps, stage = (round + i) % S;
-      const bool bad = page < 0 || page >= p.a.pages;
-      bad_pages = (bad_pages & ~(1u << stage)) | ((bad ? 1u : 0u) << stage);
-      if (lane == 0) {
-        const int64_t block = (((int64_t)(bad ? 0 : page) * p.a.Hkv + head) << blocks_log) + (b & ((1 << blocks_log) - 1));
-        mbar_arrive_expect_tx(&full[stage], C::kBlockBytes);
-        bulk_load(ring + stage * C::kBlockBytes, cache + block * C::kBlockBytes, C::kBlockBytes, &full[stage]);
-      }
-    };
-    int loaded = 0;
-    for (; loaded < min(S - 1, count); ++loaded) load(loaded);
-
     for (int i = 0; i < count; ++i) {
-      if (loaded < count) load(loaded++);  // (into the stage of block i - 1)
+      if (loaded < count) load(loaded++);  // (into the stage of pair i - 1)
       const int stage = (round + i) % S;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], ((round + i) / S) & 1, &g_attention_status, kWaitCode))) {
         alive = false;
         break;
       }
-      const uint8_t* kb = ring + stage * C::kBlockBytes;
-      const uint8_t* vb = kb + cache_half_bytes(D);
-      const int tok0 = (first + i * kWarps) * kCacheBlock;
+      const uint8_t* at = ring + stage * C::kStageBytes;
+      const int tok0 = (first + i * team) * kPair;
 
-      // S^T = K q^T: rows g, g + 8
-      float s[NT][4];
+      // S^T = K q^T: rows g, g + 8 of each block
+      float s[2][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-      {
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[b][n][0] = s[b][n][1] = s[b][n][2] = s[b][n][3] = 0.f;
+        const uint8_t* kb = at + b * cache_block_bytes(D);
         constexpr int kWords = D / 32;  // words of codes per lane and row
         uint32_t w[2][kWords];
-        uint32_t sc[2];
+        uint32_t by[2][(kWords + 1) / 2];  // a scale for two words, in both halves
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int tok = row_token(g + 8 * h);
           const uint8_t* row = kb + tok * (D / 2) + t * (D / 8);
+          if constexpr (D == 64) {
+            const uint2 x = *reinterpret_cast<const uint2*>(row);
+            w[h][0] = x.x, w[h][1] = x.y;
+          } else {
 #pragma unroll
-          for (int j = 0; j < kWords; j += 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(row + 4 * j);
-            w[h][j] = x.x;
-            w[h][j + 1] = x.y;
+            for (int j = 0; j < kWords; j += 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(row + 4 * j);
+              w[h][j] = x.x, w[h][j + 1] = x.y, w[h][j + 2] = x.z, w[h][j + 3] = x.w;
+            }
           }
           const uint8_t* sr = kb + 8 * D + tok * (D / 16) + t * (D / 64);
-          if constexpr (D == 64)
-            sc[h] = *sr;
-          else if constexpr (D == 128)
-            sc[h] = *reinterpret_cast<const uint16_t*>(sr);
-          else
-            sc[h] = *reinterpret_cast<const uint32_t*>(sr);
+          if constexpr (D == 64) {
+            by[h][0] = __byte_perm(scale_pair(*sr), 0, 0x1010);
+          } else {
+#pragma unroll
+            for (int j = 0; j < D / 64; j += 2) {
+              const uint32_t two = scale_pair(*reinterpret_cast<const uint16_t*>(sr + j));
+              by[h][j] = __byte_perm(two, 0, 0x1010);
+              by[h][j + 1] = __byte_perm(two, 0, 0x3232);
+            }
+          }
         }
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           uint32_t x[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t by = key_scale((sc[h] >> (8 * (j / 2))) & 0xffu);
             e2m1x8_to_half2x4(w[h][j], x[h]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[h][k] = mul_f16x2(x[h][k], by);
+            for (int k = 0; k < 4; ++k) x[h][k] = mul_f16x2(x[h][k], by[h][j / 2]);
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint32_t af[4] = {x[0][2 * k], x[1][2 * k], x[0][2 * k + 1], x[1][2 * k + 1]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
+            for (int n = 0; n < NT; ++n) mma_f16(s[b][n], af, qf[n][2 * j + k][0], qf[n][2 * j + k][1]);
           }
         }
       }
 
-      // scores in units of log 2, masked; the running maximum
-      const bool whole = tok0 >= all_lo && tok0 + kCacheBlock - 1 <= pos_first;
-      const bool bad = (bad_pages >> stage) & 1u;
-      float top[NT][2];
+      // scores in units of log 2, masked
+      const bool whole = tok0 >= all_lo && tok0 + kPair - 1 <= pos_first;
+      const unsigned bad = (bad_blocks >> (2 * stage)) & 3u;
+      bool grows = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = e & 1, j = tok0 + row_token(g + 8 * (e >> 1));
-          float x = s[n][e] * fac[n][c];
-          if (bad) x = NAN;
-          if (!whole) {
-            const bool sees = j <= last[n][c] && (p.a.window == 0 || j > last[n][c] - p.a.window);
-            if (!sees) x = -INFINITY;
-          }
-          s[n][e] = x;
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) top[n][c] = fmaxf(s[n][c], s[n][c + 2]);
-      }
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1)
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xffffffffu, top[n][c], x));
-      bool grows = false;
+          for (int e = 0; e < 4; ++e) s[b][n][e] *= fac[n][e & 1];
+      if (!whole || bad != 0) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = tok0 + kCacheBlock * b + row_token(g + 8 * (e >> 1)), pos = last[n][e & 1];
+              if (bad >> b & 1u) s[b][n][e] = NAN;
+              if (!(j <= pos && (p.a.window == 0 || j > pos - p.a.window))) s[b][n][e] = -INFINITY;
+            }
+      }
+      // the maximum follows when a score outgrows it by 2^8
+      float top[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) grows = grows || top[n][c] > m[n][c];
+        for (int c2 = 0; c2 < 2; ++c2) {
+          top[n][c2] = fmaxf(fmaxf(s[0][n][c2], s[0][n][c2 + 2]), fmaxf(s[1][n][c2], s[1][n][c2 + 2]));
+          grows = grows || top[n][c2] > m[n][c2] + 8.f;
+        }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const float next = fmaxf(m[n][c], top[n][c]);
-            const float by = next == -INFINITY ? 1.f : exp2_approx(m[n][c] - next);
-            m[n][c] = next;
-            l[n][c] *= by;
+          for (int c2 = 0; c2 < 2; ++c2) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top[n][c2] = fmaxf(top[n][c2], __shfl_xor_sync(0xffffffffu, top[n][c2], x));
+            const float next = fmaxf(m[n][c2], top[n][c2]);
+            const float by = next == -INFINITY ? 1.f : exp2_approx(m[n][c2] - next);
+            m[n][c2] = next;
+            minus[n][c2] = next == -INFINITY ? 0.f : -next;
+            l[n][c2] *= by;
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) {
-              o[n][j][c] *= by;
-              o[n][j][c + 2] *= by;
+              o[n][j][c2] *= by;
+              o[n][j][c2 + 2] *= by;
             }
           }
         }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[2][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float e[4];
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int i4 = 0; i4 < 4; ++i4) {
-          const float from_m = m[n][i4 & 1] == -INFINITY ? 0.f : m[n][i4 & 1];
-          e[i4] = exp2_approx(s[n][i4] - from_m);
-          l[n][i4 & 1] += e[i4];
+        for (int n = 0; n < NT; ++n) {
+          float e[4];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            e[i4] = exp2_approx(s[b][n][i4] + minus[n][i4 & 1]);
+            l[n][i4 & 1] += e[i4];
+          }
+          pf[b][n][0] = transpose8x8(pack_f16x2(e[0], e[1]));
+          pf[b][n][1] = transpose8x8(pack_f16x2(e[2], e[3]));
         }
-        pf[n][0] = transpose8x8(pack_f16x2(e[0], e[1]));
-        pf[n][1] = transpose8x8(pack_f16x2(e[2], e[3]));
-      }
 
-      // O^T += V^T p^T: columns g D / 8 .. of the values, tokens t, t + 4, t + 8, t + 12 of the block
-      {
+      // O^T += V^T p^T: columns g D / 8 .. of the values, tokens t, t + 4, t + 8, t + 12 of each block
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint8_t* vb = at + b * cache_block_bytes(D) + cache_half_bytes(D);
         constexpr int kWords = D / 64;  // words of codes per lane and token
         uint32_t w[4][kWords];
         uint32_t sc[4];
@@ -324,15 +355,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
             sc[k] = *sr;
           } else if constexpr (D == 128) {
             const uint2 x = *reinterpret_cast<const uint2*>(row);
-            w[k][0] = x.x;
-            w[k][1] = x.y;
+            w[k][0] = x.x, w[k][1] = x.y;
             sc[k] = *sr;
           } else {
             const uint4 x = *reinterpret_cast<const uint4*>(row);
-            w[k][0] = x.x;
-            w[k][1] = x.y;
-            w[k][2] = x.z;
-            w[k][3] = x.w;
+            w[k][0] = x.x, w[k][1] = x.y, w[k][2] = x.z, w[k][3] = x.w;
             sc[k] = *reinterpret_cast<const uint16_t*>(sr);
           }
         }
@@ -341,10 +368,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
           uint32_t x[4][4];  // rows of even and odd columns, tokens (t, t + 4); the same, tokens (t + 8, t + 12)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const uint32_t a = w[2 * k][j], b = w[2 * k + 1][j];
-            const uint32_t even = (a & 0x0f0f0f0fu) | ((b & 0x0f0f0f0fu) << 4);
-            const uint32_t odd = ((a >> 4) & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
-            const uint32_t by = value_scales((sc[2 * k] >> (8 * (j / 2))) & 0xffu, (sc[2 * k + 1] >> (8 * (j / 2))) & 0xffu);
+            const uint32_t a = w[2 * k][j], bb = w[2 * k + 1][j];
+            const uint32_t even = (a & 0x0f0f0f0fu) | ((bb & 0x0f0f0f0fu) << 4);
+            const uint32_t odd = ((a >> 4) & 0x0f0f0f0fu) | (bb & 0xf0f0f0f0u);
+            const uint32_t by = finite_scale_pair(__byte_perm(sc[2 * k], sc[2 * k + 1], j < 2 ? 0x40 : 0x51));
             e2m1x8_to_half2x4(even, x[2 * k]);
             e2m1x8_to_half2x4(odd, x[2 * k + 1]);
 #pragma unroll
@@ -357,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
           for (int i4 = 0; i4 < 4; ++i4) {
             const uint32_t af[4] = {x[0][i4], x[1][i4], x[2][i4], x[3][i4]};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i4], af, pf[n][0], pf[n][1]);
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i4], af, pf[b][n][0], pf[b][n][1]);
           }
         }
       }
-      __syncwarp();  // the block is read: its stage may be loaded anew
+      __syncwarp();  // the pair is read: its stage may be loaded anew
     }
     round += count;
 
@@ -372,6 +399,41 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], x);
+    const bool is_whole = from == 0 && to == span.units;
+    const int64_t part = 2 * (int64_t)worker + (from == 0 ? 1 : 0);
+    if (team == 1) {
+      // a lane has D / 8 columns of the heads 2 t, 2 t + 1
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c2 = 0; c2 < 2; ++c2) {
+          const int row = 8 * n + 2 * t + c2;
+          if (row >= rows) continue;
+          if (!is_whole) {
+            float* dst = p.parts + (part * kRows + row) * D + g * (D / 8);
+#pragma unroll
+            for (int j = 0; j < kSteps; j += 2)
+              *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[n][j][c2], o[n][j][c2 + 2], o[n][j + 1][c2], o[n][j + 1][c2 + 2]);
+            if (g == 0) *reinterpret_cast<float2*>(attn_stats<D, kRows>(p, part, row)) = make_float2(m[n][c2], l[n][c2]);
+            continue;
+          }
+          const int rr = tile * kRows + row, token = q.row0 + rr / p.group, hq = head * p.group + rr % p.group;
+          float lse;
+          const float inv = attn_finish(p, hq, m[n][c2], l[n][c2], lse);
+          __nv_bfloat16* dst = attn_out(p, token, hq) + g * (D / 8);
+#pragma unroll
+          for (int j = 0; j < kSteps; j += 4)
+            *reinterpret_cast<uint4*>(dst + 2 * j) =
+                make_uint4(pack_bf16x2(o[n][j][c2] * inv, o[n][j][c2 + 2] * inv),
+                           pack_bf16x2(o[n][j + 1][c2] * inv, o[n][j + 1][c2 + 2] * inv),
+                           pack_bf16x2(o[n][j + 2][c2] * inv, o[n][j + 2][c2 + 2] * inv),
+                           pack_bf16x2(o[n][j + 3][c2] * inv, o[n][j + 3][c2 + 2] * inv));
+          if (p.a.lse && g == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
+        }
+      __syncwarp();
+      if (u < u_end) c.next(p);
+      continue;
+    }
     float* sums = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -386,8 +448,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         }
       }
     __syncthreads();
-    const bool is_whole = from == 0 && to == span.units;
-    const int part = 2 * (int)blockIdx.x + (from == 0 ? 1 : 0);
     for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4));
       if (row >= rows) break;
@@ -410,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         acc.w += v.w * by;
       }
       if (!is_whole) {
-        *reinterpret_cast<float4*>(p.parts + ((int64_t)part * kRows + row) * D + d) = acc;
+        *reinterpret_cast<float4*>(p.parts + (part * kRows + row) * D + d) = acc;
         if (d == 0) *reinterpret_cast<float2*>(attn_stats<D, kRows>(p, part, row)) = make_float2(top, sum);
         continue;
       }
@@ -427,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   }
 }
 
-int max_workers(int sms, int D, int NT) { return sms * (D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2); }
+int max_ctas(int sms, int D, int NT) { return sms * (D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2); }
 
 template <int D, int NT>
 cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
@@ -435,11 +495,15 @@ cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
   static bool seen[64];
   cudaError_t e = allow_smem(attention_rows_kernel<D, NT>, C::kSmem, seen);
   if (e != cudaSuccess) return e;
-  p.workers = max_workers(sms, D, NT);
-  p.least = 2;
-  e = launch_dependent_smem(attention_rows_kernel<D, NT>, (unsigned)p.workers, kThreads, C::kSmem, st, p);
+  const int grid = max_ctas(sms, D, NT);
+  p.workers = grid * kWarps;
+  p.least = 4;
+  e = launch_dependent_smem(attention_rows_kernel<D, NT>, (unsigned)grid, kThreads, C::kSmem, st, p);
   if (e != cudaSuccess) return e;
-  return launch_attention_join<D, C::kRows, kUnit>(p, st);
+  // few items: many parts to each, joined by more CTAs
+  const int64_t tiles = p.a.R > 0 ? ((int64_t)p.a.T * p.group / p.a.R + C::kRows - 1) / C::kRows : 0;
+  return p.a.R * tiles * p.a.Hkv <= 64 ? launch_attention_join<D, C::kRows, 2>(p, sms, st)
+                                       : launch_attention_join<D, C::kRows, 8>(p, sms, st);
 }
 
 template <int D>
@@ -450,19 +514,20 @@ cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);
 }
 
-size_t prefix_bytes(int R) { return (((size_t)R + 1) * 8 + 255) / 256 * 256; }
+constexpr int kMaxWorkers = 4 * kWarps;  // per SM
+size_t places_bytes(int sms) { return ((size_t)sms * kMaxWorkers * sizeof(AttnPlace) + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t attention_workspace_bytes(int R, int, int, int D) {
+size_t attention_workspace_bytes(int, int, int, int D) {
   int sms = 0;
   if (current_device_sms(&sms) != cudaSuccess) sms = 152;
   size_t parts = attention_tc_parts_bytes(D, sms);
   for (int NT = 1; NT <= 2; ++NT) {
-    const size_t n = (size_t)2 * max_workers(sms, D, NT) * 8 * NT * (D + 2) * 4;
+    const size_t n = (size_t)2 * max_ctas(sms, D, NT) * kWarps * 8 * NT * (D + 2) * 4;
     parts = n > parts ? n : parts;
   }
-  return prefix_bytes(R) + (parts + 255) / 256 * 256;
+  return 256 + places_bytes(sms) + (parts + 255) / 256 * 256;
 }
 
 cudaError_t launch_attention(const moe_fp4_attention_args& a, cudaStream_t st) {
@@ -473,8 +538,9 @@ cudaError_t launch_attention(const moe_fp4_attention_args& a, cudaStream_t st) {
   p.a = a;
   p.group = a.Hq / a.Hkv;
   p.capacity = a.table_width * a.page_size;
-  p.prefix = static_cast<int64_t*>(a.workspace);
-  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + prefix_bytes(a.R));
+  p.line = static_cast<AttnLine*>(a.workspace);
+  p.places = reinterpret_cast<AttnPlace*>(static_cast<char*>(a.workspace) + 256);
+  p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + 256 + places_bytes(sms));
   switch (a.D) {
     case 64: return launch_dim<64>(p, sms, st);
     case 128: return launch_dim<128>(p, sms, st);

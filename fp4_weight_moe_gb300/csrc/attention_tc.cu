@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
   pdl_launch_dependents();
   AttnCursor<C::kRows, kTok> c;
   int64_t u, u_end;
-  if (!attn_stretch<C::kRows, kTok, C::kThreads>(p, c, u, u_end)) return;
+  int team;
+  if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, c, u, u_end, team)) return;
 
   if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -284,14 +285,10 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
           const uint8_t* block = src + (tok / 16) * cache_half_bytes(D);
           uint4 w = *reinterpret_cast<const uint4*>(block + (tok % 16) * (D / 2) + part * 16);
           uint32_t sb = *reinterpret_cast<const uint16_t*>(block + 8 * D + (tok % 16) * (D / 16) + part * 2);
-          if (kind) {  // a value's NaN scale counts as 0
-            if ((sb & 0x7fu) == 0x7fu) sb &= 0xff00u;
-            if ((sb & 0x7f00u) == 0x7f00u) sb &= 0xffu;
-          } else if (wrong >> (tok / 16) & 1u) {
-            sb = 0x7f7fu;
-          }
+          if (wrong >> (tok / 16) & 1u) sb = 0x7f7fu;
           uint32_t s2;
           asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)sb));
+          if (kind) asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5f005f00u));  // (a value's NaN scale counts as 448)
           uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
           // the chunks in an order that puts a quarter warp's on banks of their own
           const int turn = D == 64 ? 0 : D == 128 ? 2 * (part / 2) : part / 2;
@@ -505,7 +502,7 @@ cudaError_t launch_tc_dim(AttnArgs p, int sms, cudaStream_t st) {
   p.least = 4;
   e = launch_dependent_smem(attention_tc_kernel<D>, (unsigned)sms, C::kThreads, C::kSmem, st, p, static_cast<uint32_t*>(err));
   if (e != cudaSuccess) return e;
-  return launch_attention_join<D, C::kRows, C::kTok>(p, st);
+  return launch_attention_join<D, C::kRows, 8>(p, sms, st);
 }
 
 template <int D>

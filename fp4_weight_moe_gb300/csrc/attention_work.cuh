@@ -1,5 +1,5 @@
-// How an attention call's work is cut (attention.cu): shared by the kernels
-// that attend and the one that joins their parts.
+// How an attention call's work is cut (attention.cu, attention_tc.cu): shared
+// by the kernels that attend and the one that joins their parts.
 //
 // A request's queries and the heads of one key head are its rows (query i,
 // head g of the group: row i G + g), taken kRows at a time: a tile.  A tile
@@ -10,6 +10,9 @@
 // many workers and short ones fill one.  Only the first and the last item of
 // a stretch can be shared with other workers; their sums go to the worker's
 // two places in the workspace and are joined in the order of the workers.
+//
+// A worker is a CTA, or each of its warps (kTeams, where the items are short:
+// a CTA's warps would wait for each other at every item).
 #pragma once
 
 #include "attention.cuh"
@@ -17,14 +20,24 @@
 
 namespace moe_fp4 {
 
+// What the workers leave for the join.
+struct AttnLine {
+  int64_t units, each;  // stretches are whole grains: `each`, and one more for the first `more` workers
+  int more, workers, grain_log;
+};
+struct AttnPlace {  // where a worker's stretch begins
+  int row0, tile, head, rows, from, units;
+};
+
 struct AttnArgs {
   moe_fp4_attention_args a;
-  int group;      // Hq / Hkv
-  int capacity;   // tokens that a table row holds
-  float* parts;   // [2 workers][kRows][D] sums, then [2 workers][kRows][2] maximum and divisor
-  int64_t* prefix;  // [R + 1] units before each request
-  int workers;    // at most
-  int least;      // units that are worth a worker
+  int group;         // Hq / Hkv
+  int capacity;      // tokens that a table row holds
+  float* parts;      // [2 workers][kRows][D] sums, then [2 workers][kRows][2] maximum and divisor
+  AttnLine* line;
+  AttnPlace* places; // [workers]
+  int workers;       // at most
+  int least;         // units that are worth a worker
 };
 
 // Many rows to a key head (attention_tc.cu), and its parts' room.
@@ -76,6 +89,10 @@ __device__ __forceinline__ int64_t attn_units(const AttnArgs& p, int r) {
   return sum * p.a.Hkv;
 }
 
+__device__ __forceinline__ int64_t attn_quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;  // (both are not negative)
+}
+
 // A place in the line: an item, and the unit of it.  The lanes of a warp keep
 // one together.
 template <int kRows, int kUnit>
@@ -114,7 +131,7 @@ struct AttnCursor {
       if (tile + 32 >= tiles) break;  // (not reached)
     }
     span = attn_span<kUnit>(p, q, tile * kRows, kRows);
-    head = (int)(rest / max(span.units, 1));
+    head = (int)attn_quotient(rest, max(span.units, 1));
     from = (int)(rest - (int64_t)head * span.units);
   }
   // the next item of the line, of which there is one
@@ -137,14 +154,21 @@ struct AttnCursor {
   }
 };
 
-// Workers that share `units`, and the first unit of worker w.
-__device__ __forceinline__ int attn_workers(const AttnArgs& p, int64_t units) {
-  return (int)max(min((int64_t)p.workers, units / p.least), (int64_t)1);
+__device__ __forceinline__ AttnLine attn_line(int64_t units, int workers, int grain_log) {
+  const int64_t grains = (units + (1 << grain_log) - 1) >> grain_log;
+  AttnLine line = {units, attn_quotient(grains, workers), 0, workers, grain_log};
+  line.more = (int)(grains - line.each * workers);
+  return line;
 }
-__device__ __forceinline__ int64_t attn_start(int w, int64_t units, int workers) { return w * units / workers; }
+// The first unit of worker w.
+__device__ __forceinline__ int64_t attn_start(const AttnLine& line, int w) {
+  return min((w * line.each + min(w, line.more)) << line.grain_log, line.units);
+}
 // The worker that has unit u.
-__device__ __forceinline__ int attn_owner(int64_t u, int64_t units, int workers) {
-  return (int)(((u + 1) * workers - 1) / units);
+__device__ __forceinline__ int attn_owner(const AttnLine& line, int64_t u) {
+  const int64_t grain = u >> line.grain_log, longer = (line.each + 1) * line.more;
+  return grain < longer ? (int)attn_quotient(grain, line.each + 1)
+                        : line.more + (int)attn_quotient(grain - longer, line.each);
 }
 
 // Sum over the block's threads of v before this thread's, and all of it.
@@ -170,44 +194,112 @@ __device__ __forceinline__ int64_t block_before(int64_t v, int64_t* total, int64
   return before;
 }
 
-// Every CTA finds the line's length and its worker's stretch [u, u_end) of it
-// (CTA 0 writes down the sums before each request); false where it has none.
-template <int kRows, int kUnit, int kThreads>
+// Zeros for rows from, from + step, ... < to of q, by a warp: they see no key
+// (`real`: of a request), or lie behind the last sequence.
+__device__ __forceinline__ void attn_no_keys(const AttnArgs& p, int64_t from, int64_t to, int64_t step, bool real) {
+  const int quads = p.a.D / 8, lane = threadIdx.x & 31;
+  for (int64_t t = from; t < to; t += step) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + t * p.a.out_row;
+    for (int i = lane; i < p.a.Hq * quads; i += 32)
+      *reinterpret_cast<uint4*>(out + (int64_t)(i / quads) * p.a.out_head + 8 * (i % quads)) = make_uint4(0, 0, 0, 0);
+    if (p.a.lse)
+      for (int h = lane; h < p.a.Hq; h += 32) p.a.lse[t * p.a.Hq + h] = real && p.a.sinks ? p.a.sinks[h] : -INFINITY;
+  }
+}
+
+// The queries of a request that see no key: the first `before`, and those
+// from `past` on.
+struct AttnBlind {
+  int before, past;
+};
+__device__ __forceinline__ AttnBlind attn_blind(const AttnArgs& p, const AttnRequest& q) {
+  const int first = q.length - q.n;  // position of the first query
+  if (p.capacity == 0) return {q.n, q.n};
+  // (windows that lie behind the table)
+  const int64_t past = p.a.window > 0 ? (int64_t)p.capacity + p.a.window - 1 - first : q.n;
+  return {min(max(-first, 0), q.n), (int)max(min(past, (int64_t)q.n), (int64_t)0)};
+}
+
+// Every CTA finds the line's length and its worker's stretch [u, u_end) of
+// it, or each of its warps' own (then `team` is 1; CTA 0 writes the line
+// down); false where it has none.  Items that average fewer units than
+// kTeamSpan go to warps (kTeams warps of a CTA can be workers).
+template <int kRows, int kUnit, int kThreads, int kTeams, int kTeamSpan>
 __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows, kUnit>& cursor, int64_t& u,
-                                             int64_t& u_end) {
-  __shared__ int64_t shared[kThreads / 32];
-  __shared__ int64_t found_rest;
-  __shared__ int found;
+                                             int64_t& u_end, int& team) {
+  __shared__ int64_t shared[2][kThreads / 32];
+  __shared__ int64_t found_rest[kTeams];
+  __shared__ int found[kTeams];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int each = ceil_div(max(p.a.R, 1), kThreads);
   const int r0 = min((int)threadIdx.x * each, p.a.R), r1 = min(r0 + each, p.a.R);
-  int64_t mine = 0, units;
-  for (int r = r0; r < r1; ++r) mine += attn_units<kRows, kUnit>(p, r);
-  const int64_t before = block_before<kThreads>(mine, &units, shared);
-  if (blockIdx.x == 0) {
-    int64_t at = before;
-    for (int r = r0; r < r1; ++r) {
-      p.prefix[r] = at;
-      if (r + 1 < r1) at += attn_units<kRows, kUnit>(p, r);
-    }
-    if (threadIdx.x == 0) p.prefix[p.a.R] = units;
+  int64_t mine = 0, items = 0, all_items;
+  bool blind = false;  // a request of this thread's has queries that see no key
+  for (int r = r0; r < r1; ++r) {
+    const AttnRequest q = attn_request(p, r);
+    mine += attn_units<kRows, kUnit>(p, r);
+    if (kTeams > 1) items += (int64_t)attn_tiles<kRows>(p, q) * p.a.Hkv;
+    const AttnBlind b = attn_blind(p, q);
+    blind = blind || b.before > 0 || b.past < q.n;
   }
-  const int workers = attn_workers(p, units);
-  if (units == 0 || (int)blockIdx.x >= workers) return false;
-  u = attn_start(blockIdx.x, units, workers);
-  u_end = attn_start(blockIdx.x + 1, units, workers);
-  if (before <= u && u < before + mine) {
-    int64_t at = before;
-    int r = r0;
-    for (; r + 1 < r1; ++r) {
-      const int64_t n = attn_units<kRows, kUnit>(p, r);
-      if (u < at + n) break;
-      at += n;
+  int64_t units;
+  const int64_t before = block_before<kThreads>(mine, &units, shared[0]);
+  if (kTeams > 1) block_before<kThreads>(items, &all_items, shared[1]);
+  if (__any_sync(0xffffffffu, blind))
+    for (int i = 0; i < each; ++i) {
+      AttnRequest q = {0, 0, 0};
+      AttnBlind b = {0, 0};
+      if (r0 + i < r1) {
+        q = attn_request(p, r0 + i);
+        b = attn_blind(p, q);
+      }
+      for (unsigned todo = __ballot_sync(0xffffffffu, b.before > 0 || b.past < q.n); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1;
+        const int64_t row0 = __shfl_sync(0xffffffffu, q.row0, from), n = __shfl_sync(0xffffffffu, q.n, from);
+        const int first = __shfl_sync(0xffffffffu, b.before, from), past = __shfl_sync(0xffffffffu, b.past, from);
+        attn_no_keys(p, row0 + blockIdx.x, row0 + first, gridDim.x, true);
+        attn_no_keys(p, row0 + past + blockIdx.x, row0 + n, gridDim.x, true);
+      }
     }
-    found = r;
-    found_rest = u - at;
+  {
+    const int64_t at = (int64_t)blockIdx.x * (kThreads / 32) + warp, step = (int64_t)gridDim.x * (kThreads / 32);
+    const int start = p.a.R > 0 ? min(max(p.a.offsets[0], 0), p.a.T) : 0;
+    const int end = p.a.R > 0 ? min(max(p.a.offsets[p.a.R], 0), p.a.T) : 0;
+    attn_no_keys(p, at, start, step, false);
+    attn_no_keys(p, max(start, end) + at, p.a.T, step, false);
+  }
+
+  team = kTeams > 1 && units < kTeamSpan * all_items ? 1 : kTeams;
+  static_assert(kTeams == 1 || kTeams == 4, "a grain is a unit of each warp");
+  const int most = team == kTeams ? p.workers / kTeams : p.workers;
+  const AttnLine line = attn_line(units, (int)max(min((int64_t)most, attn_quotient(units, p.least)), (int64_t)1),
+                                  kTeams > 1 && team > 1 ? 2 : 0);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.line = line;
+  const int teams = kTeams / team, w0 = (int)blockIdx.x * teams;
+  if (line.units == 0 || w0 >= line.workers) return false;
+  for (int i = 0; i < teams; ++i) {
+    const int64_t at_u = w0 + i < line.workers ? attn_start(line, w0 + i) : 0;
+    if (before <= at_u && at_u < before + mine) {
+      int64_t at = before;
+      int r = r0;
+      for (; r + 1 < r1; ++r) {
+        const int64_t n = attn_units<kRows, kUnit>(p, r);
+        if (at_u < at + n) break;
+        at += n;
+      }
+      found[i] = r;
+      found_rest[i] = at_u - at;
+    }
   }
   __syncthreads();
-  cursor.start(p, found, found_rest);
+  const int i = team == 1 && kTeams > 1 ? warp : 0, w = w0 + i;
+  u = u_end = 0;
+  if (w >= line.workers) return true;
+  u = attn_start(line, w);
+  u_end = attn_start(line, w + 1);
+  cursor.start(p, found[i], found_rest[i]);
+  if (team == 1 && kTeams > 1 ? lane == 0 : threadIdx.x == 0)
+    p.places[w] = {cursor.q.row0, cursor.tile, cursor.head, cursor.rows(p), cursor.from, cursor.span.units};
   return true;
 }
 
@@ -242,18 +334,21 @@ __device__ __forceinline__ float row_scale(float top, float& back) {
 // A row's last step: from its maximum (units of log 2) and divisor, with the
 // sink's term, the factor of its sums, and its lse.
 __device__ __forceinline__ float attn_finish(const AttnArgs& p, int head, float top, float sum, float& lse) {
+  if (top == -INFINITY && sum == 0.f) {  // no key
+    lse = p.a.sinks ? p.a.sinks[head] : -INFINITY;
+    return 0.f;
+  }
   float by = 1.f;
   if (p.a.sinks) {
     const float sink = p.a.sinks[head] * kLog2e, next = fmaxf(top, sink);
     if (next != -INFINITY) {
-      // (a maximum of -inf: no key, or none but NaN scores)
-      by = top == -INFINITY ? (sum == sum ? 0.f : 1.f) : exp2_approx(top - next);
+      by = top == -INFINITY ? 1.f : exp2_approx(top - next);  // (-inf: none but NaN scores)
       sum = sum * by + exp2_approx(sink - next);
       top = next;
     }
   }
-  lse = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) * kLn2 + logf(sum);
-  return sum == 0.f ? 0.f : p.a.v_scale * by / sum;
+  lse = (top == -INFINITY ? 0.f : top) * kLn2 + logf(sum);
+  return p.a.v_scale * by / sum;
 }
 
 __device__ __forceinline__ __nv_bfloat16* attn_out(const AttnArgs& p, int token, int head) {
@@ -271,105 +366,137 @@ __device__ __forceinline__ float* attn_stats(const AttnArgs& p, int64_t part, in
   return p.parts + (int64_t)2 * p.workers * kRows * D + (part * kRows + row) * 2;
 }
 
-// CTAs x < workers: x joins the parts of the item that its stretch begins in
-// the middle of, if no earlier stretch does, in the workers' order, kJoinRows
-// rows of it.  The others write the rows that no worker has: queries that see
-// no key, and rows behind the last sequence.
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinParts = 64;  // parts at a time
 
-template <int D, int kRows, int kUnit>
-__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(AttnArgs p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  if ((int)blockIdx.x < p.workers) {
-    const int64_t units = p.prefix[p.a.R];
-    const int workers = attn_workers(p, units), w = blockIdx.x;
-    if (w == 0 || w >= workers || units == 0) return;
-    const int64_t u = attn_start(w, units, workers);
-    int lo = 0, hi = p.a.R;  // prefix[lo] <= u < prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.prefix[mid] <= u)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    AttnCursor<kRows, kUnit> c;
-    c.start(p, lo, u - p.prefix[lo]);
-    const int64_t u0 = u - c.from;
-    if (c.from == 0 || attn_start(w - 1, units, workers) > u0) return;
-    const int last = attn_owner(u0 + c.span.units - 1, units, workers);
-    const int row0 = blockIdx.y * kJoinRows, rows = min(c.rows(p) - row0, kJoinRows);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kJoinThreads) {
-      const int row = row0 + i / (D / 4), d = 4 * (i % (D / 4));
-      float top = -INFINITY, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int x = w - 1; x <= last; ++x) {
-        const int64_t part = 2 * (int64_t)x + (x == w - 1 ? 1 : 0);
-        const float2 st = *reinterpret_cast<const float2*>(attn_stats<D, kRows>(p, part, row));
-        const float4 v = *reinterpret_cast<const float4*>(p.parts + (part * kRows + row) * D + d);
-        const float next = fmaxf(top, st.x);
-        const float old_by = top == next ? 1.f : exp2_approx(top - next);
-        const float new_by = st.x == next ? 1.f : exp2_approx(st.x - next);
-        top = next;
-        sum = sum * old_by + st.y * new_by;
-        acc.x = acc.x * old_by + v.x * new_by;
-        acc.y = acc.y * old_by + v.y * new_by;
-        acc.z = acc.z * old_by + v.z * new_by;
-        acc.w = acc.w * old_by + v.w * new_by;
+// The parts of the item that worker w's stretch begins in the middle of: w -
+// 1's second place and the first ones of w .. last, summed in that order.
+template <int D, int kRows, int kJoin>
+__device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at, int w, int last) {
+  // a thread has four columns of a row, kGroups threads the same, kTurns times
+  constexpr int kQuads = D / 4;
+  constexpr int kBusy = kJoin * kQuads < kJoinThreads ? kJoin * kQuads : kJoinThreads;
+  constexpr int kGroups = kJoinThreads / kBusy, kTurns = kJoin * kQuads / kBusy;
+  __shared__ float factor[kJoin][kJoinParts];
+  __shared__ float old_factor[kJoin], tops[kJoin], sums[kJoin];
+  __shared__ float4 shared_acc[kGroups > 1 ? kJoinThreads : 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.y * kJoin, rows = min(at.rows - row0, kJoin);
+  if (rows <= 0) return;
+  const int parts = last - w + 2;
+  auto part_of = [&](int x) { return 2 * (int64_t)(w - 1 + x) + (x == 0 ? 1 : 0); };
+  __syncthreads();  // (the item before this one is done with what they share)
+  float4 acc[kTurns];
+#pragma unroll
+  for (int y = 0; y < kTurns; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x < kJoin) tops[threadIdx.x] = -INFINITY, sums[threadIdx.x] = 0.f;
+  for (int x0 = 0; x0 < parts; x0 += kJoinParts) {
+    const int n = min(parts - x0, kJoinParts);
+    __syncthreads();
+    for (int row = warp; row < rows; row += kJoinThreads / 32) {
+      float mx[kJoinParts / 32], lx[kJoinParts / 32];
+      float top = tops[row];
+      const float before = top;
+#pragma unroll
+      for (int y = 0; y < kJoinParts / 32; ++y) {
+        const int x = lane + 32 * y;
+        const float2 st = x < n ? *reinterpret_cast<const float2*>(attn_stats<D, kRows>(p, part_of(x0 + x), row0 + row))
+                                : make_float2(-INFINITY, 0.f);
+        mx[y] = st.x, lx[y] = st.y;
+        top = fmaxf(top, st.x);
       }
-      const int rr = c.tile * kRows + row, token = c.q.row0 + rr / p.group, hq = c.head * p.group + rr % p.group;
-      float lse;
-      const float inv = attn_finish(p, hq, top, sum, lse);
-      *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (p.a.lse && d == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
-    }
-    return;
-  }
-  if (blockIdx.y > 0) return;
-  const int token = (blockIdx.x - p.workers) * kJoinThreads + threadIdx.x;
-  bool none = false, inside = false;  // sees no key; is a request's
-  if (token < p.a.T) {
-    inside = p.a.R > 0 && token >= p.a.offsets[0] && token < p.a.offsets[p.a.R];
-    none = !inside;
-    if (inside) {
-      int lo = 0, hi = p.a.R;  // offsets[lo] <= token < offsets[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.a.offsets[mid] <= token)
-          lo = mid;
-        else
-          hi = mid;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      float sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < kJoinParts / 32; ++y) {
+        // (equal: both may be -inf, of parts without a key, or of NaN scores)
+        const float by = mx[y] == top ? 1.f : exp2_approx(mx[y] - top);
+        factor[row][lane + 32 * y] = by;
+        sum += lx[y] * by;
       }
-      const AttnRequest q = attn_request(p, lo);
-      none = attn_span<1>(p, q, (token - q.row0) * p.group, p.group).units == 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      __syncwarp();
+      if (lane == 0) {
+        const float by = before == top ? 1.f : exp2_approx(before - top);
+        old_factor[row] = by;
+        sums[row] = sums[row] * by + sum;
+        tops[row] = top;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int y = 0; y < kTurns; ++y) {
+      const int i = threadIdx.x % kBusy + y * kBusy, row = i / kQuads, d = 4 * (i % kQuads);
+      if (row >= rows) continue;
+      const float by = old_factor[row];
+      acc[y].x *= by, acc[y].y *= by, acc[y].z *= by, acc[y].w *= by;
+#pragma unroll 8
+      for (int x = threadIdx.x / kBusy; x < n; x += kGroups) {
+        const float4 v = *reinterpret_cast<const float4*>(p.parts + (part_of(x0 + x) * kRows + row0 + row) * D + d);
+        const float f = factor[row][x];
+        acc[y].x += v.x * f, acc[y].y += v.y * f, acc[y].z += v.z * f, acc[y].w += v.w * f;
+      }
     }
   }
-  const int warp0 = token - (threadIdx.x & 31), lane = threadIdx.x & 31;
-  const unsigned real = __ballot_sync(0xffffffffu, inside);
-  for (unsigned todo = __ballot_sync(0xffffffffu, none); todo; todo &= todo - 1) {
-    const int at = __ffs(todo) - 1, t = warp0 + at;
-    for (int i = lane; i < p.a.Hq * (D / 8); i += 32)
-      *reinterpret_cast<uint4*>(attn_out(p, t, i / (D / 8)) + 8 * (i % (D / 8))) = make_uint4(0, 0, 0, 0);
-    if (p.a.lse)
-      for (int h = lane; h < p.a.Hq; h += 32)
-        p.a.lse[(int64_t)t * p.a.Hq + h] = (real >> at & 1u) && p.a.sinks ? p.a.sinks[h] : -INFINITY;
+  if constexpr (kGroups > 1) {  // (one turn)
+    shared_acc[threadIdx.x] = acc[0];
+    __syncthreads();
+    if (threadIdx.x >= kBusy) return;
+#pragma unroll
+    for (int y = 1; y < kGroups; ++y) {
+      const float4 v = shared_acc[threadIdx.x + y * kBusy];
+      acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+    }
+  }
+#pragma unroll
+  for (int y = 0; y < kTurns; ++y) {
+    const int i = threadIdx.x % kBusy + y * kBusy, row = i / kQuads, d = 4 * (i % kQuads);
+    if (row >= rows) continue;
+    const int rr = at.tile * kRows + row0 + row, token = at.row0 + rr / p.group, hq = at.head * p.group + rr % p.group;
+    float lse;
+    const float inv = attn_finish(p, hq, tops[row], sums[row], lse);
+    *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
+        make_uint2(pack_bf16x2(acc[y].x * inv, acc[y].y * inv), pack_bf16x2(acc[y].z * inv, acc[y].w * inv));
+    if (p.a.lse && d == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
   }
 }
 
-template <int D, int kRows, int kUnit>
-cudaError_t launch_attention_join(const AttnArgs& p, cudaStream_t st) {
+// Joins each item that workers share, kJoin rows to a CTA, where the first
+// stretch that begins in its middle does.  The CTAs look through the workers
+// 32 at a time.
+template <int D, int kRows, int kJoin>
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(AttnArgs p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const AttnLine line = *p.line;
+  for (int w0 = blockIdx.x; w0 < line.workers && line.units > 0; w0 += 32 * gridDim.x) {
+    const int mine = w0 + (threadIdx.x & 31) * (int)gridDim.x;
+    bool joins = false;
+    if (mine > 0 && mine < line.workers) {
+      const int from = p.places[mine].from;
+      joins = from != 0 && attn_start(line, mine - 1) <= attn_start(line, mine) - from;
+    }
+    for (unsigned todo = __ballot_sync(0xffffffffu, joins); todo; todo &= todo - 1) {
+      const int w = w0 + (__ffs(todo) - 1) * (int)gridDim.x;
+      const AttnPlace at = p.places[w];
+      attn_join<D, kRows, kJoin>(p, at, w, attn_owner(line, attn_start(line, w) - at.from + at.units - 1));
+    }
+  }
+}
+
+template <int D, int kRows, int kJoin>
+cudaError_t launch_attention_join(const AttnArgs& p, int sms, cudaStream_t st) {
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)(p.workers + ceil_div(p.a.T, kJoinThreads)), (unsigned)ceil_div(kRows, kJoinRows));
+  c.gridDim = dim3((unsigned)min(p.workers, 2 * sms), (unsigned)(kRows / kJoin));
   c.blockDim = dim3(kJoinThreads);
   c.stream = st;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, attention_join_kernel<D, kRows, kUnit>, p);
+  return cudaLaunchKernelEx(&c, attention_join_kernel<D, kRows, kJoin>, p);
 }
 
 }  // namespace moe_fp4

@@ -850,7 +850,7 @@ MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, 
  * (p < 0) gets out 0 and lse sinks[h], or -inf.  Rows of q behind
  * offsets[R] get 0 and -inf.  What lies in the cache outside the keys a query
  * sees does not touch its output, NaN included.  A key with a NaN scale makes
- * the queries that see it NaN; NaN scales of values count as 0 (the store
+ * the queries that see it NaN; NaN scales of values count as 448 (the store
  * above marks the keys of a token with non-finite values, too).  A page
  * number outside [0, pages) reads as NaN keys.  Tokens past table_width *
  * page_size are not looked for.

@@ -170,8 +170,8 @@ def test_values_nan_scales_and_bad_pages(new):
     b = Batch([100, 50], D, 1, 16)
     q = queries(2 * new, 2, D, 1)
     page = int(b.tables[0, 2])
-    b.cache[page, 0, 0, 1, 8 * D:] = 0x7f  # the values of tokens 32 .. 47
-    b.v[0][32:48] = 0
+    b.cache[page, 0, 0, 1, :8 * D], b.cache[page, 0, 0, 1, 8 * D:] = 0x22, 0x7f  # the values of tokens 32 .. 47
+    b.v[0][32:48] = 448
     for wrong in (-1, b.cache.shape[0], 2 ** 31 - 1):
         tables = b.tables.clone()
         tables[1, 1] = wrong

@@ -159,13 +159,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     int last[NT][2];  // position of the columns' queries, -1: no row
     const int base_pos = q.length - q.n;
     const int rows = c.rows(p);
+    const AttnRows tile_rows = attn_rows(p, tile * kRows);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = tile * kRows + 8 * n + g;
+      const AttnRows row = attn_row(p, tile_rows, 8 * n + g);
       float v[D / 4], top = 0.f;
       const bool real = 8 * n + g < rows;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(q.row0 + row / p.group) * p.a.q_row +
-                                 (int64_t)(head * p.group + row % p.group) * p.a.q_head + t * (D / 4);
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)(q.row0 + row.query) * p.a.q_row +
+                                 (int64_t)(head * p.group + row.head) * p.a.q_head + t * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 w = real ? *reinterpret_cast<const uint4*>(src + 8 * i) : make_uint4(0, 0, 0, 0);
@@ -191,12 +192,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
       for (int c = 0; c < 2; ++c) {
         fac[n][c] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + c)) * (p.a.scale * p.a.k_scale * kLog2e);
         const int col = 8 * n + 2 * t + c;
-        last[n][c] = col < rows ? base_pos + (tile * kRows + col) / p.group : -1;
+        last[n][c] = col < rows ? base_pos + attn_row(p, tile_rows, col).query : -1;
       }
     }
     // blocks that every row sees whole
-    const int pos_first = base_pos + tile * kRows / p.group;
-    const int pos_last = base_pos + (tile * kRows + rows - 1) / p.group;
+    const int pos_first = base_pos + tile_rows.query;
+    const int pos_last = base_pos + attn_row(p, tile_rows, rows - 1).query;
     const int all_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
 
     float o[NT][kSteps][4], m[NT][2], minus[NT][2], l[NT][2];  // (minus: -m, or 0 while that is -inf)
@@ -417,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
             if (g == 0) *reinterpret_cast<float2*>(attn_stats<D, kRows>(p, part, row)) = make_float2(m[n][c2], l[n][c2]);
             continue;
           }
-          const int rr = tile * kRows + row, token = q.row0 + rr / p.group, hq = head * p.group + rr % p.group;
+          const AttnRows rr = attn_row(p, tile_rows, row);
+          const int token = q.row0 + rr.query, hq = head * p.group + rr.head;
           float lse;
           const float inv = attn_finish(p, hq, m[n][c2], l[n][c2], lse);
           __nv_bfloat16* dst = attn_out(p, token, hq) + g * (D / 8);
@@ -474,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         if (d == 0) *reinterpret_cast<float2*>(attn_stats<D, kRows>(p, part, row)) = make_float2(top, sum);
         continue;
       }
-      const int rr = tile * kRows + row, token = q.row0 + rr / p.group, hq = head * p.group + rr % p.group;
+      const AttnRows rr = attn_row(p, tile_rows, row);
+      const int token = q.row0 + rr.query, hq = head * p.group + rr.head;
       float lse;
       const float inv = attn_finish(p, hq, top, sum, lse);
       *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
@@ -510,7 +513,7 @@ template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
   // rows that an average request has to a key head
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
-  if (rows > 32) return launch_attention_tc(p, sms, st);
+  if (rows > 12) return launch_attention_tc(p, sms, st);
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);
 }
 
@@ -537,6 +540,7 @@ cudaError_t launch_attention(const moe_fp4_attention_args& a, cudaStream_t st) {
   AttnArgs p = {};
   p.a = a;
   p.group = a.Hq / a.Hkv;
+  p.inverse = (65536 + p.group - 1) / p.group;
   p.capacity = a.table_width * a.page_size;
   p.line = static_cast<AttnLine*>(a.workspace);
   p.places = reinterpret_cast<AttnPlace*>(static_cast<char*>(a.workspace) + 256);

@@ -44,33 +44,64 @@ struct TcCfg {
   static constexpr uint32_t kHalf = kBlocks * cache_half_bytes(D);
   static constexpr int kRaw = D == 64 ? 6 : 3;   // half steps in flight
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kDecWarps = kTiles == 2 ? 4 : 8;
-  static constexpr int kThreads = 32 * 16;       // (whole warpgroups, for the split of registers)
-  static constexpr int kMmaWarp = 12, kLoadWarp = 13;
+  static constexpr int kDecWarps = 8;
+  static constexpr int kMmaWarp = kSoftWarps + kDecWarps, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole warpgroups, for the split of registers)
+  // registers of the softmax, the decode and the last warpgroup's threads: together no more than the launch's
+  static constexpr int kSoftRegs = kTiles == 2 ? 136 : 208, kDecRegs = kTiles == 2 ? 72 : 88, kLastRegs = kTiles == 2 ? 64 : 80;
+  static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
+  static_assert(32 * (kSoftWarps * kSoftRegs + kDecWarps * kDecRegs + 4 * kLastRegs) <= kThreads * kLaunchRegs, "registers");
   static constexpr uint32_t kTmemO = 2 * 128;    // the sums lie behind two buffers of scores
   static constexpr uint32_t kBytes = kTiles * kQTile + 4 * kKv + kRaw * kHalf;
   static constexpr uint32_t kBarBytes = 512;
   static constexpr uint32_t kSmem = kBytes + kBarBytes + 1024 /*align*/;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kTmemO + kTiles * D <= 512, "tensor memory");
-  static_assert(kSoftWarps + kDecWarps == 12, "three warpgroups, then MMA and loads");
 };
 
-// Shared-memory descriptor of an operand whose rows of 128 bytes are its
-// N direction (64 values) and go along K: 8 rows to a swizzled group of 1024
-// bytes, `panel` bytes to the next 64 values.
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t saddr, uint32_t panel) {
-  return smem_desc(saddr, panel, 1024, kLayoutSW128);
+// The low word of an operand's shared-memory descriptor (its address; offsets
+// in units of 16 bytes add to it), and the high words of the two kinds: rows
+// of 128 bytes along K, eight to a swizzled group of 1024 bytes; and, for the
+// values, rows along N, with `lbo` (in the low word) to the next 64 of N.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return (uint32_t)smem_desc(saddr, lbo, 1024, kLayoutSW128);
+}
+__device__ __forceinline__ uint32_t desc_hi() { return (uint32_t)(smem_desc(0, 16, 1024, kLayoutSW128) >> 32); }
+
+// Four K = 16 steps of D (+)= A B from a converged warp, operands kA and kB
+// units of 16 bytes apart from step to step; the first adds to D if `add`.
+template <int kA, int kB>
+__device__ __forceinline__ void mma_f16_4(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 da, db;\n\t.reg .b32 ta, tb;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 q, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t"
+      "add.u32 ta, %1, %6;\n\tadd.u32 tb, %2, %7;\n\tmov.b64 da, {ta, %3};\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, q;\n\t"
+      "add.u32 ta, ta, %6;\n\tadd.u32 tb, tb, %7;\n\tmov.b64 da, {ta, %3};\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, q;\n\t"
+      "add.u32 ta, ta, %6;\n\tadd.u32 tb, tb, %7;\n\tmov.b64 da, {ta, %3};\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, q;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(add ? 1u : 0u), "n"(kA), "n"(kB)
+      : "memory");
 }
 
-// D (+)= A B with A (FP16, a row per lane, two values a column) in tensor
-// memory, from a converged warp.
-__device__ __forceinline__ void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                bool accumulate) {
+// The same with A (FP16, a row per lane, two values a column) in tensor memory.
+template <int kB>
+__device__ __forceinline__ void mma_f16_ts_4(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 db;\n\t.reg .b32 ta, tb;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\tsetp.eq.u32 q, %4, %4;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t"
+      "add.u32 ta, %1, 8;\n\tadd.u32 tb, %2, %6;\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, q;\n\t"
+      "add.u32 ta, ta, 8;\n\tadd.u32 tb, tb, %6;\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, q;\n\t"
+      "add.u32 ta, ta, 8;\n\tadd.u32 tb, tb, %6;\n\tmov.b64 db, {tb, %3};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [ta], db, %4, q;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(add ? 1u : 0u), "n"(kB)
       : "memory");
 }
 
@@ -80,6 +111,12 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
       "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0,%1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
@@ -126,10 +163,17 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
   }
   pdl_wait();
   pdl_launch_dependents();
-  AttnCursor<C::kRows, kTok> c;
-  int64_t u, u_end;
-  int team;
-  if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, c, u, u_end, team)) return;
+  // each warp's place in its CTA's stretch (in shared memory: its registers
+  // are worth more to the loops between items)
+  __shared__ AttnCursor<C::kRows, kTok> cursors[C::kThreads / 32];
+  AttnCursor<C::kRows, kTok>& c = cursors[warp];
+  int left;  // units of the stretch that are left
+  {
+    int64_t u, u_end;
+    int team;
+    if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, c, u, u_end, team)) return;
+    left = (int)(u_end - u);
+  }
 
   if (warp == C::kMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -142,14 +186,14 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
   };
 
   if (warp >= C::kSoftWarps + C::kDecWarps) {
-    regs_dec<64>();
+    regs_dec<C::kLastRegs>();
     if (warp == C::kLoadWarp) {
       const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
       const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);
       uint32_t half = 0;
       bool ok = true;
-      while (ok && u < u_end) {
-        const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+      while (ok && left > 0) {
+        const int steps = min(c.span.units - c.from, left);
         const int end_block = (c.span.hi + kCacheBlock - 1) / kCacheBlock;
         const int32_t* table = p.a.tables + (int64_t)c.r * p.a.table_row;
         int b = (c.span.first + c.from) * C::kBlocks + lane;
@@ -179,35 +223,36 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
           }
           if (!ok) break;
         }
-        u += steps;
-        if (u < u_end) c.next(p);
+        left -= steps;
+        if (left > 0) c.next(p);
       }
     } else if (warp == C::kMmaWarp) {
       const uint32_t idesc_s = idesc_f16(128, kTok), idesc_o = idesc_f16(128, D) | (1u << 16);
       uint32_t step = 0;         // over all items
       uint32_t item = 0;
       bool ok = true;
+      const uint32_t hi = desc_hi();
+      const uint32_t q_lo = desc_lo(smem_u32(q_smem), 16), k_lo = desc_lo(smem_u32(k_smem), 16);
+      const uint32_t v_lo = desc_lo(smem_u32(v_smem), C::kPanel);
       auto scores = [&](int tile, uint32_t at, int buffer) {  // S = Q K^T of step `at` into a buffer
-        const uint32_t q0 = smem_u32(q_smem) + tile * C::kQTile, k0 = smem_u32(k_smem) + (at & 1) * C::kKv;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_warp(tmem + buffer * 128, smem_desc(q0 + (k / 4) * 16384 + (k % 4) * 32, 16, 1024, kLayoutSW128),
-                       smem_desc(k0 + (k / 4) * C::kPanel + (k % 4) * 32, 16, 1024, kLayoutSW128), idesc_s, k > 0);
+        for (int k = 0; k < D / 64; ++k)  // 64 columns: a panel
+          mma_f16_4<2, 2>(tmem + buffer * 128, q_lo + tile * (C::kQTile >> 4) + k * 1024,
+                          k_lo + (at & 1) * (C::kKv >> 4) + k * (C::kPanel >> 4), hi, idesc_s, k > 0);
         mma_commit_warp(&s_full[buffer]);
       };
       auto sums = [&](int tile, uint32_t at, int buffer, bool first) {  // O += P V
-        const uint32_t v0 = smem_u32(v_smem) + (at & 1) * C::kKv;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kTok / 16; ++k)
-          mma_f16_ts_warp(tmem + C::kTmemO + tile * D, tmem + buffer * 128 + 8 * k, desc_n_major(v0 + k * 2048, C::kPanel),
-                          idesc_o, !first || k > 0);
+        for (int k = 0; k < kTok / 64; ++k)  // 16 tokens a step: 2048 bytes
+          mma_f16_ts_4<128>(tmem + C::kTmemO + tile * D, tmem + buffer * 128 + 32 * k,
+                            v_lo + (at & 1) * (C::kKv >> 4) + k * 512, hi, idesc_o, !first || k > 0);
         mma_commit_warp(&pv_done[tile]);
       };
       uint32_t p_seen[2] = {0, 0};
-      while (ok && u < u_end) {
-        const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+      while (ok && left > 0) {
+        const int steps = min(c.span.units - c.from, left);
         if constexpr (kTiles == 2) {
           ok = wait(&kv_full[step & 1], step >> 1);
           for (int n = 0; ok && n < 2; ++n) {
@@ -258,19 +303,19 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
           }
         }
         ++item;
-        u += steps;
-        if (ok && u < u_end) c.next(p);
+        left -= steps;
+        if (ok && left > 0) c.next(p);
       }
     }
   } else if (warp >= C::kSoftWarps) {
     // decode: a unit is 32 values of a token
-    regs_dec<80>();
+    regs_dec<C::kDecRegs>();
     constexpr int kParts = D / 32, kUnits = kTok * kParts, kDecThreads = 32 * C::kDecWarps;
     const int tid = threadIdx.x - 32 * C::kSoftWarps;
     uint32_t half = 0;
     bool ok = true;
-    while (ok && u < u_end) {
-      const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
+    while (ok && left > 0) {
+      const int steps = min(c.span.units - c.from, left);
       for (int i = 0; ok && i < 2 * steps; ++i, ++half) {
         const uint32_t s = half % C::kRaw, step = half >> 1, kind = half & 1, buf = 2 * kind + (step & 1), round = step >> 1;
         ok = wait(&raw_full[s], half / C::kRaw);
@@ -314,62 +359,74 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
           mbar_arrive(&kv_full[buf]);
         }
       }
-      u += steps;
-      if (ok && u < u_end) c.next(p);
+      left -= steps;
+      if (ok && left > 0) c.next(p);
     }
   } else {
-    regs_inc<kTiles == 2 ? 176 : 208>();
+    regs_inc<C::kSoftRegs>();
     const int n = warp / 4, row_in_tile = threadIdx.x & 127, tile_row = 128 * n + row_in_tile;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_tmem = tmem + lanes + C::kTmemO + n * D;
     uint32_t step = 0;  // over all items
     uint32_t item = 0;
     bool ok = true;
-    while (ok && u < u_end) {
-      const int steps = (int)min((int64_t)c.span.units - c.from, u_end - u);
-      const int rows = c.rows(p), row = c.tile * C::kRows + tile_row;
-      const bool real = tile_row < rows;
-      const int token = c.q.row0 + row / p.group, hq = c.head * p.group + row % p.group;
-      const int base_pos = c.q.length - c.q.n;
-      const int pos = real ? base_pos + row / p.group : -1;
+    while (ok && left > 0) {
+      const int steps = min(c.span.units - c.from, left);
       float fac;
+      const AttnRows tile_rows = attn_rows(p, c.tile * C::kRows);
       {
-        // q in FP16, the sign of the scale with it
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
-                                                          (int64_t)token * p.a.q_row + (int64_t)hq * p.a.q_head);
-        float top = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = real ? src[i] : make_uint4(0, 0, 0, 0);
-          float v[8];
-          bf16x8_to_float(x, v);
+        const int rows = c.rows(p);
+        // q in FP16, the sign of the scale with it: D / 8 lanes to a row, the warp's 32 rows in turn
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
+        const int l = lane % kLanes, side = lane / kLanes, first = 32 * (warp & 3);  // (row of the tile)
+        float back = 1.f;
+        uint8_t* dst = q_smem + n * C::kQTile + (l / 8) * 16384;
+#pragma unroll 1
+        for (int i = 0; i < kTurns; i += 8) {
+          uint4 x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+          for (int y = 0; y < 8; ++y) {
+            const int r = 128 * n + first + (i + y) * kAtOnce + side;
+            const AttnRows rr = attn_row(p, tile_rows, r);
+            x[y] = r < rows ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
+                                                              (int64_t)(c.q.row0 + rr.query) * p.a.q_row +
+                                                              (int64_t)(c.head * p.group + rr.head) * p.a.q_head + 8 * l)
+                            : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const int r = first + (i + y) * kAtOnce + side;
+            float v[8], top = 0.f, b;
+            bf16x8_to_float(x[y], v);
+#pragma unroll
+            for (int z = 0; z < 8; ++z) top = fmaxf(top, fabsf(v[z]));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            float by = row_scale(top, b);
+            by = p.a.scale < 0.f ? -by : p.a.scale == 0.f ? 0.f : by;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((l % 8) ^ (r & 7)) << 4)) =
+                make_uint4(pack_f16x2(v[0] * by, v[1] * by), pack_f16x2(v[2] * by, v[3] * by),
+                           pack_f16x2(v[4] * by, v[5] * by), pack_f16x2(v[6] * by, v[7] * by));
+            const float mine = __shfl_sync(0xffffffffu, b, (lane % kAtOnce) * kLanes);
+            if (lane / kAtOnce == i + y) back = mine;
+          }
         }
-        float back;
-        float by = row_scale(top, back);
         fac = fmaxf(back * fabsf(p.a.scale) * p.a.k_scale * kLog2e, 0x1p-120f);  // (above 0: masked scores stay -inf)
-        by = p.a.scale < 0.f ? -by : p.a.scale == 0.f ? 0.f : by;
-        uint8_t* dst = q_smem + n * C::kQTile + row_in_tile * 128;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 x = real ? src[i] : make_uint4(0, 0, 0, 0);
-          float v[8];
-          bf16x8_to_float(x, v);
-          const uint4 h = make_uint4(pack_f16x2(v[0] * by, v[1] * by), pack_f16x2(v[2] * by, v[3] * by),
-                                     pack_f16x2(v[4] * by, v[5] * by), pack_f16x2(v[6] * by, v[7] * by));
-          *reinterpret_cast<uint4*>(dst + (i / 8) * 16384 + (((i % 8) ^ (row_in_tile & 7)) << 4)) = h;
-        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[n]);
       }
-      // steps that every row of the tile sees whole
-      const int pos_first = base_pos + (c.tile * C::kRows + 128 * n) / p.group;
-      const int pos_last = base_pos + (c.tile * C::kRows + min(128 * n + 128, rows) - 1) / p.group;
-      const int all_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
-      const int lowest = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;  // first token that the row sees
+      int pos, lowest;          // the row's position, the first token that it sees
+      int whole_lo, whole_hi;   // tokens that every row of the tile sees
+      {
+        const int rows = c.rows(p), base_pos = c.q.length - c.q.n;
+        pos = tile_row < rows ? base_pos + attn_row(p, tile_rows, tile_row).query : -1;
+        lowest = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
+        const int pos_last = base_pos + attn_row(p, tile_rows, min(128 * n + 128, rows) - 1).query;
+        whole_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
+        whole_hi = base_pos + attn_row(p, tile_rows, 128 * n).query;
+      }
 
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
@@ -382,27 +439,51 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
         }
         tc_fence_after();
         const uint32_t s_tmem = tmem + lanes + buffer * 128;
-        uint32_t s[kTok / 32][32];
-#pragma unroll
-        for (int x = 0; x < kTok / 32; ++x) TmemLd<32>::start(s_tmem + 32 * x, s[x]);
-#pragma unroll
-        for (int x = 0; x < kTok / 32; ++x) TmemLd<32>::wait(s[x]);
-        if (!(tok0 >= all_lo && tok0 + kTok - 1 <= pos_first)) {
+        if (tok0 < whole_lo || tok0 + kTok - 1 > whole_hi) {
+          // masked where they are, so that the loop below has no test for it
+          // (as predicates there, they took as many instructions as the rest)
           const int hi = pos - tok0, lo = lowest - tok0;
+#pragma unroll 1
+          for (int x = 0; x < kTok; x += 16) {
+            uint32_t s[16];
+            tmem_ld16(s_tmem + x, s);
 #pragma unroll
-          for (int x = 0; x < kTok / 32; ++x)
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (32 * x + y > hi || 32 * x + y < lo) s[x][y] = 0xff800000u;
+            for (int y = 0; y < 16; ++y)
+              if (x + y > hi || x + y < lo) s[y] = 0xff800000u;
+            tmem_st16(s_tmem + x, s);
+          }
+          tmem_wait_st();
         }
-        float top = -INFINITY;
+        uint32_t h[kTok / 2];
+        float2 sum[2];  // (sums and maxima in chains of their own, which depend on one another less)
+        // against the maximum so far; where a score outgrows it, once more against its own
+#pragma unroll 1
+        for (int pass = 0;; ++pass) {
+          const float from_m = m == -INFINITY ? 0.f : m;
+          const float2 fac2 = make_float2(fac, fac), minus = make_float2(-from_m, -from_m);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          uint32_t s[2][16];
+          TmemLd<16>::start(s_tmem, s[0]);
 #pragma unroll
-        for (int x = 0; x < kTok / 32; ++x)
+          for (int x = 0; x < kTok / 16; ++x) {
+            TmemLd<16>::wait(s[x & 1]);
+            if (x + 1 < kTok / 16) TmemLd<16>::start(s_tmem + 16 * (x + 1), s[(x + 1) & 1]);
 #pragma unroll
-          for (int y = 0; y < 32; y += 2) top = fmaxf(fmaxf(top, __uint_as_float(s[x][y])), __uint_as_float(s[x][y + 1]));
-        top *= fac;
-        const bool grows = top > m + 8.f || (m == -INFINITY && top > m);
-        if (__any_sync(0xffffffffu, grows)) {
+            for (int y = 0; y < 16; y += 2)
+              tops[y / 2 % 4] = max3(tops[y / 2 % 4], __uint_as_float(s[x & 1][y]), __uint_as_float(s[x & 1][y + 1]));
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              float2 e = ffma2(make_float2(__uint_as_float(s[x & 1][2 * y]), __uint_as_float(s[x & 1][2 * y + 1])), fac2, minus);
+              e.x = exp2_approx(e.x);
+              e.y = exp2_approx(e.y);
+              sum[y & 1] = fadd2(sum[y & 1], e);
+              h[8 * x + y] = pack_f16x2(e.x, e.y);
+            }
+          }
+          const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * fac;
+          const bool grows = top > m + 8.f;  // (m -inf: as soon as there is a key)
+          if (!__any_sync(0xffffffffu, grows) || pass > 0) break;
           const float by = grows ? exp2_approx(m - top) : 1.f;
           if (grows) m = top;
           l.x *= by;
@@ -423,21 +504,10 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
             }
           }
         }
-        const float from_m = m == -INFINITY ? 0.f : m;
-        const float2 fac2 = make_float2(fac, fac), minus = make_float2(-from_m, -from_m);
+        if (!ok) break;
+        l = fadd2(l, fadd2(sum[0], sum[1]));
 #pragma unroll
-        for (int x = 0; x < kTok / 32; ++x) {
-          uint32_t h[16];
-#pragma unroll
-          for (int y = 0; y < 16; ++y) {
-            float2 e = ffma2(make_float2(__uint_as_float(s[x][2 * y]), __uint_as_float(s[x][2 * y + 1])), fac2, minus);
-            e.x = exp2_approx(e.x);
-            e.y = exp2_approx(e.y);
-            l = fadd2(l, e);
-            h[y] = pack_f16x2(e.x, e.y);
-          }
-          tmem_st16(s_tmem + 16 * x, h);
-        }
+        for (int x = 0; x < kTok / 32; ++x) tmem_st16(s_tmem + 16 * x, *reinterpret_cast<uint32_t(*)[16]>(&h[16 * x]));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -448,39 +518,64 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
       if (kTiles == 1 && steps > 1 && ok) ok = wait(&pv_done[n], step - 2);
       if (!ok || !wait(&pv_done[n], step - 1)) break;
       tc_fence_after();
+      // The sums go out by way of the queries' place (the item's scores are
+      // all done): 128 bytes of a row at a time, so that stores lie along rows.
+      const int rows = c.rows(p);
       const float sum = l.x + l.y;
       const bool whole = c.from == 0 && steps == c.span.units;
-      float lse = 0.f, inv = 0.f;
-      float* part = nullptr;
-      if (whole) {
-        if (real) inv = attn_finish(p, hq, m, sum, lse);
-        if (real && p.a.lse) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
-      } else {
-        const int64_t at = 2 * (int64_t)blockIdx.x + (c.from == 0 ? 1 : 0);
-        part = p.parts + (at * C::kRows + tile_row) * D;
-        if (real) *reinterpret_cast<float2*>(attn_stats<D, C::kRows>(p, at, tile_row)) = make_float2(m, sum);
+      const int64_t part = 2 * (int64_t)blockIdx.x + (c.from == 0 ? 1 : 0);
+      float inv = 1.f;
+      if (tile_row < rows) {
+        if (whole) {
+          const AttnRows rr = attn_row(p, tile_rows, tile_row);
+          const int hq = c.head * p.group + rr.head;
+          float lse;
+          inv = attn_finish(p, hq, m, sum, lse);
+          if (p.a.lse) p.a.lse[(int64_t)(c.q.row0 + rr.query) * p.a.Hq + hq] = lse;
+        } else {
+          *reinterpret_cast<float2*>(attn_stats<D, C::kRows>(p, part, tile_row)) = make_float2(m, sum);
+        }
       }
-      __nv_bfloat16* out = attn_out(p, token, hq);
+      uint8_t* stage = q_smem + n * C::kQTile + (warp & 3) * 32 * 128;  // 32 rows of 128 bytes, the warp's own
+      const int chunk_row = lane / 8, chunk = lane % 8, row0 = 128 * n + 32 * (warp & 3);
+      const int columns = whole ? 64 : 32;  // of 128 bytes
 #pragma unroll 1
-      for (int x = 0; x < D / 16; ++x) {
-        uint32_t o[16];
-        tmem_ld16(o_tmem + 16 * x, o);
-        if (real && whole) {
-          uint32_t w[8];
+      for (int x = 0; x < D; x += columns) {
+        uint32_t o[32];
+        if (whole) {
 #pragma unroll
-          for (int y = 0; y < 8; ++y) w[y] = pack_bf16x2(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
-          *reinterpret_cast<uint4*>(out + 16 * x) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(out + 16 * x + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-        } else if (real) {
+          for (int y = 0; y < 2; ++y) {
+            uint32_t f[32];
+            tmem_ld32(o_tmem + x + 32 * y, f);
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<uint4*>(part + 16 * x + 4 * y) = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+            for (int z = 0; z < 16; ++z)
+              o[16 * y + z] = pack_bf16x2(__uint_as_float(f[2 * z]) * inv, __uint_as_float(f[2 * z + 1]) * inv);
+          }
+        } else {
+          tmem_ld32(o_tmem + x, o);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) =
+              make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const int r = 4 * y + chunk_row;
+          if (row0 + r >= rows) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
+          const AttnRows rr = attn_row(p, tile_rows, row0 + r);
+          if (whole)
+            *reinterpret_cast<uint4*>(attn_out(p, c.q.row0 + rr.query, c.head * p.group + rr.head) + x + 8 * chunk) = v;
+          else
+            *reinterpret_cast<uint4*>(p.parts + (part * C::kRows + row0 + r) * D + x + 4 * chunk) = v;
         }
         __syncwarp();
       }
       ++item;
-      u += steps;
-      if (u < u_end) c.next(p);
+      left -= steps;
+      if (left > 0) c.next(p);
     }
   }
   tc_fence_before();

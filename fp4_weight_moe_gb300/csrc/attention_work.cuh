@@ -31,7 +31,7 @@ struct AttnPlace {  // where a worker's stretch begins
 
 struct AttnArgs {
   moe_fp4_attention_args a;
-  int group;         // Hq / Hkv
+  int group, inverse; // Hq / Hkv, and 2^16 over it, rounded up
   int capacity;      // tokens that a table row holds
   float* parts;      // [2 workers][kRows][D] sums, then [2 workers][kRows][2] maximum and divisor
   AttnLine* line;
@@ -55,6 +55,20 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs& p, int r) {
   q.n = max(min(p.a.offsets[r + 1], p.a.T) - q.row0, 0);
   q.length = max(p.a.lengths[r], 0);
   return q;
+}
+
+// Rows of a tile as queries and heads of the group.
+struct AttnRows {
+  int query, head;  // of the tile's first row
+};
+__device__ __forceinline__ AttnRows attn_rows(const AttnArgs& p, int row) {
+  const int query = row / p.group;
+  return {query, row - query * p.group};
+}
+// Row `row` of the tile (a division of less than 1024 by at most 64: exact).
+__device__ __forceinline__ AttnRows attn_row(const AttnArgs& p, const AttnRows& first, int row) {
+  const int at = first.head + row, query = (at * p.inverse) >> 16;
+  return {first.query + query, at - query * p.group};
 }
 
 // The keys that rows [row, row + rows) of a request see: [lo, hi), in units.
@@ -453,7 +467,8 @@ __device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at
   for (int y = 0; y < kTurns; ++y) {
     const int i = threadIdx.x % kBusy + y * kBusy, row = i / kQuads, d = 4 * (i % kQuads);
     if (row >= rows) continue;
-    const int rr = at.tile * kRows + row0 + row, token = at.row0 + rr / p.group, hq = at.head * p.group + rr % p.group;
+    const AttnRows r = attn_row(p, attn_rows(p, at.tile * kRows), row0 + row);
+    const int token = at.row0 + r.query, hq = at.head * p.group + r.head;
     float lse;
     const float inv = attn_finish(p, hq, tops[row], sums[row], lse);
     *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =

@@ -8,13 +8,16 @@
 // their values), with every load under way before the first sum.  The
 // rotation's partner column i + rot / 2 is rot / 16 lanes away, a shuffle.
 //
-// Keys bound for the cache are computed in pairs of FP32 numbers (value and
-// rest; sums and products without error by the published steps of D. E. Knuth,
-// TAOCP 2, 4.2.2, and T. J. Dekker, "A floating-point technique for extending
-// the available precision", 1971), good to about 2^-44: rounded to FP32 that
-// is the number next to the formula's, whatever order sums are taken in, and
-// so are its codes.  Straight FP32 is off by a unit or two, which moves about
-// one code in 10^7 across a border of its rounding, by a third of its value.
+// Keys bound for the cache have to give the codes of the FP32 number next to
+// the formula's, whatever order sums are taken in; straight FP32 is off by a
+// few units, which moves about one code in 10^7 across a border of its
+// rounding, by a third of its value.  So each key is quantised from FP32 with
+// its bound of error added and taken away: where both give the same scales and
+// codes (all but one head in a hundred) they are the right ones.  The others
+// are computed again in pairs of FP32 numbers (value and rest; sums and
+// products without error by the published steps of D. E. Knuth, TAOCP 2,
+// 4.2.2, and T. J. Dekker, "A floating-point technique for extending the
+// available precision", 1971), good to about 2^-44.
 #include "attention.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"
@@ -23,7 +26,7 @@ namespace moe_fp4 {
 namespace {
 
 constexpr int kRopeThreads = 128;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;
 
 // hi + lo, |lo| at most half a unit of hi.
 struct Pair {
@@ -55,15 +58,8 @@ __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
 __device__ __forceinline__ Pair lane_xor(Pair v, int o) {
   return {__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)};
 }
-__device__ __forceinline__ float lane_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-
-__device__ __forceinline__ void set(float& v, float x) { v = x; }
-__device__ __forceinline__ void set(Pair& v, float x) { v = {x, 0.f}; }
-__device__ __forceinline__ float value(Pair v) { return __fadd_rn(v.hi, v.lo); }
-
 // 1 / sqrt(x): the hardware's approximation, and for a pair a step of
 // y + y (r / 2 + 3 r^2 / 8) from the exact rest r = 1 - x y^2.
-__device__ __forceinline__ float inverse_root(float x) { return rsqrtf(x); }
 __device__ __forceinline__ Pair inverse_root(Pair x) {
   const float y = rsqrtf(x.hi);
   const Pair y2 = two_prod(y, y);
@@ -74,14 +70,14 @@ __device__ __forceinline__ Pair inverse_root(Pair x) {
   return {y, y * r * __fmaf_rn(0.375f, r, 0.5f)};
 }
 
-// A lane's factors of the rotation, the weights among them: column i becomes
-// x_i own_i + partner_i other_i, times the norm.
-struct Factors {
-  float c[8], s[8], w[8], w_other[8];  // (s with its sign)
+// The weights of a lane's columns and of their partners', and the angles of a
+// position (halves: eight; interleaved: four pairs').
+struct Weights {
+  float own[8], other[8];
 };
-
-__device__ __forceinline__ float product(float a, float b, float) { return a * b; }
-__device__ __forceinline__ Pair product(float a, float b, Pair) { return two_prod(a, b); }
+struct Angles {
+  float4 c[2], s[2];
+};
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
   const uint32_t p[4] = {u.x, u.y, u.z, u.w};
@@ -92,14 +88,87 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&v)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  uint32_t p[4];
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// A lane's part in a head: its place, and the lane of the rotation's partners.
+struct Lane {
+  int l, half, l_other, from;
+  bool turned, low;
+};
+template <int D>
+__device__ __forceinline__ Lane lane_of(const moe_fp4_qk_norm_rope_args& a, int lane) {
+  Lane at;
+  at.l = lane % (D / 8);
+  at.half = a.rot / 16;  // lanes of half the rotated columns
+  at.turned = a.rotary && 8 * at.l < a.rot;
+  at.low = at.l < at.half;
+  at.l_other = at.turned && !a.interleaved ? (at.low ? at.l + at.half : at.l - at.half) : at.l;
+  at.from = lane - at.l + at.l_other;
+  return at;
+}
+
+__device__ __forceinline__ void load_weights(Weights& w, const moe_fp4_qk_norm_rope_args& a, const void* wp,
+                                             const Lane& at) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    p[i] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int i = 0; i < 8; ++i) w.own[i] = w.other[i] = 1.f;
+  if (!wp) return;
+  if (a.weights_f32) {
+    const float4* p = static_cast<const float4*>(wp);
+    const float4 x0 = p[2 * at.l], x1 = p[2 * at.l + 1], o0 = p[2 * at.l_other], o1 = p[2 * at.l_other + 1];
+    w.own[0] = x0.x, w.own[1] = x0.y, w.own[2] = x0.z, w.own[3] = x0.w;
+    w.own[4] = x1.x, w.own[5] = x1.y, w.own[6] = x1.z, w.own[7] = x1.w;
+    w.other[0] = o0.x, w.other[1] = o0.y, w.other[2] = o0.z, w.other[3] = o0.w;
+    w.other[4] = o1.x, w.other[5] = o1.y, w.other[6] = o1.z, w.other[7] = o1.w;
+  } else {
+    unpack8(static_cast<const uint4*>(wp)[at.l], w.own);
+    unpack8(static_cast<const uint4*>(wp)[at.l_other], w.other);
   }
-  return make_uint4(p[0], p[1], p[2], p[3]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w.own[i] = a.offset + w.own[i], w.other[i] = a.offset + w.other[i];
+  if (a.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w.other[i] = w.own[i ^ 1];
+  }
+}
+
+__device__ __forceinline__ int64_t position(const moe_fp4_qk_norm_rope_args& a, int64_t t) {
+  if (!a.rotary) return 0;
+  return a.positions_i64 ? static_cast<const int64_t*>(a.positions)[t] : static_cast<const int32_t*>(a.positions)[t];
+}
+
+__device__ __forceinline__ void load_angles(Angles& g, const moe_fp4_qk_norm_rope_args& a, int64_t pos, const Lane& at) {
+  const float none = pos < 0 || pos >= a.positions_max ? NAN : 1.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    g.c[i] = make_float4(none, none, none, none), g.s[i] = make_float4(none, none, none, none);
+  if (!at.turned || none != 1.f) return;
+  const float* row = a.rotary + pos * a.rot;
+  const float4* c = reinterpret_cast<const float4*>(row + (a.interleaved ? 4 * at.l : at.low ? 8 * at.l : 8 * (at.l - at.half)));
+  const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(c) + a.rot / 2);
+  g.c[0] = c[0], g.s[0] = s[0];
+  if (!a.interleaved) g.c[1] = c[1], g.s[1] = s[1];
+}
+
+// Column i becomes x_i c_i + partner_i s_i, times the norm: cosines, and sines
+// with their signs, for each of the lane's columns.
+__device__ __forceinline__ void spread_angles(float (&c)[8], float (&s)[8], const Angles& g, const Lane& at,
+                                              int interleaved) {
+  if (!at.turned) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+    return;
+  }
+  const float c0[4] = {g.c[0].x, g.c[0].y, g.c[0].z, g.c[0].w}, c1[4] = {g.c[1].x, g.c[1].y, g.c[1].z, g.c[1].w};
+  const float s0[4] = {g.s[0].x, g.s[0].y, g.s[0].z, g.s[0].w}, s1[4] = {g.s[1].x, g.s[1].y, g.s[1].z, g.s[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float ch = i < 4 ? c0[i % 4] : c1[i % 4], sh = i < 4 ? s0[i % 4] : s1[i % 4];
+    c[i] = interleaved ? c0[i / 2] : ch;
+    s[i] = interleaved ? (i % 2 ? s0[i / 2] : -s0[i / 2]) : at.low ? -sh : sh;
+  }
 }
 
 // The rotation's partners of a lane's columns; zeros where nothing is turned.
@@ -116,74 +185,144 @@ __device__ __forceinline__ uint4 partners(uint4 x, int from, bool turned, int in
   return turned ? o : make_uint4(0, 0, 0, 0);
 }
 
-// A lane's eight columns of a head, normed and rotated.  F is float or Pair.
-template <int D, class F>
-__device__ __forceinline__ void norm_rotate(F (&y)[8], const float (&x)[8], const float (&o)[8], bool normed,
-                                            const Factors& f, float eps) {
-  F inv;
-  if (normed) {
-    F sum;
-    set(sum, 0.f);
+// A lane's eight columns of a key, normed and rotated in pairs, as FP32.
+template <int D>
+__device__ __forceinline__ void norm_rotate_pairs(float2 (&y)[4], const moe_fp4_qk_norm_rope_args& a, int64_t t, uint4 raw,
+                                                  uint4 partner, const Lane& at) {
+  Weights w;
+  load_weights(w, a, a.w_k, at);
+  Angles g;
+  load_angles(g, a, position(a, t), at);
+  float c[8], s[8], x[8], o[8];
+  spread_angles(c, s, g, at, a.interleaved);
+  unpack8(raw, x);
+  unpack8(partner, o);
+  Pair inv = {1.f, 0.f};
+  if (a.w_k) {
+    Pair sum = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = sum + product(x[i], x[i], sum);
+    for (int i = 0; i < 8; ++i) sum = sum + two_prod(x[i], x[i]);
 #pragma unroll
     for (int n = D / 16; n > 0; n >>= 1) sum = sum + lane_xor(sum, n);
-    F e;
-    set(e, eps);
-    inv = inverse_root(sum * (1.f / D) + e);
-  } else {
-    set(inv, 1.f);
+    inv = inverse_root(sum * (1.f / D) + Pair{a.eps, 0.f});
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    y[i] = (product(f.c[i], f.w[i], inv) * x[i] + product(f.s[i], f.w_other[i], inv) * o[i]) * inv;
+  for (int i = 0; i < 8; ++i) {
+    const Pair v = (two_prod(c[i], w.own[i]) * x[i] + two_prod(s[i], w.other[i]) * o[i]) * inv;
+    x[i] = __fadd_rn(v.hi, v.lo);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+}
+
+// The same in FP32, two columns at a time, with factors that have the weights.
+template <int D>
+__device__ __forceinline__ void norm_rotate(float2 (&y)[4], uint4 raw, uint4 partner, bool normed, const float2 (&c)[4],
+                                            const float2 (&s)[4], float eps) {
+  float xs[8], os[8];
+  unpack8(raw, xs);
+  unpack8(partner, os);
+  float2 x[4], o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(xs[2 * i], xs[2 * i + 1]), o[i] = make_float2(os[2 * i], os[2 * i + 1]);
+  float inv = 1.f;
+  if (normed) {
+    float2 sum = fmul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sum = ffma2(x[i], x[i], sum);
+    float all = sum.x + sum.y;
+#pragma unroll
+    for (int n = D / 16; n > 0; n >>= 1) all += __shfl_xor_sync(0xffffffffu, all, n);
+    inv = rsqrtf(fmaf(all, 1.f / D, eps));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = fmul2(ffma2(x[i], c[i], fmul2(o[i], s[i])), both(inv));
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3_bits(float v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(r) : "f"(v));
+  return r & 0xffu;
+}
+
+__device__ __forceinline__ uint32_t e2m1_pair(float2 q) {
+  uint16_t b;
+  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u16.u8 %0, t;\n\t}" : "=h"(b) : "f"(q.y), "f"(q.x));
+  return b & 0xffu;
+}
+
+// top / 6, correctly rounded (quotients, fp8_quant.cuh).
+__device__ __forceinline__ float sixth(float top) {
+  const float t = top * (1.f / 6.f);
+  return fmaf(fmaf(t, -6.f, top), 1.f / 6.f, t);
 }
 
 // Eight of a block's sixteen columns (the others in lane ^ 1): their codes,
 // and the block's scale byte.  `bad`: the block has an infinity or a NaN.
-// Quotients are correctly rounded (quotients, fp8_quant.cuh), the scales' too.
-__device__ __forceinline__ uint32_t quantise8(float (&u)[8], float scale, uint32_t& scale_byte, bool& bad) {
-  if (scale != 1.f) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const float v = __fdiv_rn(u[0], scale);  // (around, so that the code is there once)
-#pragma unroll
-      for (int j = 0; j < 7; ++j) u[j] = u[j + 1];
-      u[7] = v;
-    }
-  }
+// kBounded: the columns are off by up to `off`; false where that leaves their
+// codes or scale open.
+struct Quantised {
+  uint32_t codes, scale;
+  bool bad;
+};
+template <bool kBounded>
+__device__ __forceinline__ bool quantise8(const float2 (&u)[4], float off, Quantised& r) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(u[i])));
-  const float other = __shfl_xor_sync(0xffffffffu, top, 1);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(other));
-  bad = !(top < INFINITY);
-  const float t = top * (1.f / 6.f);
-  uint16_t s8;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(s8) : "f"(fmaf(fmaf(t, -6.f, top), 1.f / 6.f, t)));
-  scale_byte = s8 & 0xffu;
-  const float s = e4m3_to_float(scale_byte);
-  const float2 y = both(recip_rn(s)), neg = both(-s);
-  uint32_t codes = 0;
+  for (int i = 0; i < 4; ++i) top = max_nan(max_nan(top, fabsf(u[i].x)), fabsf(u[i].y));
+  top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  r.bad = !(top < INFINITY);
+  r.scale = e4m3_bits(sixth(kBounded ? top + off : top));
+  bool sure = !kBounded || r.scale == e4m3_bits(sixth(top - off));
+  const float s = e4m3_to_float(r.scale), y = recip_rn(s);
+  r.codes = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 q = quotients(make_float2(u[2 * i], u[2 * i + 1]), neg, y);
-    uint16_t b;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u16.u8 %0, t;\n\t}"
-        : "=h"(b)
-        : "f"(q.y), "f"(q.x));
-    codes |= (uint32_t)(b & 0xffu) << (8 * i);
+    if (kBounded) {
+      const float2 q = fmul2(u[i], both(y)), e = both(off * y);
+      const uint32_t up = e2m1_pair(make_float2(q.x + e.x, q.y + e.y)), down = e2m1_pair(make_float2(q.x - e.x, q.y - e.y));
+      sure = sure && up == down;
+      r.codes |= up << (8 * i);
+    } else {
+      r.codes |= e2m1_pair(quotients(u[i], both(-s), both(y))) << (8 * i);
+    }
   }
-  if (bad) scale_byte = 0x7fu;
-  return bad || scale_byte == 0 ? 0 : codes;
+  if (r.bad || r.scale == 0) r.codes = 0;
+  if (r.bad) r.scale = 0x7fu;
+  return sure || r.bad;
 }
 
-// `per`: heads of a warp's task (a multiple of what it has under way at once).
+__device__ __forceinline__ void divide8(float2 (&u)[4], float scale) {
+  if (scale == 1.f) return;
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {  // (around, so that the code is there once)
+    const float2 v = make_float2(__fdiv_rn(u[0].x, scale), __fdiv_rn(u[0].y, scale));
+    u[0] = u[1], u[1] = u[2], u[2] = u[3], u[3] = v;
+  }
+}
+
+// Whether `v` holds on any lane of this lane's head.
 template <int D>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(moe_fp4_qk_norm_rope_args a, int per_q, int q_tasks,
-                                                                    int per_k, int tasks) {
+__device__ __forceinline__ bool head_any(bool v, int side) {
+  constexpr int kLanes = D / 8;
+  const unsigned lanes = __ballot_sync(0xffffffffu, v) >> (side * kLanes);
+  return (kLanes == 32 ? lanes : lanes & ((1u << (kLanes % 32)) - 1)) != 0;
+}
+
+// A warp's task: per_q queries or per_k keys of a token.  Its loads are one
+// iteration ahead.  (Several tokens to a task, with the weights kept, needed
+// more registers than there are: 77 us where this takes 49, @ROPE@.)
+template <int D, int kBlocks = 7>
+__global__ void __launch_bounds__(kRopeThreads, kBlocks) qk_norm_rope_kernel(moe_fp4_qk_norm_rope_args a, int per_q,
+                                                                             int q_tasks, int per_k, int tasks) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;  // heads side by side in a warp
-  const int lane = threadIdx.x & 31, l = lane % kLanes, side = lane / kLanes;
+  const int lane = threadIdx.x & 31, side = lane / kLanes;
   const int64_t task = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) >> 5;
   pdl_wait();
   pdl_launch_dependents();
@@ -193,131 +332,130 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(moe_fp4_qk_n
   const bool is_q = kind_task < q_tasks;
   const int first = is_q ? kind_task * per_q : (kind_task - q_tasks) * per_k;
   const int end = is_q ? min(first + per_q, a.Hq) : min(first + per_k, a.Hkv);
-  const bool store = a.cache && !is_q;
-
-  // weights and angles of this lane's columns
-  Factors f;
-  const int half = a.rot / 16;  // lanes of half the rotated columns
-  const bool turned = a.rotary && 8 * l < a.rot, low = l < half;
-  const int l_other = turned && !a.interleaved ? (low ? l + half : l - half) : l;
-  const int from = lane - l + l_other;
+  const Lane at = lane_of<D>(a, lane);
   const void* wp = is_q ? a.w_q : a.w_k;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f.c[i] = 1.f, f.s[i] = 0.f, f.w[i] = 1.f, f.w_other[i] = 1.f;
-  if (wp) {
-    if (a.weights_f32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(wp));
-      const float4 x0 = p[2 * l], x1 = p[2 * l + 1], o0 = p[2 * l_other], o1 = p[2 * l_other + 1];
-      f.w[0] = x0.x, f.w[1] = x0.y, f.w[2] = x0.z, f.w[3] = x0.w;
-      f.w[4] = x1.x, f.w[5] = x1.y, f.w[6] = x1.z, f.w[7] = x1.w;
-      f.w_other[0] = o0.x, f.w_other[1] = o0.y, f.w_other[2] = o0.z, f.w_other[3] = o0.w;
-      f.w_other[4] = o1.x, f.w_other[5] = o1.y, f.w_other[6] = o1.z, f.w_other[7] = o1.w;
-    } else {
-      unpack8(static_cast<const uint4*>(wp)[l], f.w);
-      unpack8(static_cast<const uint4*>(wp)[l_other], f.w_other);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f.w[i] = a.offset + f.w[i], f.w_other[i] = a.offset + f.w_other[i];
-    if (a.interleaved) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f.w_other[i] = f.w[i ^ 1];
-    }
-  }
-  if (turned) {
-    const int64_t pos = a.positions_i64 ? static_cast<const int64_t*>(a.positions)[t]
-                                        : static_cast<const int32_t*>(a.positions)[t];
-    if (pos < 0 || pos >= a.positions_max) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f.c[i] = f.s[i] = NAN;
-    } else {
-      const float* row = a.rotary + pos * a.rot;
-      const float4* c = reinterpret_cast<const float4*>(row + (a.interleaved ? 4 * l : low ? 8 * l : 8 * (l - half)));
-      const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(c) + a.rot / 2);
-      const float4 c0 = c[0], s0 = s[0];
-      if (a.interleaved) {
-        f.c[0] = f.c[1] = c0.x, f.c[2] = f.c[3] = c0.y, f.c[4] = f.c[5] = c0.z, f.c[6] = f.c[7] = c0.w;
-        f.s[1] = s0.x, f.s[3] = s0.y, f.s[5] = s0.z, f.s[7] = s0.w;
-        f.s[0] = -s0.x, f.s[2] = -s0.y, f.s[4] = -s0.z, f.s[6] = -s0.w;
-      } else {
-        const float4 c1 = c[1], s1 = s[1];
-        f.c[0] = c0.x, f.c[1] = c0.y, f.c[2] = c0.z, f.c[3] = c0.w;
-        f.c[4] = c1.x, f.c[5] = c1.y, f.c[6] = c1.z, f.c[7] = c1.w;
-        f.s[0] = s0.x, f.s[1] = s0.y, f.s[2] = s0.z, f.s[3] = s0.w;
-        f.s[4] = s1.x, f.s[5] = s1.y, f.s[6] = s1.z, f.s[7] = s1.w;
-        if (low) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f.s[i] = -f.s[i];
-        }
-      }
-    }
-  }
-
+  const bool normed = wp != nullptr;
   const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(is_q ? a.q_in : a.k_in) +
-                            t * (is_q ? a.q_row : a.k_row) + 8 * l;
+                            t * (is_q ? a.q_row : a.k_row) + 8 * at.l;
   const int64_t step = is_q ? a.q_head : a.k_head;
-  if (!store) {
+  Weights w;
+  Angles g;
+  load_angles(g, a, position(a, t), at);
+  load_weights(w, a, wp, at);
+  float2 c[4], s[4];  // factors of the columns and of their partners, the weights among them
+  auto factors = [&]() {
+    float cc[8], ss[8];
+    spread_angles(cc, ss, g, at, a.interleaved);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      f.c[i] *= f.w[i], f.s[i] *= f.w_other[i];
-      f.w[i] = f.w_other[i] = 1.f;
+    for (int i = 0; i < 4; ++i) {
+      c[i] = make_float2(cc[2 * i] * w.own[2 * i], cc[2 * i + 1] * w.own[2 * i + 1]);
+      s[i] = make_float2(ss[2 * i] * w.other[2 * i], ss[2 * i + 1] * w.other[2 * i + 1]);
     }
+  };
+  if (is_q || !a.cache) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_q ? a.q_out : a.k_out) +
-                         t * (is_q ? a.q_out_row : a.k_out_row) + 8 * l;
+                         t * (is_q ? a.q_out_row : a.k_out_row) + 8 * at.l;
     const int64_t out_step = is_q ? a.q_out_head : a.k_out_head;
-#pragma unroll 1
-    for (int base = first; base < end; base += kUnroll * kHeads) {
-      uint4 raw[kUnroll];
+    uint4 raw[kUnroll];
+    auto load = [&](int base) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int h = base + u * kHeads + side;
         raw[u] = h < end ? *reinterpret_cast<const uint4*>(in + h * step) : make_uint4(0, 0, 0, 0);
       }
+    };
+    load(first);
+    factors();
+#pragma unroll 1
+    for (int base = first; base < end; base += kUnroll * kHeads) {
+      uint4 now[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) now[u] = raw[u];
+      load(base + kUnroll * kHeads);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         if (base + u * kHeads >= end) break;  // (the same for the whole warp)
-        float x[8], o[8], y[8];
-        unpack8(raw[u], x);
-        unpack8(partners(raw[u], from, turned, a.interleaved), o);
-        norm_rotate<D>(y, x, o, wp != nullptr, f, a.eps);
+        float2 y[4];
+        norm_rotate<D>(y, now[u], partners(now[u], at.from, at.turned, a.interleaved), normed, c, s, a.eps);
         const int h = base + u * kHeads + side;
-        if (h < end) *reinterpret_cast<uint4*>(out + h * out_step) = pack8(y);
+        if (h < end)
+          *reinterpret_cast<uint4*>(out + h * out_step) = make_uint4(pack2(y[0]), pack2(y[1]), pack2(y[2]), pack2(y[3]));
       }
     }
     return;
   }
 
+  const __nv_bfloat16* vin = static_cast<const __nv_bfloat16*>(a.v_in) + t * a.v_row + 8 * at.l;
+  const int64_t head_bytes = (int64_t)(a.page_size / kCacheBlock) * cache_block_bytes(D);
+  uint4 next_raw, next_vals;
+  auto load = [&](int h) {
+    next_raw = h < end ? *reinterpret_cast<const uint4*>(in + h * step) : make_uint4(0, 0, 0, 0);
+    next_vals = h < end ? *reinterpret_cast<const uint4*>(vin + h * a.v_head) : make_uint4(0, 0, 0, 0);
+  };
+  load(first + side);
+  factors();
   const int64_t slot = a.slots[t];
+  // What FP32 may be off by: with |x| <= sqrt(D) after the norm, half of 13
+  // additions' and the root's three units, four products and a division,
+  // below 2^-20 of sqrt(D) (|c w| + |s w'|); twice that, for the slack between.
+  float off = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    off = fmaxf(off, fmaxf(fabsf(c[j].x) + fabsf(s[j].x), fabsf(c[j].y) + fabsf(s[j].y)));
+  off = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, 1));
+  off *= 0x1p-19f * (D == 64 ? 8.f : D == 128 ? 11.4f : 16.f) / a.k_scale;
   const bool kept = slot >= 0 && slot < (int64_t)a.pages * a.page_size;
-  const __nv_bfloat16* vin = static_cast<const __nv_bfloat16*>(a.v_in) + t * a.v_row + 8 * l;
+  const CachePlace place = cache_place(kept ? slot : 0, 0, a.Hkv, a.page_size, D);
+  uint8_t* codes = static_cast<uint8_t*>(a.cache) + place.codes + 4 * at.l;
+  uint8_t* scales = static_cast<uint8_t*>(a.cache) + place.scales + at.l / 2;
+  unsigned again = 0;  // iterations whose keys' codes are open
 #pragma unroll 1
   for (int base = first; base < end; base += kHeads) {
     const int h = base + side;
+    const uint4 raw = next_raw, vals = next_vals;
+    load(h + kHeads);
+    const uint4 other = partners(raw, at.from, at.turned, a.interleaved);
+    Quantised k, v;
+    float2 u[4];
+    norm_rotate<D>(u, raw, other, normed, c, s, a.eps);
+    divide8(u, a.k_scale);
+    const bool sure = quantise8<true>(u, off, k) && normed;
+    again |= (__any_sync(0xffffffffu, !sure) ? 1u : 0u) << ((base - first) / kHeads);
+    float x[8];
+    unpack8(vals, x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = make_float2(x[2 * j], x[2 * j + 1]);
+    divide8(u, a.v_scale);
+    quantise8<false>(u, 0.f, v);
+    if (head_any<D>(k.bad || v.bad, side)) k.scale = 0x7fu;
+    if (h < end && kept) {
+      const int64_t head = h * head_bytes;
+      *reinterpret_cast<uint32_t*>(codes + head) = k.codes;
+      *reinterpret_cast<uint32_t*>(codes + head + cache_half_bytes(D)) = v.codes;
+      if (at.l % 2 == 0) {
+        scales[head] = (uint8_t)k.scale;
+        scales[head + cache_half_bytes(D)] = (uint8_t)v.scale;
+      }
+    }
+  }
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int h = first + (__ffs(again) - 1) * kHeads + side;
     const uint4 raw = h < end ? *reinterpret_cast<const uint4*>(in + h * step) : make_uint4(0, 0, 0, 0);
     const uint4 vals = h < end ? *reinterpret_cast<const uint4*>(vin + h * a.v_head) : make_uint4(0, 0, 0, 0);
-    float x[8], o[8], u[8];
-    Pair p[8];
-    unpack8(raw, x);
-    unpack8(partners(raw, from, turned, a.interleaved), o);
-    norm_rotate<D>(p, x, o, wp != nullptr, f, a.eps);
+    Quantised k;
+    float2 u[4];
+    norm_rotate_pairs<D>(u, a, t, raw, partners(raw, at.from, at.turned, a.interleaved), at);
+    divide8(u, a.k_scale);
+    quantise8<false>(u, 0.f, k);
+    float x[8], top = 0.f;
+    unpack8(vals, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = value(p[i]);
-    uint32_t k_scale, v_scale;
-    bool k_bad, v_bad;
-    const uint32_t k_codes = quantise8(u, a.k_scale, k_scale, k_bad);
-    unpack8(vals, u);
-    const uint32_t v_codes = quantise8(u, a.v_scale, v_scale, v_bad);
-    const unsigned bad = __ballot_sync(0xffffffffu, k_bad || v_bad) >> (side * kLanes);
-    if ((kLanes == 32 ? bad : bad & ((1u << (kLanes % 32)) - 1)) != 0) k_scale = 0x7fu;
+    for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(__fdiv_rn(x[i], a.v_scale)));
+    if (head_any<D>(k.bad || !(top < INFINITY), side)) k.scale = 0x7fu;
     if (h < end && kept) {
-      const CachePlace at = cache_place(slot, h, a.Hkv, a.page_size, D);
-      uint8_t* k = static_cast<uint8_t*>(a.cache);
-      uint8_t* v = k + cache_half_bytes(D);
-      *reinterpret_cast<uint32_t*>(k + at.codes + 4 * l) = k_codes;
-      *reinterpret_cast<uint32_t*>(v + at.codes + 4 * l) = v_codes;
-      if (l % 2 == 0) {
-        k[at.scales + l / 2] = (uint8_t)k_scale;
-        v[at.scales + l / 2] = (uint8_t)v_scale;
-      }
+      *reinterpret_cast<uint32_t*>(codes + h * head_bytes) = k.codes;
+      if (at.l % 2 == 0) scales[h * head_bytes] = (uint8_t)k.scale;
     }
   }
 }
@@ -328,13 +466,14 @@ cudaError_t launch_dim(const moe_fp4_qk_norm_rope_args& a, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = current_device_sms(&sms);
   if (e != cudaSuccess) return e;
-  // few tokens: a task of what a warp has under way; many: all of a token's
-  // queries, so that its weights and angles are read once
+  // few tokens: a task of what a warp has under way; many: all heads of a kind,
+  // so that weights and angles are read once
   const bool many = a.T >= 16 * sms;
   const int per_q = many ? ceil_div(a.Hq, kAtOnce) * kAtOnce : kAtOnce;
-  const int per_k = !a.cache ? per_q : many ? 4 * kHeads : kHeads;
+  const int per_k = !a.cache ? per_q : many ? min(ceil_div(a.Hkv, kHeads), 32) * kHeads : kHeads;
   const int q_tasks = ceil_div(a.Hq, per_q), tasks = q_tasks + ceil_div(a.Hkv, per_k);
-  const int64_t grid = ((int64_t)a.T * tasks + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  const int64_t warps = (int64_t)a.T * tasks;
+  const int64_t grid = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch_dependent(qk_norm_rope_kernel<D>, (unsigned)grid, kRopeThreads, st, a, per_q, q_tasks, per_k, tasks);
 }

@@ -15,13 +15,13 @@ stream (or ``stream``).
 """
 from __future__ import annotations
 
-import math
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
 from . import _capi
-from .ops import _BF16, _F32, _INT_MAX, _device, _empty, _fail, _float_type, _on, _raw_stream, _vector
+from .ops import _BF16, _F32, _INT_MAX, _current_device, _device, _empty, _fail, _float_type, _on, _raw_stream, _vector
 
 _I32, _I64, _U8, _BOOL = torch.int32, torch.int64, torch.uint8, torch.bool
 _PACK_STEP = _capi.MoeFp4CacheStepArgs.PACK.pack
@@ -40,6 +40,9 @@ class CacheStep(NamedTuple):
     accepted: torch.Tensor    # int32 [R]: new tokens, or 0 where the request was refused
 
 
+# Each call costs the host more than a small kernel costs the GPU: the
+# functions below look at the usual arguments in one test, and leave all others
+# to these, which find and name what is wrong.
 def _heads(t: torch.Tensor, name: str, dev: int, rows=None, heads=None, dim=None):
     """Check a bfloat16 [tokens, heads, D] tensor with contiguous columns;
     returns its strides per token and per head."""
@@ -91,6 +94,24 @@ def _tables(t: torch.Tensor, dev: int, R: int):
     return t.data_ptr(), (t.stride(0) if R != 1 else t.shape[1]), t.shape[1]
 
 
+def _step_arguments(lengths, new_tokens, tables, free_pages, free_count, tokens):
+    """(table width, its row stride) of cache_step's arguments, checked one by one."""
+    dev = _device(lengths)
+    if lengths.dim() != 1 or lengths.shape[0] > _INT_MAX:
+        raise ValueError(f"lengths must be a vector, not {list(lengths.shape)}")
+    if not 0 <= tokens <= _INT_MAX:
+        raise ValueError(f"tokens must be in [0, 2^31), not {tokens}")
+    R = lengths.shape[0]
+    _vector(lengths, "lengths", _I32, dev, R)
+    _vector(new_tokens, "new_tokens", _I32, dev, R)
+    _, row, width = _tables(tables, dev, R)
+    if free_pages.dim() != 1 or free_pages.shape[0] > _INT_MAX:
+        raise ValueError(f"free_pages must be a vector, not {list(free_pages.shape)}")
+    _vector(free_pages, "free_pages", _I32, dev, free_pages.shape[0])
+    _vector(free_count, "free_count", _I32, dev, 1)
+    return width, row
+
+
 def alloc_fp4_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
     """A zeroed cache: uint8 ``[pages, kv_heads, page_size // 16, 2, 9 *
     head_dim]``.  Of each 16 tokens of a head first the keys, then the values,
@@ -134,36 +155,39 @@ def cache_step(lengths: torch.Tensor, new_tokens: torch.Tensor, tables: torch.Te
         with _on(stream, lengths):
             return cache_step(lengths, new_tokens, tables, free_pages, free_count, page_size, tokens, finished,
                               lengths_out, free_count_out)
-    dev = _device(lengths)
-    if lengths.dim() != 1 or lengths.shape[0] > _INT_MAX:
-        raise ValueError(f"lengths must be a vector, not {list(lengths.shape)}")
-    if not 0 <= tokens <= _INT_MAX:
-        raise ValueError(f"tokens must be in [0, 2^31), not {tokens}")
-    R, device = lengths.shape[0], lengths.device
-    p_len = _int_vector(lengths, "lengths", _I32, dev, R)
-    p_new = _int_vector(new_tokens, "new_tokens", _I32, dev, R)
-    p_tab, tab_row, width = _tables(tables, dev, R)
-    if free_pages.dim() != 1 or free_pages.shape[0] > _INT_MAX:
-        raise ValueError(f"free_pages must be a vector, not {list(free_pages.shape)}")
-    p_free = _int_vector(free_pages, "free_pages", _I32, dev, free_pages.shape[0])
-    p_count = _int_vector(free_count, "free_count", _I32, dev, 1)
+    dev, device = lengths.get_device(), lengths.device
+    shape, tab_shape, free_shape = lengths.shape, tables.shape, free_pages.shape
+    R = shape[0] if shape else -1
+    if (dev >= 0 and dev == _current_device() and len(shape) == 1 and len(tab_shape) == 2 and tab_shape[0] == R
+            and len(free_shape) == 1 and lengths.dtype is new_tokens.dtype is tables.dtype is free_pages.dtype
+            is free_count.dtype is _I32 and new_tokens.shape == shape and free_count.shape == (1,)
+            and new_tokens.get_device() == tables.get_device() == free_pages.get_device() == free_count.get_device() == dev
+            and lengths.is_contiguous() and new_tokens.is_contiguous() and tables.is_contiguous()
+            and free_pages.is_contiguous() and R <= _INT_MAX and tab_shape[1] <= _INT_MAX and free_shape[0] <= _INT_MAX
+            and 0 <= tokens <= _INT_MAX):
+        width = tab_row = tab_shape[1]
+    else:
+        width, tab_row = _step_arguments(lengths, new_tokens, tables, free_pages, free_count, tokens)
     p_fin = 0
     if finished is not None:
         _vector(finished, "finished", _U8 if finished.dtype is _U8 else _BOOL, dev, R)
         p_fin = finished.data_ptr()
     if lengths_out is None:
         lengths_out = _empty(R, dtype=_I32, device=device)
+    else:
+        _vector(lengths_out, "lengths_out", _I32, dev, R)
     if free_count_out is None:
         free_count_out = _empty(1, dtype=_I32, device=device)
-    p_len_out = _int_vector(lengths_out, "lengths_out", _I32, dev, R)
-    p_count_out = _int_vector(free_count_out, "free_count_out", _I32, dev, 1)
+    else:
+        _vector(free_count_out, "free_count_out", _I32, dev, 1)
     offsets = _empty(R + 1, dtype=_I32, device=device)
     positions = _empty(tokens, dtype=_I32, device=device)
     slots = _empty(tokens, dtype=_I64, device=device)
     accepted = _empty(R, dtype=_I32, device=device)
     st = _capi.lib().moe_fp4_cache_step(
-        _PACK_STEP(p_len, p_new, p_fin, p_tab, tab_row, p_free, p_count, offsets.data_ptr(), positions.data_ptr(),
-                   slots.data_ptr(), p_len_out, p_count_out, accepted.data_ptr(), width, free_pages.shape[0],
+        _PACK_STEP(lengths.data_ptr(), new_tokens.data_ptr(), p_fin, tables.data_ptr(), tab_row, free_pages.data_ptr(),
+                   free_count.data_ptr(), offsets.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                   lengths_out.data_ptr(), free_count_out.data_ptr(), accepted.data_ptr(), width, free_shape[0],
                    page_size, R, tokens), _raw_stream(dev))
     if st:
         _fail("moe_fp4_cache_step", st)
@@ -178,9 +202,10 @@ def fp4_cache_read(cache: torch.Tensor, slots: torch.Tensor, k_scale: float = 1.
             return fp4_cache_read(cache, slots, k_scale, v_scale)
     dev = _device(cache)
     pages, heads, page_size, D = _cache_sizes(cache, dev)
-    if slots.dim() != 1 or slots.shape[0] > _INT_MAX:
-        raise ValueError(f"slots must be a vector, not {list(slots.shape)}")
-    T = slots.shape[0]
+    shape = slots.shape
+    if len(shape) != 1 or shape[0] > _INT_MAX:
+        raise ValueError(f"slots must be a vector, not {list(shape)}")
+    T = shape[0]
     p_slots = _int_vector(slots, "slots", _I64, dev, T)
     k = _empty((T, heads, D), dtype=_BF16, device=cache.device)
     v = _empty((T, heads, D), dtype=_BF16, device=cache.device)
@@ -218,28 +243,42 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
             return qk_norm_rope(q, k, positions, rotary, q_weight, k_weight, eps, weight_offset, interleaved, v, cache,
                                 slots, k_scale, v_scale)
     dev = _device(q)
-    q_row, q_head = _heads(q, "q", dev)
-    T, Hq, D = q.shape
-    if k.dim() != 3:
-        raise ValueError(f"k must be [{T}, heads, {D}], not {list(k.shape)}")
-    Hkv = k.shape[1]
-    k_row, k_head = _heads(k, "k", dev, T, Hkv, D)
-    if T > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX:
-        raise ValueError(f"q and k must have fewer than 2^31 tokens, heads and columns, not {list(q.shape)}")
+    shape, k_shape = q.shape, k.shape
+    if (len(shape) == 3 and len(k_shape) == 3 and q.dtype is k.dtype is _BF16 and k.get_device() == dev
+            and shape[0] == k_shape[0] and shape[2] == k_shape[2] and q.stride(2) == 1 and k.stride(2) == 1
+            and shape[0] <= _INT_MAX and shape[1] <= _INT_MAX and k_shape[1] <= _INT_MAX and shape[2] <= _INT_MAX):
+        T, Hq, D = shape
+        Hkv = k_shape[1]
+        q_row, q_head, _ = q.stride()
+        k_row, k_head, _ = k.stride()
+        if T == 1:  # (has no stride of its own)
+            q_row = k_row = 0
+        if Hq == 1:
+            q_head = 0
+        if Hkv == 1:
+            k_head = 0
+    else:
+        q_row, q_head = _heads(q, "q", dev)
+        T, Hq, D = shape
+        if len(k_shape) != 3:
+            raise ValueError(f"k must be [{T}, heads, {D}], not {list(k_shape)}")
+        Hkv = k_shape[1]
+        k_row, k_head = _heads(k, "k", dev, T, Hkv, D)
+        if T > _INT_MAX or Hq > _INT_MAX or Hkv > _INT_MAX or D > _INT_MAX:
+            raise ValueError(f"q and k must have fewer than 2^31 tokens, heads and columns, not {list(shape)}")
     p_v = v_row = v_head = p_rot = p_pos = p_cache = p_slots = p_k = w_f32 = 0
     pos64 = places = rot = pages = page_size = 0
     p_wq = p_wk = 0
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            dtype = _float_type(w, name)
-            if name == "k_weight" and q_weight is not None and dtype is not q_weight.dtype:
-                raise TypeError(f"k_weight must be {q_weight.dtype}, as q_weight, not {dtype}")
-            _vector(w, name, dtype, dev, D)
-            w_f32 = 1 if dtype is _F32 else 0
     if q_weight is not None:
-        p_wq = q_weight.data_ptr()
+        dtype = _float_type(q_weight, "q_weight")
+        _vector(q_weight, "q_weight", dtype, dev, D)
+        p_wq, w_f32 = q_weight.data_ptr(), 1 if dtype is _F32 else 0
     if k_weight is not None:
-        p_wk = k_weight.data_ptr()
+        dtype = _float_type(k_weight, "k_weight")
+        if q_weight is not None and dtype is not q_weight.dtype:
+            raise TypeError(f"k_weight must be {q_weight.dtype}, as q_weight, not {dtype}")
+        _vector(k_weight, "k_weight", dtype, dev, D)
+        p_wk, w_f32 = k_weight.data_ptr(), 1 if dtype is _F32 else 0
     if rotary is not None:
         if positions is None:
             raise ValueError("rotary needs positions")
@@ -292,6 +331,32 @@ def alloc_fp4_attention_workspace(R_max: int, heads: int, kv_heads: int, head_di
     return torch.empty(n, dtype=_U8, device=device or torch.device("cuda"))
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(R: int, heads: int, kv_heads: int, D: int, dev: int) -> int:
+    return _capi.moe_fp4_attention_workspace_bytes(R, heads, kv_heads, D)
+
+
+def _attention_arguments(q, cache, tables, lengths, offsets, window):
+    """Sizes and strides of fp4_attention's arguments, checked one by one."""
+    dev = _device(q)
+    q_row, q_head = _heads(q, "q", dev)
+    T, Hq, D = q.shape
+    if T > _INT_MAX or Hq > _INT_MAX:
+        raise ValueError(f"q must have fewer than 2^31 tokens and heads, not {list(q.shape)}")
+    pages, Hkv, page_size, width = _cache_sizes(cache, dev)
+    if width != D:
+        raise ValueError(f"the cache has heads of {width} columns, q of {D}")
+    if lengths.dim() != 1 or lengths.shape[0] >= _INT_MAX:
+        raise ValueError(f"lengths must be a vector, not {list(lengths.shape)}")
+    R = lengths.shape[0]
+    _vector(lengths, "lengths", _I32, dev, R)
+    _vector(offsets, "offsets", _I32, dev, R + 1)
+    _, tab_row, tab_width = _tables(tables, dev, R)
+    if not 0 <= window <= _INT_MAX:
+        raise ValueError(f"window must be in [0, 2^31), not {window}")
+    return T, Hq, D, q_row, q_head, pages, Hkv, page_size, R, tab_width, tab_row
+
+
 def fp4_attention(q: torch.Tensor, cache: torch.Tensor, tables: torch.Tensor, lengths: torch.Tensor,
                   offsets: torch.Tensor, scale: Optional[float] = None, window: int = 0,
                   sinks: Optional[torch.Tensor] = None, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -318,43 +383,45 @@ def fp4_attention(q: torch.Tensor, cache: torch.Tensor, tables: torch.Tensor, le
         with _on(stream, q):
             return fp4_attention(q, cache, tables, lengths, offsets, scale, window, sinks, k_scale, v_scale, out,
                                  return_lse, workspace)
-    dev = _device(q)
-    q_row, q_head = _heads(q, "q", dev)
-    T, Hq, D = q.shape
-    if T > _INT_MAX or Hq > _INT_MAX:
-        raise ValueError(f"q must have fewer than 2^31 tokens and heads, not {list(q.shape)}")
-    pages, Hkv, page_size, width = _cache_sizes(cache, dev)
-    if width != D:
-        raise ValueError(f"the cache has heads of {width} columns, q of {D}")
-    if lengths.dim() != 1 or lengths.shape[0] > _INT_MAX:
-        raise ValueError(f"lengths must be a vector, not {list(lengths.shape)}")
-    R = lengths.shape[0]
-    p_len = _int_vector(lengths, "lengths", _I32, dev, R)
-    p_off = _int_vector(offsets, "offsets", _I32, dev, R + 1)
-    p_tab, tab_row, tab_width = _tables(tables, dev, R)
-    if not 0 <= window <= _INT_MAX:
-        raise ValueError(f"window must be in [0, 2^31), not {window}")
+    dev, device = q.get_device(), q.device
+    shape, c_shape, tab_shape = q.shape, cache.shape, tables.shape
+    if (dev >= 0 and dev == _current_device() and len(shape) == 3 and len(c_shape) == 5 and len(tab_shape) == 2
+            and q.dtype is _BF16 and cache.dtype is _U8 and tables.dtype is lengths.dtype is offsets.dtype is _I32
+            and cache.get_device() == tables.get_device() == lengths.get_device() == offsets.get_device() == dev
+            and c_shape[3] == 2 and c_shape[4] == 9 * shape[2] and lengths.shape == (tab_shape[0],)
+            and offsets.shape == (tab_shape[0] + 1,) and q.is_contiguous() and cache.is_contiguous()
+            and tables.is_contiguous() and lengths.is_contiguous() and offsets.is_contiguous()
+            and shape[0] <= _INT_MAX and shape[1] <= _INT_MAX and c_shape[0] <= _INT_MAX and tab_shape[0] < _INT_MAX
+            and tab_shape[1] <= _INT_MAX and 0 <= window <= _INT_MAX):
+        T, Hq, D = shape
+        q_row, q_head = Hq * D, D
+        pages, Hkv, page_size = c_shape[0], c_shape[1], c_shape[2] * CACHE_BLOCK
+        R, tab_width = tab_shape
+        tab_row = tab_width
+    else:
+        T, Hq, D, q_row, q_head, pages, Hkv, page_size, R, tab_width, tab_row = _attention_arguments(
+            q, cache, tables, lengths, offsets, window)
     p_sinks = p_lse = 0
     if sinks is not None:
         _vector(sinks, "sinks", _F32, dev, Hq)
         p_sinks = sinks.data_ptr()
     if out is None:
-        out = _empty((T, Hq, D), dtype=_BF16, device=q.device)
+        out = _empty(shape, dtype=_BF16, device=device)
         out_row, out_head = Hq * D, D
     else:
         out_row, out_head = _heads(out, "out", dev, T, Hq, D)
     lse = None
     if return_lse:
-        lse = _empty((T, Hq), dtype=_F32, device=q.device)
+        lse = _empty((T, Hq), dtype=_F32, device=device)
         p_lse = lse.data_ptr()
     if workspace is None:
-        workspace = _empty(_capi.moe_fp4_attention_workspace_bytes(R, Hq, Hkv, D), dtype=_U8, device=q.device)
-    elif workspace.device != q.device or not workspace.is_contiguous():
+        workspace = _empty(_workspace_bytes(R, Hq, Hkv, D, dev), dtype=_U8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on q's device")
     st = _capi.lib().moe_fp4_attention(
-        _PACK_ATTENTION(q.data_ptr(), q_row, q_head, cache.data_ptr(), p_tab, tab_row, p_len, p_off, p_sinks,
-                        out.data_ptr(), out_row, out_head, p_lse, workspace.data_ptr(), workspace.nbytes,
-                        1.0 / math.sqrt(D) if scale is None else scale, k_scale, v_scale, window, T, R, Hq, Hkv, D,
+        _PACK_ATTENTION(q.data_ptr(), q_row, q_head, cache.data_ptr(), tables.data_ptr(), tab_row, lengths.data_ptr(),
+                        offsets.data_ptr(), p_sinks, out.data_ptr(), out_row, out_head, p_lse, workspace.data_ptr(),
+                        workspace.nbytes, D ** -0.5 if scale is None else scale, k_scale, v_scale, window, T, R, Hq, Hkv, D,
                         pages, page_size, tab_width), _raw_stream(dev))
     if st:
         _fail("moe_fp4_attention", st)

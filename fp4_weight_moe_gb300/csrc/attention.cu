@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   pdl_wait();
   pdl_launch_dependents();
 
-  AttnCursor<kRows, kPair> c;
+  AttnCursor<kRows, kPair, 16> c;
   int64_t u, u_end;
   int team;
   if (!attn_stretch<kRows, kPair, kThreads, kWarps, kTeamSpan>(p, c, u, u_end, team)) return;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     const AttnRequest q = c.q;
     const AttnSpan span = c.span;
     const int r = c.r, tile = c.tile, head = c.head, from = c.from;
-    const int to = (int)min((int64_t)span.units, from + u_end - u);
+    const int to = from + attn_take(c, u_end - u);
     u += to - from;
 
     // this warp's pairs of blocks: first, first + team, ...; their copies

@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
   pdl_launch_dependents();
   // each warp's place in its CTA's stretch (in shared memory: its registers
   // are worth more to the loops between items)
-  __shared__ AttnCursor<C::kRows, kTok> cursors[C::kThreads / 32];
-  AttnCursor<C::kRows, kTok>& c = cursors[warp];
+  __shared__ AttnCursor<C::kRows, kTok, 2> cursors[C::kThreads / 32];
+  AttnCursor<C::kRows, kTok, 2>& c = cursors[warp];
   int left;  // units of the stretch that are left
   {
     int64_t u, u_end;
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
       uint32_t half = 0;
       bool ok = true;
       while (ok && left > 0) {
-        const int steps = min(c.span.units - c.from, left);
+        const int steps = attn_take(c, left);
         const int end_block = (c.span.hi + kCacheBlock - 1) / kCacheBlock;
         const int32_t* table = p.a.tables + (int64_t)c.r * p.a.table_row;
         int b = (c.span.first + c.from) * C::kBlocks + lane;
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
       };
       uint32_t p_seen[2] = {0, 0};
       while (ok && left > 0) {
-        const int steps = min(c.span.units - c.from, left);
+        const int steps = attn_take(c, left);
         if constexpr (kTiles == 2) {
           ok = wait(&kv_full[step & 1], step >> 1);
           for (int n = 0; ok && n < 2; ++n) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
     uint32_t half = 0;
     bool ok = true;
     while (ok && left > 0) {
-      const int steps = min(c.span.units - c.from, left);
+      const int steps = attn_take(c, left);
       for (int i = 0; ok && i < 2 * steps; ++i, ++half) {
         const uint32_t s = half % C::kRaw, step = half >> 1, kind = half & 1, buf = 2 * kind + (step & 1), round = step >> 1;
         ok = wait(&raw_full[s], half / C::kRaw);
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
     uint32_t item = 0;
     bool ok = true;
     while (ok && left > 0) {
-      const int steps = min(c.span.units - c.from, left);
+      const int steps = attn_take(c, left);
       float fac;
       const AttnRows tile_rows = attn_rows(p, c.tile * C::kRows);
       {

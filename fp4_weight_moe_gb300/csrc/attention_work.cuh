@@ -12,7 +12,8 @@
 // two places in the workspace and are joined in the order of the workers.
 //
 // A worker is a CTA, or each of its warps (kTeams, where the items are short:
-// a CTA's warps would wait for each other at every item).
+// a CTA's warps would wait for each other at every item).  Items of at most
+// kWhole units are not shared: they are their first unit's worker's.
 #pragma once
 
 #include "attention.cuh"
@@ -109,8 +110,9 @@ __device__ __forceinline__ int64_t attn_quotient(int64_t a, int64_t b) {
 
 // A place in the line: an item, and the unit of it.  The lanes of a warp keep
 // one together.
-template <int kRows, int kUnit>
+template <int kRows, int kUnit_, int kWhole_>
 struct AttnCursor {
+  static constexpr int kUnit = kUnit_, kWhole = kWhole_;
   AttnRequest q;
   AttnSpan span;
   int r, tiles, tile, head, from;
@@ -185,29 +187,6 @@ __device__ __forceinline__ int attn_owner(const AttnLine& line, int64_t u) {
                         : line.more + (int)attn_quotient(grain - longer, line.each);
 }
 
-// Sum over the block's threads of v before this thread's, and all of it.
-template <int kThreads>
-__device__ __forceinline__ int64_t block_before(int64_t v, int64_t* total, int64_t* shared) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t upto = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  __syncthreads();
-  if (lane == 31) shared[warp] = upto;
-  __syncthreads();
-  int64_t before = upto - v, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += shared[w];
-    all += shared[w];
-  }
-  *total = all;
-  return before;
-}
-
 // Zeros for rows from, from + step, ... < to of q, by a warp: they see no key
 // (`real`: of a request), or lie behind the last sequence.
 __device__ __forceinline__ void attn_no_keys(const AttnArgs& p, int64_t from, int64_t to, int64_t step, bool real) {
@@ -238,27 +217,47 @@ __device__ __forceinline__ AttnBlind attn_blind(const AttnArgs& p, const AttnReq
 // it, or each of its warps' own (then `team` is 1; CTA 0 writes the line
 // down); false where it has none.  Items that average fewer units than
 // kTeamSpan go to warps (kTeams warps of a CTA can be workers).
-template <int kRows, int kUnit, int kThreads, int kTeams, int kTeamSpan>
-__device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows, kUnit>& cursor, int64_t& u,
+template <int kRows, int kUnit, int kThreads, int kTeams, int kTeamSpan, int kWhole>
+__device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows, kUnit, kWhole>& cursor, int64_t& u,
                                              int64_t& u_end, int& team) {
-  __shared__ int64_t shared[2][kThreads / 32];
-  __shared__ int64_t found_rest[kTeams];
-  __shared__ int found[kTeams];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int64_t warp_units[kWarps], found_rest[kTeams];
+  __shared__ int warp_items[kWarps], found[kTeams];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int each = ceil_div(max(p.a.R, 1), kThreads);
   const int r0 = min((int)threadIdx.x * each, p.a.R), r1 = min(r0 + each, p.a.R);
-  int64_t mine = 0, items = 0, all_items;
+  const int start = p.a.R > 0 ? min(max(p.a.offsets[0], 0), p.a.T) : 0;
+  const int end = p.a.R > 0 ? min(max(p.a.offsets[p.a.R], 0), p.a.T) : 0;
+  int64_t mine = 0;
+  int items = 0;
   bool blind = false;  // a request of this thread's has queries that see no key
   for (int r = r0; r < r1; ++r) {
     const AttnRequest q = attn_request(p, r);
-    mine += attn_units<kRows, kUnit>(p, r);
-    if (kTeams > 1) items += (int64_t)attn_tiles<kRows>(p, q) * p.a.Hkv;
+    const int tiles = attn_tiles<kRows>(p, q);
+    items += tiles * p.a.Hkv;
+    int64_t sum = 0;
+    for (int i = 0; i < tiles; ++i) sum += attn_span<kUnit>(p, q, i * kRows, kRows).units;
+    mine += sum * p.a.Hkv;
     const AttnBlind b = attn_blind(p, q);
     blind = blind || b.before > 0 || b.past < q.n;
   }
-  int64_t units;
-  const int64_t before = block_before<kThreads>(mine, &units, shared[0]);
-  if (kTeams > 1) block_before<kThreads>(items, &all_items, shared[1]);
+  int64_t before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += x;
+  }
+  items = __reduce_add_sync(0xffffffffu, items);
+  if (lane == 31) warp_units[warp] = before, warp_items[warp] = items;
+  before -= mine;
+  __syncthreads();
+  int64_t units = 0, all_items = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_units[w];
+    units += warp_units[w];
+    all_items += warp_items[w];
+  }
   if (__any_sync(0xffffffffu, blind))
     for (int i = 0; i < each; ++i) {
       AttnRequest q = {0, 0, 0};
@@ -275,10 +274,8 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
         attn_no_keys(p, row0 + past + blockIdx.x, row0 + n, gridDim.x, true);
       }
     }
-  {
-    const int64_t at = (int64_t)blockIdx.x * (kThreads / 32) + warp, step = (int64_t)gridDim.x * (kThreads / 32);
-    const int start = p.a.R > 0 ? min(max(p.a.offsets[0], 0), p.a.T) : 0;
-    const int end = p.a.R > 0 ? min(max(p.a.offsets[p.a.R], 0), p.a.T) : 0;
+  if (start > 0 || max(start, end) < p.a.T) {
+    const int64_t at = (int64_t)blockIdx.x * kWarps + warp, step = (int64_t)gridDim.x * kWarps;
     attn_no_keys(p, at, start, step, false);
     attn_no_keys(p, max(start, end) + at, p.a.T, step, false);
   }
@@ -312,9 +309,20 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
   u = attn_start(line, w);
   u_end = attn_start(line, w + 1);
   cursor.start(p, found[i], found_rest[i]);
+  const bool passes = cursor.from > 0 && cursor.span.units <= kWhole;  // (an item that a worker before has whole)
   if (team == 1 && kTeams > 1 ? lane == 0 : threadIdx.x == 0)
-    p.places[w] = {cursor.q.row0, cursor.tile, cursor.head, cursor.rows(p), cursor.from, cursor.span.units};
+    p.places[w] = {cursor.q.row0, cursor.tile, cursor.head, cursor.rows(p), passes ? 0 : cursor.from, cursor.span.units};
+  if (passes) {
+    u += cursor.span.units - cursor.from;
+    if (u < u_end) cursor.next(p);
+  }
   return true;
+}
+
+// The units of the cursor's item that are this worker's, of a stretch of `left`.
+template <int kRows, int kUnit, int kWhole>
+__device__ __forceinline__ int attn_take(const AttnCursor<kRows, kUnit, kWhole>& c, int64_t left) {
+  return c.span.units <= kWhole ? c.span.units - c.from : (int)min((int64_t)c.span.units - c.from, left);
 }
 
 // ---------------------------------------------------------------- pieces of the kernels

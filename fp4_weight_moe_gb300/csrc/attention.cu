@@ -33,6 +33,9 @@ constexpr int kPair = 2 * kCacheBlock;  // tokens that a warp takes in one go: t
 // Items of fewer pairs on average go to a warp each (64 key heads' windows of
 // 128 tokens of 128 requests: @WIN@; with the four warps of a CTA @WIN4@).
 constexpr int kTeamSpan = 64;
+// Items of at most so many pairs are one worker's: a warp takes 0.6 us a pair by
+// itself, a part and its join about 4 us.
+constexpr int kWholePairs = 6;
 constexpr uint32_t kWaitCode = 1u;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -97,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   pdl_wait();
   pdl_launch_dependents();
 
-  AttnCursor<kRows, kPair, 16> c;
+  AttnCursor<kRows, kPair, kWholePairs> c;
   int64_t u, u_end;
   int team;
   if (!attn_stretch<kRows, kPair, kThreads, kWarps, kTeamSpan>(p, c, u, u_end, team)) return;

@@ -38,7 +38,7 @@ struct AttnArgs {
   AttnLine* line;
   AttnPlace* places; // [workers]
   int workers;       // at most
-  int least;         // units that are worth a worker
+  int least;         // units that are worth a worker (an item always is)
 };
 
 // Many rows to a key head (attention_tc.cu), and its parts' room.
@@ -283,7 +283,8 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
   team = kTeams > 1 && units < kTeamSpan * all_items ? 1 : kTeams;
   static_assert(kTeams == 1 || kTeams == 4, "a grain is a unit of each warp");
   const int most = team == kTeams ? p.workers / kTeams : p.workers;
-  const AttnLine line = attn_line(units, (int)max(min((int64_t)most, attn_quotient(units, p.least)), (int64_t)1),
+  const int64_t worth = max(all_items, attn_quotient(units, p.least)), grains = kTeams > 1 && team > 1 ? (units + 3) / 4 : units;
+  const AttnLine line = attn_line(units, (int)max(min((int64_t)most, min(worth, grains)), (int64_t)1),
                                   kTeams > 1 && team > 1 ? 2 : 0);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.line = line;
   const int teams = kTeams / team, w0 = (int)blockIdx.x * teams;
@@ -393,7 +394,7 @@ constexpr int kJoinThreads = 256, kJoinParts = 64;  // parts at a time
 // The parts of the item that worker w's stretch begins in the middle of: w -
 // 1's second place and the first ones of w .. last, summed in that order.
 template <int D, int kRows, int kJoin>
-__device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at, int w, int last) {
+__device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at, int row0, int w, int last) {
   // a thread has four columns of a row, kGroups threads the same, kTurns times
   constexpr int kQuads = D / 4;
   constexpr int kBusy = kJoin * kQuads < kJoinThreads ? kJoin * kQuads : kJoinThreads;
@@ -402,7 +403,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at
   __shared__ float old_factor[kJoin], tops[kJoin], sums[kJoin];
   __shared__ float4 shared_acc[kGroups > 1 ? kJoinThreads : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.y * kJoin, rows = min(at.rows - row0, kJoin);
+  const int rows = min(at.rows - row0, kJoin);
   if (rows <= 0) return;
   const int parts = last - w + 2;
   auto part_of = [&](int x) { return 2 * (int64_t)(w - 1 + x) + (x == 0 ? 1 : 0); };
@@ -485,41 +486,37 @@ __device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at
   }
 }
 
-// Joins each item that workers share, kJoin rows to a CTA, where the first
-// stretch that begins in its middle does.  The CTAs look through the workers
-// 32 at a time.
+// Joins each item that workers share, kJoin rows at a time, where the first
+// stretch that begins in its middle does.  The CTAs look through their shares
+// of workers and groups of rows, 32 at a time.
 template <int D, int kRows, int kJoin>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(AttnArgs p) {
+  constexpr int kGroupsOfRows = kRows / kJoin;
   pdl_wait();
   pdl_launch_dependents();
   const AttnLine line = *p.line;
-  for (int w0 = blockIdx.x; w0 < line.workers && line.units > 0; w0 += 32 * gridDim.x) {
-    const int mine = w0 + (threadIdx.x & 31) * (int)gridDim.x;
+  if (line.units == 0) return;
+  const int all = line.workers * kGroupsOfRows;
+  for (int i0 = blockIdx.x; i0 < all; i0 += 32 * gridDim.x) {
+    const int mine = i0 + (threadIdx.x & 31) * (int)gridDim.x, worker = mine / kGroupsOfRows;
     bool joins = false;
-    if (mine > 0 && mine < line.workers) {
-      const int from = p.places[mine].from;
-      joins = from != 0 && attn_start(line, mine - 1) <= attn_start(line, mine) - from;
+    if (mine < all && worker > 0) {
+      const int from = p.places[worker].from;
+      joins = from != 0 && attn_start(line, worker - 1) <= attn_start(line, worker) - from;
     }
     for (unsigned todo = __ballot_sync(0xffffffffu, joins); todo; todo &= todo - 1) {
-      const int w = w0 + (__ffs(todo) - 1) * (int)gridDim.x;
+      const int i = i0 + (__ffs(todo) - 1) * (int)gridDim.x, w = i / kGroupsOfRows;
       const AttnPlace at = p.places[w];
-      attn_join<D, kRows, kJoin>(p, at, w, attn_owner(line, attn_start(line, w) - at.from + at.units - 1));
+      attn_join<D, kRows, kJoin>(p, at, (i % kGroupsOfRows) * kJoin, w,
+                                 attn_owner(line, attn_start(line, w) - at.from + at.units - 1));
     }
   }
 }
 
 template <int D, int kRows, int kJoin>
 cudaError_t launch_attention_join(const AttnArgs& p, int sms, cudaStream_t st) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)min(p.workers, 2 * sms), (unsigned)(kRows / kJoin));
-  c.blockDim = dim3(kJoinThreads);
-  c.stream = st;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, attention_join_kernel<D, kRows, kJoin>, p);
+  const int grid = min(p.workers * (kRows / kJoin), (kRows > 16 ? 8 : 4) * sms);
+  return launch_dependent(attention_join_kernel<D, kRows, kJoin>, (unsigned)grid, kJoinThreads, st, p);
 }
 
 }  // namespace moe_fp4

@@ -516,7 +516,7 @@ template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
   // rows that an average request has to a key head
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
-  if (rows > 12) return launch_attention_tc(p, sms, st);
+  if (rows > 16) return launch_attention_tc(p, (int)rows, sms, st);
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);
 }
 

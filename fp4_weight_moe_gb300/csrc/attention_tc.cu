@@ -18,8 +18,8 @@
 //   load warp      a block's half (keys or values of 16 tokens) to a bulk
 //                  copy, a lane each, into a ring of half steps.
 // With two tiles each has its scores; while one's softmax runs, the other's
-// products do.  With one (D = 256, whose sums take half of tensor memory) two
-// buffers of scores alternate between steps.
+// products do.  With one (few rows, or D = 256, whose sums take half of tensor
+// memory) two buffers of scores alternate between steps.
 //
 // The maximum follows the scores only when they outgrow it by 2^8 (p stays
 // within FP16, sums and divisor are taken against the same m), so that the
@@ -32,9 +32,9 @@ namespace moe_fp4 {
 
 namespace {
 
-template <int D>
+template <int D, int kTiles_>
 struct TcCfg {
-  static constexpr int kTiles = D <= 128 ? 2 : 1;
+  static constexpr int kTiles = kTiles_;
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kTok = D <= 128 ? 128 : 64;
   static constexpr int kBlocks = kTok / kCacheBlock;
@@ -42,7 +42,7 @@ struct TcCfg {
   static constexpr uint32_t kKv = kTok * D * 2;  // decoded keys or values of a step
   static constexpr uint32_t kPanel = kTok * 128;    // 64 columns of them: swizzled rows of 128 bytes
   static constexpr uint32_t kHalf = kBlocks * cache_half_bytes(D);
-  static constexpr int kRaw = D == 64 ? 6 : 3;   // half steps in flight
+  static constexpr int kRaw = D == 64 || (D == 128 && kTiles == 1) ? 6 : 3;  // half steps in flight
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kDecWarps = 8;
   static constexpr int kMmaWarp = kSoftWarps + kDecWarps, kLoadWarp = kMmaWarp + 1;
@@ -122,10 +122,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 constexpr uint32_t kTcWait = 2u;
 
-template <int D>
-__global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(AttnArgs p, uint32_t* err) {
-  using C = TcCfg<D>;
-  constexpr int kTok = C::kTok, kTiles = C::kTiles;
+template <int D, int kTiles>
+__global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_kernel(AttnArgs p, uint32_t* err) {
+  using C = TcCfg<D, kTiles>;
+  constexpr int kTok = C::kTok;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* q_smem = smem;
@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
         whole_hi = base_pos + attn_row(p, tile_rows, 128 * n).query;
       }
 
+      const int warp_rows = c.rows(p);
       float m = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
       int tok0 = (c.span.first + c.from) * kTok;
@@ -438,6 +439,12 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
           break;
         }
         tc_fence_after();
+        if (tile_row - lane >= warp_rows) {  // (no rows of this warp's: nobody reads what it leaves)
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[buffer]);
+          continue;
+        }
         const uint32_t s_tmem = tmem + lanes + buffer * 128;
         if (tok0 < whole_lo || tok0 + kTok - 1 > whole_hi) {
           // masked where they are, so that the loop below has no test for it
@@ -584,38 +591,40 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1) attention_tc_kernel(Att
   if (warp == C::kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
-cudaError_t launch_tc_dim(AttnArgs p, int sms, cudaStream_t st) {
-  using C = TcCfg<D>;
+template <int D, int kTiles>
+cudaError_t launch_tiles(AttnArgs p, int sms, cudaStream_t st) {
+  using C = TcCfg<D, kTiles>;
   static bool seen[64];
-  cudaError_t e = allow_smem(attention_tc_kernel<D>, C::kSmem, seen);
+  cudaError_t e = allow_smem(attention_tc_kernel<D, kTiles>, C::kSmem, seen);
   if (e != cudaSuccess) return e;
   void* err = nullptr;
   e = attention_status_address(&err);
   if (e != cudaSuccess) return e;
   p.workers = sms;
   p.least = 4;
-  e = launch_dependent_smem(attention_tc_kernel<D>, (unsigned)sms, C::kThreads, C::kSmem, st, p, static_cast<uint32_t*>(err));
+  e = launch_dependent_smem(attention_tc_kernel<D, kTiles>, (unsigned)sms, C::kThreads, C::kSmem, st, p, static_cast<uint32_t*>(err));
   if (e != cudaSuccess) return e;
   return launch_attention_join<D, C::kRows, 8>(p, sms, st);
 }
 
+// Tiles of rows side by side: two, but where D = 256 leaves room for the sums
+// of one, and where an average request has rows for one.
+constexpr int most_tiles(int D) { return D <= 128 ? 2 : 1; }
+
 template <int D>
-size_t parts_bytes(int sms) {
-  return (size_t)2 * sms * TcCfg<D>::kRows * (D + 2) * 4;
+cudaError_t launch_tc_dim(const AttnArgs& p, int rows, int sms, cudaStream_t st) {
+  return rows <= 128 ? launch_tiles<D, 1>(p, sms, st) : launch_tiles<D, most_tiles(D)>(p, sms, st);
 }
 
 }  // namespace
 
-size_t attention_tc_parts_bytes(int D, int sms) {
-  return D == 64 ? parts_bytes<64>(sms) : D == 128 ? parts_bytes<128>(sms) : parts_bytes<256>(sms);
-}
+size_t attention_tc_parts_bytes(int D, int sms) { return (size_t)2 * sms * 128 * most_tiles(D) * (D + 2) * 4; }
 
-cudaError_t launch_attention_tc(const AttnArgs& p, int sms, cudaStream_t st) {
+cudaError_t launch_attention_tc(const AttnArgs& p, int rows, int sms, cudaStream_t st) {
   switch (p.a.D) {
-    case 64: return launch_tc_dim<64>(p, sms, st);
-    case 128: return launch_tc_dim<128>(p, sms, st);
-    default: return launch_tc_dim<256>(p, sms, st);
+    case 64: return launch_tc_dim<64>(p, rows, sms, st);
+    case 128: return launch_tc_dim<128>(p, rows, sms, st);
+    default: return launch_tc_dim<256>(p, rows, sms, st);
   }
 }
 

@@ -41,8 +41,9 @@ struct AttnArgs {
   int least;         // units that are worth a worker (an item always is)
 };
 
-// Many rows to a key head (attention_tc.cu), and its parts' room.
-cudaError_t launch_attention_tc(const AttnArgs& p, int sms, cudaStream_t st);
+// Many rows to a key head (attention_tc.cu; `rows`: of an average request), and
+// its parts' room.
+cudaError_t launch_attention_tc(const AttnArgs& p, int rows, int sms, cudaStream_t st);
 size_t attention_tc_parts_bytes(int D, int sms);
 
 // A request of the batch.

@@ -545,21 +545,29 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       }
       uint8_t* stage = q_smem + n * C::kQTile + (warp & 3) * 32 * 128;  // 32 rows of 128 bytes, the warp's own
       const int chunk_row = lane / 8, chunk = lane % 8, row0 = 128 * n + 32 * (warp & 3);
-      const int columns = whole ? 64 : 32;  // of 128 bytes
+      uint8_t* to[8];  // where the lane's rows go
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        const int r = row0 + 4 * y + chunk_row;
+        const AttnRows rr = attn_row(p, tile_rows, r);
+        to[y] = r >= rows ? nullptr
+                : whole ? reinterpret_cast<uint8_t*>(attn_out(p, c.q.row0 + rr.query, c.head * p.group + rr.head)) + 16 * chunk
+                        : reinterpret_cast<uint8_t*>(p.parts + (part * C::kRows + r) * D) + 16 * chunk;
+      }
 #pragma unroll 1
-      for (int x = 0; x < D; x += columns) {
+      for (int x = 0; x < D * (whole ? 2 : 4); x += 128) {
         uint32_t o[32];
         if (whole) {
+          uint32_t f[2][32];
+          TmemLd<32>::start(o_tmem + x / 2, f[0]);
+          TmemLd<32>::start(o_tmem + x / 2 + 32, f[1]);
+          TmemLd<32>::wait(f[0]);
+          TmemLd<32>::wait(f[1]);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t f[32];
-            tmem_ld32(o_tmem + x + 32 * y, f);
-#pragma unroll
-            for (int z = 0; z < 16; ++z)
-              o[16 * y + z] = pack_bf16x2(__uint_as_float(f[2 * z]) * inv, __uint_as_float(f[2 * z + 1]) * inv);
-          }
+          for (int z = 0; z < 32; ++z)
+            o[z] = pack_bf16x2(__uint_as_float(f[z / 16][2 * z % 32]) * inv, __uint_as_float(f[z / 16][2 * z % 32 + 1]) * inv);
         } else {
-          tmem_ld32(o_tmem + x, o);
+          tmem_ld32(o_tmem + x / 4, o);
         }
         __syncwarp();
 #pragma unroll
@@ -567,17 +575,13 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) =
               make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
         __syncwarp();
+        uint4 v[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          const int r = 4 * y + chunk_row;
-          if (row0 + r >= rows) continue;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((chunk ^ (r & 7)) << 4));
-          const AttnRows rr = attn_row(p, tile_rows, row0 + r);
-          if (whole)
-            *reinterpret_cast<uint4*>(attn_out(p, c.q.row0 + rr.query, c.head * p.group + rr.head) + x + 8 * chunk) = v;
-          else
-            *reinterpret_cast<uint4*>(p.parts + (part * C::kRows + row0 + r) * D + x + 4 * chunk) = v;
-        }
+        for (int y = 0; y < 8; ++y)
+          v[y] = *reinterpret_cast<const uint4*>(stage + (4 * y + chunk_row) * 128 + ((chunk ^ ((4 * y + chunk_row) & 7)) << 4));
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          if (to[y]) *reinterpret_cast<uint4*>(to[y] + x) = v[y];
         __syncwarp();
       }
       ++item;

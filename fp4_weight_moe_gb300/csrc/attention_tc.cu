@@ -3,12 +3,12 @@
 //
 // A CTA takes kTiles tiles of 128 rows (query and head of a group each) over a
 // key head's tokens, kTok at a time (a step):
-//   softmax warps  (four per tile of rows, or of one tile) own a row per
-//                  thread: they bring q to shared memory as FP16, scaled by a
-//                  power of two per row; read a step's scores from tensor
-//                  memory, take the running maximum, and put p = 2^(x - m)
-//                  back over them in FP16, the second product's A operand;
-//                  at the end they read the sums and write the rows out;
+//   softmax warps  (four or eight per tile of rows) own a row, or half of its
+//                  columns, per thread: they bring q to shared memory as FP16,
+//                  scaled by a power of two per row; read a step's scores from
+//                  tensor memory, take the running maximum, and put p =
+//                  2^(x - m) back over them in FP16, the second product's A
+//                  operand; at the end they read the sums and write the rows;
 //   decode warps   turn the cache's codes into FP16 (exact: at most six
 //                  significant bits in [2^-10, 2688]) in shared memory, in the
 //                  128-byte-swizzled layout that the products read: keys
@@ -43,16 +43,24 @@ struct TcCfg {
   static constexpr uint32_t kPanel = kTok * 128;    // 64 columns of them: swizzled rows of 128 bytes
   static constexpr uint32_t kHalf = kBlocks * cache_half_bytes(D);
   static constexpr int kRaw = D == 64 || (D == 128 && kTiles == 1) ? 6 : 3;  // half steps in flight
-  static constexpr int kSoftWarps = 4 * kTiles;
+  // A row's threads: with one tile, whose softmax the products of the other
+  // buffer hide no longer, two (35 rows of five requests of 100000 tokens 273
+  // us with one, 257 with two); two tiles' hide one another's, and twice the
+  // warps take more instructions (chunks of 2048 tokens 586 and 611 us).
+  static constexpr int kSides = kTiles == 1 ? 2 : 1;
+  static constexpr int kCols = kTok / kSides;  // of a step's scores: a softmax thread's
+  static constexpr int kSoftWarps = 4 * kSides * kTiles;
   static constexpr int kDecWarps = 8;
   static constexpr int kMmaWarp = kSoftWarps + kDecWarps, kLoadWarp = kMmaWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 4);  // (whole warpgroups, for the split of registers)
   // registers of the softmax, the decode and the last warpgroup's threads: together no more than the launch's
-  static constexpr int kSoftRegs = kTiles == 2 ? 136 : 208, kDecRegs = kTiles == 2 ? 72 : 88, kLastRegs = kTiles == 2 ? 64 : 80;
+  static constexpr int kSoftRegs = 136, kDecRegs = 72, kLastRegs = 64;
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
   static_assert(32 * (kSoftWarps * kSoftRegs + kDecWarps * kDecRegs + 4 * kLastRegs) <= kThreads * kLaunchRegs, "registers");
   static constexpr uint32_t kTmemO = 2 * 128;    // the sums lie behind two buffers of scores
-  static constexpr uint32_t kBytes = kTiles * kQTile + 4 * kKv + kRaw * kHalf;
+  // the sums go out by way of 4096 bytes to a softmax warp: the queries' place, if that is enough
+  static constexpr uint32_t kStage = D == 64 && kSides == 2 ? 4096 * kSoftWarps : 0;
+  static constexpr uint32_t kBytes = kTiles * kQTile + 4 * kKv + kRaw * kHalf + kStage;
   static constexpr uint32_t kBarBytes = 512;
   static constexpr uint32_t kSmem = kBytes + kBarBytes + 1024 /*align*/;
   static_assert(kSmem <= 227 * 1024, "shared memory");
@@ -120,19 +128,37 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The warps that share rows (one, or two of 64 threads, all of which come):
+// whether any of them says so.
+template <int kSides>
+__device__ __forceinline__ bool rows_any(int id, bool x) {
+  if constexpr (kSides == 1) return __any_sync(0xffffffffu, x);
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(id), "r"((uint32_t)x) : "memory");
+  return r != 0;
+}
+template <int kSides>
+__device__ __forceinline__ void rows_sync(int id) {
+  if constexpr (kSides == 1)
+    __syncwarp();
+  else
+    asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
+}
+
 constexpr uint32_t kTcWait = 2u;
 
 template <int D, int kTiles>
 __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_kernel(AttnArgs p, uint32_t* err) {
   using C = TcCfg<D, kTiles>;
-  constexpr int kTok = C::kTok;
+  constexpr int kTok = C::kTok, kSides = C::kSides;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* q_smem = smem;
   uint8_t* k_smem = q_smem + kTiles * C::kQTile;  // two buffers
   uint8_t* v_smem = k_smem + 2 * C::kKv;          // two buffers
   uint8_t* raw = v_smem + 2 * C::kKv;
-  uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw + C::kRaw * C::kHalf);
+  uint64_t* raw_full = reinterpret_cast<uint64_t*>(raw + C::kRaw * C::kHalf + C::kStage);
   uint64_t* raw_empty = raw_full + C::kRaw;
   uint64_t* kv_full = raw_empty + C::kRaw;  // [keys 0, keys 1, values 0, values 1]
   uint64_t* kv_empty = kv_full + 4;
@@ -155,9 +181,9 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 4 * C::kSides);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], 4 * C::kSides);
     }
     fence_mbar_init();
   }
@@ -167,6 +193,11 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   // are worth more to the loops between items)
   __shared__ AttnCursor<C::kRows, kTok, 2> cursors[C::kThreads / 32];
   AttnCursor<C::kRows, kTok, 2>& c = cursors[warp];
+  // what the threads of a row tell each other: its queries' factor (in the
+  // first half), their scores' largest, their divisors
+  __shared__ float told[2][C::kRows];
+  __shared__ uint32_t dead[4 * kTiles];  // a wait of a row's gave up
+  if (threadIdx.x < 4 * kTiles) dead[threadIdx.x] = 0;  // (seen behind the barrier below)
   int left;  // units of the stretch that are left
   {
     int64_t u, u_end;
@@ -364,9 +395,13 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
     }
   } else {
     regs_inc<C::kSoftRegs>();
-    const int n = warp / 4, row_in_tile = threadIdx.x & 127, tile_row = 128 * n + row_in_tile;
+    // a row's threads have kCols of a step's columns each, and D / kSides of the sums'
+    const int n = warp / (4 * kSides), side_of = kSides == 2 ? (warp >> 2) & 1 : 0;
+    const int row_in_tile = threadIdx.x & 127, tile_row = 128 * n + row_in_tile;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_tmem = tmem + lanes + C::kTmemO + n * D;
+    const uint32_t o_tmem = tmem + lanes + C::kTmemO + n * D + side_of * (D / kSides);
+    const int pair = 4 * n + (warp & 3), id = 1 + pair;  // (of the two warps that share rows: a barrier of their own)
+    const int col0 = side_of * C::kCols;
     uint32_t step = 0;  // over all items
     uint32_t item = 0;
     bool ok = true;
@@ -376,16 +411,16 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       const AttnRows tile_rows = attn_rows(p, c.tile * C::kRows);
       {
         const int rows = c.rows(p);
-        // q in FP16, the sign of the scale with it: D / 8 lanes to a row, the warp's 32 rows in turn
-        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kAtOnce;
-        const int l = lane % kLanes, side = lane / kLanes, first = 32 * (warp & 3);  // (row of the tile)
+        // q in FP16, the sign of the scale with it: D / 8 lanes to a row, 32 / kSides of the rows to a warp
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kTurns = 32 / kSides / kAtOnce, kFlight = kTurns < 8 ? kTurns : 8;
+        const int l = lane % kLanes, side = lane / kLanes, first = 32 * (warp & 3) + 32 / kSides * side_of;  // (row of the tile)
         float back = 1.f;
         uint8_t* dst = q_smem + n * C::kQTile + (l / 8) * 16384;
 #pragma unroll 1
-        for (int i = 0; i < kTurns; i += 8) {
-          uint4 x[8];
+        for (int i = 0; i < kTurns; i += kFlight) {
+          uint4 x[kFlight];
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
+          for (int y = 0; y < kFlight; ++y) {
             const int r = 128 * n + first + (i + y) * kAtOnce + side;
             const AttnRows rr = attn_row(p, tile_rows, r);
             x[y] = r < rows ? *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) +
@@ -394,7 +429,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
                             : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
+          for (int y = 0; y < kFlight; ++y) {
             const int r = first + (i + y) * kAtOnce + side;
             float v[8], top = 0.f, b;
             bf16x8_to_float(x[y], v);
@@ -407,12 +442,20 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
             *reinterpret_cast<uint4*>(dst + r * 128 + (((l % 8) ^ (r & 7)) << 4)) =
                 make_uint4(pack_f16x2(v[0] * by, v[1] * by), pack_f16x2(v[2] * by, v[3] * by),
                            pack_f16x2(v[4] * by, v[5] * by), pack_f16x2(v[6] * by, v[7] * by));
-            const float mine = __shfl_sync(0xffffffffu, b, (lane % kAtOnce) * kLanes);
-            if (lane / kAtOnce == i + y) back = mine;
+            if (kSides == 2) {
+              if (l == 0) told[0][128 * n + r] = b;
+            } else {
+              const float mine = __shfl_sync(0xffffffffu, b, (lane % kAtOnce) * kLanes);
+              if (lane / kAtOnce == i + y) back = mine;
+            }
           }
         }
-        fac = fmaxf(back * fabsf(p.a.scale) * p.a.k_scale * kLog2e, 0x1p-120f);  // (above 0: masked scores stay -inf)
         fence_proxy_async_smem();
+        if (kSides == 2) {
+          rows_sync<kSides>(id);
+          back = told[0][tile_row];
+        }
+        fac = fmaxf(back * fabsf(p.a.scale) * p.a.k_scale * kLog2e, 0x1p-120f);  // (above 0: masked scores stay -inf)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[n]);
@@ -435,8 +478,11 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       for (int i = 0; i < steps; ++i, ++step, tok0 += kTok) {
         const int buffer = kTiles == 2 ? n : (int)(step & 1);
         if (!wait(&s_full[buffer], kTiles == 2 ? step : step >> 1)) {
-          ok = false;
-          break;
+          if (kSides == 1 || tile_row - lane >= warp_rows) {
+            ok = false;
+            break;
+          }
+          dead[pair] = 1;  // (told before the next vote, behind which both warps leave)
         }
         tc_fence_after();
         if (tile_row - lane >= warp_rows) {  // (no rows of this warp's: nobody reads what it leaves)
@@ -445,13 +491,13 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           if (lane == 0) mbar_arrive(&p_full[buffer]);
           continue;
         }
-        const uint32_t s_tmem = tmem + lanes + buffer * 128;
+        const uint32_t s_tmem = tmem + lanes + buffer * 128 + col0;
         if (tok0 < whole_lo || tok0 + kTok - 1 > whole_hi) {
           // masked where they are, so that the loop below has no test for it
           // (as predicates there, they took as many instructions as the rest)
-          const int hi = pos - tok0, lo = lowest - tok0;
+          const int hi = pos - tok0 - col0, lo = lowest - tok0 - col0;
 #pragma unroll 1
-          for (int x = 0; x < kTok; x += 16) {
+          for (int x = 0; x < C::kCols; x += 16) {
             uint32_t s[16];
             tmem_ld16(s_tmem + x, s);
 #pragma unroll
@@ -461,7 +507,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           }
           tmem_wait_st();
         }
-        uint32_t h[kTok / 2];
+        uint32_t h[C::kCols / 2];
         float2 sum[2];  // (sums and maxima in chains of their own, which depend on one another less)
         // against the maximum so far; where a score outgrows it, once more against its own
 #pragma unroll 1
@@ -473,9 +519,9 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           uint32_t s[2][16];
           TmemLd<16>::start(s_tmem, s[0]);
 #pragma unroll
-          for (int x = 0; x < kTok / 16; ++x) {
+          for (int x = 0; x < C::kCols / 16; ++x) {
             TmemLd<16>::wait(s[x & 1]);
-            if (x + 1 < kTok / 16) TmemLd<16>::start(s_tmem + 16 * (x + 1), s[(x + 1) & 1]);
+            if (x + 1 < C::kCols / 16) TmemLd<16>::start(s_tmem + 16 * (x + 1), s[(x + 1) & 1]);
 #pragma unroll
             for (int y = 0; y < 16; y += 2)
               tops[y / 2 % 4] = max3(tops[y / 2 % 4], __uint_as_float(s[x & 1][y]), __uint_as_float(s[x & 1][y + 1]));
@@ -488,21 +534,32 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
               h[8 * x + y] = pack_f16x2(e.x, e.y);
             }
           }
-          const float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * fac;
-          const bool grows = top > m + 8.f;  // (m -inf: as soon as there is a key)
-          if (!__any_sync(0xffffffffu, grows) || pass > 0) break;
+          float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * fac;
+          // (m -inf: as soon as there is a key; and behind it both have read their scores, over which p goes)
+          if (kSides == 2) tc_fence_before();
+          bool grows = top > m + 8.f;
+          const bool any = rows_any<kSides>(id, grows);
+          if (kSides == 2) tc_fence_after();
+          if (!any || pass > 0) break;
+          if (kSides == 2) {
+            told[side_of][tile_row] = top;
+            rows_sync<kSides>(id);
+            top = fmaxf(told[0][tile_row], told[1][tile_row]);
+            grows = top > m + 8.f;
+          }
           const float by = grows ? exp2_approx(m - top) : 1.f;
           if (grows) m = top;
           l.x *= by;
           l.y *= by;
           if (i > 0) {
             if (!wait(&pv_done[n], step - 1)) {
-              ok = false;
-              break;
+              ok = kSides == 2;
+              if (kSides == 1) break;
+              dead[pair] = 1;
             }
             tc_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < D / 16; ++x) {
+            for (int x = 0; x < D / kSides / 16; ++x) {
               uint32_t o[16];
               tmem_ld16(o_tmem + 16 * x, o);
 #pragma unroll
@@ -511,24 +568,35 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
             }
           }
         }
-        if (!ok) break;
+        if (kSides == 1 && !ok) break;
         l = fadd2(l, fadd2(sum[0], sum[1]));
 #pragma unroll
-        for (int x = 0; x < kTok / 32; ++x) tmem_st16(s_tmem + 16 * x, *reinterpret_cast<uint32_t(*)[16]>(&h[16 * x]));
+        for (int x = 0; x < C::kCols / 32; ++x)
+          tmem_st16(s_tmem - col0 / 2 + 16 * x, *reinterpret_cast<uint32_t(*)[16]>(&h[16 * x]));
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buffer]);
+        if (kSides == 2 && *(volatile uint32_t*)&dead[pair]) {
+          ok = false;
+          break;
+        }
       }
       // (the last scores come before the last two sums where buffers alternate,
       // and a wait for a phase is met by the one two before it: both, in order)
       if (kTiles == 1 && steps > 1 && ok) ok = wait(&pv_done[n], step - 2);
-      if (!ok || !wait(&pv_done[n], step - 1)) break;
+      if (kSides == 1) {
+        if (!ok || !wait(&pv_done[n], step - 1)) break;
+      } else {
+        if (ok) ok = wait(&pv_done[n], step - 1);
+        told[side_of][tile_row] = l.x + l.y;
+        if (rows_any<kSides>(id, !ok)) break;
+      }
       tc_fence_after();
       // The sums go out by way of the queries' place (the item's scores are
       // all done): 128 bytes of a row at a time, so that stores lie along rows.
       const int rows = c.rows(p);
-      const float sum = l.x + l.y;
+      const float sum = kSides == 1 ? l.x + l.y : told[0][tile_row] + told[1][tile_row];
       const bool whole = c.from == 0 && steps == c.span.units;
       const int64_t part = 2 * (int64_t)blockIdx.x + (c.from == 0 ? 1 : 0);
       float inv = 1.f;
@@ -538,33 +606,37 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           const int hq = c.head * p.group + rr.head;
           float lse;
           inv = attn_finish(p, hq, m, sum, lse);
-          if (p.a.lse) p.a.lse[(int64_t)(c.q.row0 + rr.query) * p.a.Hq + hq] = lse;
-        } else {
+          if (p.a.lse && side_of == 0) p.a.lse[(int64_t)(c.q.row0 + rr.query) * p.a.Hq + hq] = lse;
+        } else if (side_of == 0) {
           *reinterpret_cast<float2*>(attn_stats<D, C::kRows>(p, part, tile_row)) = make_float2(m, sum);
         }
       }
-      uint8_t* stage = q_smem + n * C::kQTile + (warp & 3) * 32 * 128;  // 32 rows of 128 bytes, the warp's own
+      uint8_t* stage = C::kStage ? raw + C::kRaw * C::kHalf + 4096 * warp  // 32 rows of 128 bytes, the warp's own
+                                 : q_smem + n * C::kQTile + side_of * 16384 + (warp & 3) * 32 * 128;
       const int chunk_row = lane / 8, chunk = lane % 8, row0 = 128 * n + 32 * (warp & 3);
+      const int row_bytes = (whole ? 2 : 4) * D / kSides;  // this warp's of a row
       uint8_t* to[8];  // where the lane's rows go
 #pragma unroll
       for (int y = 0; y < 8; ++y) {
         const int r = row0 + 4 * y + chunk_row;
         const AttnRows rr = attn_row(p, tile_rows, r);
         to[y] = r >= rows ? nullptr
-                : whole ? reinterpret_cast<uint8_t*>(attn_out(p, c.q.row0 + rr.query, c.head * p.group + rr.head)) + 16 * chunk
-                        : reinterpret_cast<uint8_t*>(p.parts + (part * C::kRows + r) * D) + 16 * chunk;
+                          : (whole ? reinterpret_cast<uint8_t*>(attn_out(p, c.q.row0 + rr.query, c.head * p.group + rr.head))
+                                   : reinterpret_cast<uint8_t*>(p.parts + (part * C::kRows + r) * D)) +
+                                side_of * row_bytes + 16 * chunk;
       }
 #pragma unroll 1
-      for (int x = 0; x < D * (whole ? 2 : 4); x += 128) {
+      for (int x = 0; x < row_bytes; x += 128) {
         uint32_t o[32];
         if (whole) {
-          uint32_t f[2][32];
-          TmemLd<32>::start(o_tmem + x / 2, f[0]);
-          TmemLd<32>::start(o_tmem + x / 2 + 32, f[1]);
-          TmemLd<32>::wait(f[0]);
-          TmemLd<32>::wait(f[1]);
+          constexpr int kLoads = D / kSides < 64 ? 1 : 2;  // (columns that make 128 bytes, or all that there are)
+          uint32_t f[kLoads][32];
 #pragma unroll
-          for (int z = 0; z < 32; ++z)
+          for (int y = 0; y < kLoads; ++y) TmemLd<32>::start(o_tmem + x / 2 + 32 * y, f[y]);
+#pragma unroll
+          for (int y = 0; y < kLoads; ++y) TmemLd<32>::wait(f[y]);
+#pragma unroll
+          for (int z = 0; z < 16 * kLoads; ++z)
             o[z] = pack_bf16x2(__uint_as_float(f[z / 16][2 * z % 32]) * inv, __uint_as_float(f[z / 16][2 * z % 32 + 1]) * inv);
         } else {
           tmem_ld32(o_tmem + x / 4, o);
@@ -572,8 +644,9 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         __syncwarp();
 #pragma unroll
         for (int y = 0; y < 8; ++y)
-          *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          if (D / kSides >= 64 || 16 * y < row_bytes)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
         __syncwarp();
         uint4 v[8];
 #pragma unroll
@@ -581,9 +654,10 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           v[y] = *reinterpret_cast<const uint4*>(stage + (4 * y + chunk_row) * 128 + ((chunk ^ ((4 * y + chunk_row) & 7)) << 4));
 #pragma unroll
         for (int y = 0; y < 8; ++y)
-          if (to[y]) *reinterpret_cast<uint4*>(to[y] + x) = v[y];
+          if (to[y] && (D / kSides >= 64 || x + 16 * chunk < row_bytes)) *reinterpret_cast<uint4*>(to[y] + x) = v[y];
         __syncwarp();
       }
+      if (kSides == 2) rows_sync<kSides>(id);  // (the next queries go over both sides' place)
       ++item;
       left -= steps;
       if (left > 0) c.next(p);

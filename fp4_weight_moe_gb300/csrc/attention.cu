@@ -16,6 +16,15 @@
 // products' rows as (0, 4, 1, 5, 2, 6, 3, 7), and the same 8 later, so that
 // the lanes that read the values of their two tokens at once lie on other
 // banks.  q is scaled by a power of two per row into FP16's range.
+//
+// Bound by the cache's bytes (0.56 of a byte a value, each read once for a
+// group of up to 16 rows) and by the 650 or so instructions that a warp takes
+// for 32 tokens of 128 columns, which take as long: of 64 requests' 440 MB the
+// copies alone take 76 us, the arithmetic alone 76, both 97 (4.5 TB/s), and
+// the join of the shared items 8 (the counters: 57% of the issue slots, half
+// of the ALU's, 52% of the memory's time).  Six of ten instructions turn
+// codes into FP16 and scale them, which FP16's products need and the values'
+// 8-bit forms would not carry exactly.
 #include "attention_work.cuh"
 #include "host.cuh"
 #include "tcgen05.cuh"
@@ -30,8 +39,8 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kPair = 2 * kCacheBlock;  // tokens that a warp takes in one go: two blocks
-// Items of fewer pairs on average go to a warp each (64 key heads' windows of
-// 128 tokens of 128 requests: @WIN@; with the four warps of a CTA @WIN4@).
+// Items of fewer pairs on average go to a warp each (windows of 128 tokens of
+// 128 requests: 16.4 us; with the four warps of a CTA to an item 24.4).
 constexpr int kTeamSpan = 64;
 // Items of at most so many pairs are one worker's: a warp takes 0.6 us a pair by
 // itself, a part and its join about 4 us.
@@ -514,7 +523,10 @@ cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
-  // rows that an average request has to a key head
+  // Rows that an average request has to a key head.  Up to 8 fill one product
+  // of 8 columns and up to 16 two (16 requests of 16384 tokens, some four
+  // queries of four heads each: 98 us; on tiles of 128 rows, whose decoding
+  // warps bring 2.9 TB/s, 180).
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
   if (rows > 16) return launch_attention_tc(p, (int)rows, sms, st);
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);

@@ -18,6 +18,11 @@
 // products without error by the published steps of D. E. Knuth, TAOCP 2,
 // 4.2.2, and T. J. Dekker, "A floating-point technique for extending the
 // available precision", 1971), good to about 2^-44.
+//
+// 8192 tokens of 32 query and 8 key heads of 128 columns (178 MB): 46 us, 3.9
+// TB/s; bound by issue (69% of the slots, the ALU 59% busy: a quotient, two
+// borders and a code for each of the cached values), not by memory (without
+// the cache 1001 tokens of wide heads take 7.2 us, which is 2.6 TB/s of L2).
 #include "attention.cuh"
 #include "fp8_quant.cuh"
 #include "host.cuh"
@@ -317,7 +322,7 @@ __device__ __forceinline__ bool head_any(bool v, int side) {
 
 // A warp's task: per_q queries or per_k keys of a token.  Its loads are one
 // iteration ahead.  (Several tokens to a task, with the weights kept, needed
-// more registers than there are: 77 us where this takes 49, @ROPE@.)
+// more registers than there are: 77 us where this took 49.)
 template <int D, int kBlocks = 7>
 __global__ void __launch_bounds__(kRopeThreads, kBlocks) qk_norm_rope_kernel(moe_fp4_qk_norm_rope_args a, int per_q,
                                                                              int q_tasks, int per_k, int tasks) {

@@ -1,6 +1,7 @@
 """GB300-native fused FP4-weight mixture-of-experts layer, and the operators
 around it (FP8 block-scaled products, norms, the router's choice; see
-``ops``).
+``ops``; a paged cache in 4 bits and the attention over it; see
+``attention``).
 
 The compute path is ``libmoe_fp4.so`` (hand-written CUDA for sm_103a behind a
 C ABI, see ``include/moe_fp4.h``).  This package is its thin Python binding:

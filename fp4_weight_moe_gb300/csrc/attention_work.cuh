@@ -84,7 +84,7 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& p, const AttnReque
   AttnSpan s;
   const int q0 = row / p.group, q1 = min((row + rows - 1) / p.group, q.n - 1);
   const int p0 = q.length - q.n + q0, p1 = q.length - q.n + q1;
-  s.lo = p.a.window > 0 ? max(p0 - p.a.window + 1, 0) : 0;
+  s.lo = p.a.window > 0 ? max(max(p0, 0) - p.a.window + 1, 0) : 0;  // (p0 -n at least: its difference stays in 32 bits)
   s.hi = min(p1 + 1, p.capacity);
   s.first = s.lo / kUnit;
   s.units = s.hi > s.lo ? (s.hi + kUnit - 1) / kUnit - s.first : 0;

@@ -108,7 +108,9 @@ int moe_fp4_attention(const moe_fp4_attention_args* p, void* stream) {
   if (st != MOE_FP4_OK) return st;
   if (!page_ok(a.page_size)) return MOE_FP4_EUNSUPPORTED;
   if (a.pages <= 0 || a.table_width < 0 || a.window < 0) return MOE_FP4_EINVAL;
-  if ((int64_t)a.table_width * a.page_size > INT32_MAX || (int64_t)a.T * a.Hq > INT32_MAX) return MOE_FP4_EUNSUPPORTED;
+  // (a step past the last token is counted in 32 bits too)
+  if ((int64_t)a.table_width * a.page_size > INT32_MAX - 1023 || (int64_t)a.T * a.Hq > INT32_MAX)
+    return MOE_FP4_EUNSUPPORTED;
   if (!std::isfinite(a.scale) || !positive(a.k_scale) || !positive(a.v_scale)) return MOE_FP4_EINVAL;
   if (a.T == 0) return MOE_FP4_OK;
   if (!heads_ok(a.q, a.q_row, a.q_head, a.T, a.Hq, a.D, false) ||

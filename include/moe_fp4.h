@@ -859,7 +859,8 @@ MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, 
  * the probabilities in FP16; sums, maxima and divisors are FP32.  Results are
  * deterministic for given inputs and device.
  * q and out: bf16 [T][Hq][D], 16-byte aligned, strides multiples of 8
- * elements (MOE_FP4_EINVAL); Hq % Hkv == 0, Hq / Hkv <= 64, R <= 65536
+ * elements (MOE_FP4_EINVAL); Hq % Hkv == 0, Hq / Hkv <= 64, R <= 65536,
+ * table_width * page_size <= 2^31 - 1024, T * Hq < 2^31
  * (MOE_FP4_EUNSUPPORTED).  workspace: moe_fp4_attention_workspace_bytes
  * bytes, 256-byte aligned, no initialisation needed; calls that may run at
  * the same time need workspaces of their own.

@@ -105,6 +105,10 @@ def test_attention_arguments():
     for bad in (dict(D=96), dict(Hq=9), dict(Hq=130, q_row=16640, out_row=16640), dict(R=65537), dict(page_size=20),
                 dict(table_width=1 << 27, table_row=1 << 27)):
         assert attention(**bad) == EUNSUPPORTED, bad
+    # a table whose last step of tokens would pass 32 bits, and the widest that does not
+    for width, page in (((1 << 27) - 1, 16), ((1 << 24) - 1, 128)):
+        assert attention(table_width=width, table_row=width, page_size=page) == EUNSUPPORTED
+    assert attention(table_width=(1 << 27) - 64, table_row=1 << 27, T=0) == OK
     # heads within rows, or rows within heads
     assert attention(out_row=128, out_head=504) == EINVAL
     for bad in (dict(workspace=0), dict(workspace=P + 16), dict(workspace_bytes=64)):

@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from tests.attention_util import Batch, check, check_lse
+from tests.attention_util import Batch, check, check_lse, stored
 from tests.gpu_util import ensure_built
 
 pytestmark = pytest.mark.gpu
@@ -85,6 +85,39 @@ def test_no_keys_and_no_queries(D, sinks):
     for rows in (out[0:2], out[off[4]:off[4] + 3], out[off[6]:]):
         assert (rows == 0).all()
     assert (lse[off[6]:] == -math.inf).all()
+
+
+@pytest.mark.parametrize("new", [[9, 30], [60, 40], [400, 300]])
+def test_widest_window_behind_queries_without_keys(new):
+    """The first query's position less the window passes 32 bits; the window leaves out no key."""
+    m = _m()
+    b = Batch([3, 25], 128, 2, 16, 5)
+    q = queries(sum(new), 4, 128, 6)
+    want = run(m, b, q, new)
+    got = run(m, b, q, new, window=2 ** 31 - 1, out=torch.full_like(want, 7.0))
+    assert torch.equal(got, want)
+    assert (want[new[0] - 1] != 0).any() and (want[-1] != 0).any()
+
+
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("new", [[1, 2], [9, 12], [25, 31], [150, 90]])
+def test_growing_scores(D, new):
+    """Each 32 tokens' keys twice as large, so that the running maximum moves in most steps, and not in all rows."""
+    m = _m()
+    b = Batch([900, 333], D, 2, 64, 11)
+    # (a scale's exponent, four bits above three of its fraction, up by one per 32 tokens, from 2^-6 on)
+    for r, length in enumerate(b.lengths):
+        for at in range(0, length, 16):
+            scales = b.cache[int(b.tables[r, at // 64]), :, at % 64 // 16, 0, 8 * D:]
+            larger = (scales & 7) | (min(1 + at // 32, 14) << 3)
+            scales.copy_(torch.where((scales & 0x7f) == 0x7f, scales, larger))
+        t = torch.arange(length)
+        b.k[r] = stored(b.cache, b.tables[r, t // 64].long() * 64 + t % 64, D)[0]
+    q = queries(sum(new), 8, D, 12)
+    out, lse = run(m, b, q, new, return_lse=True)
+    want = b.want(q, sums(new), 1 / math.sqrt(D), 0, None, 1.0, 1.0)
+    check(out, want[0], want[2])
+    check_lse(lse, want[1], want[3])
 
 
 def test_empty_batches():

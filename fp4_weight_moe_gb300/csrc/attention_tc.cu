@@ -348,47 +348,48 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   } else if (warp >= C::kSoftWarps) {
     // decode: a unit is 32 values of a token
     regs_dec<C::kDecRegs>();
-    constexpr int kParts = D / 32, kUnits = kTok * kParts, kDecThreads = 32 * C::kDecWarps;
+    constexpr int kParts = D / 32, kDecThreads = 32 * C::kDecWarps;
     const int tid = threadIdx.x - 32 * C::kSoftWarps;
-    uint32_t half = 0;
+    // a thread's units are kDecThreads / kParts tokens apart, a multiple of 16:
+    // the same place in other blocks
+    constexpr int kApart = kDecThreads / kParts;
+    static_assert(kApart % 16 == 0 && kTok % kApart == 0, "units");
+    const int tok = tid / kParts, part = tid % kParts;
+    // its chunks in an order that puts a quarter warp's on banks of their own
+    const int turn = D == 64 ? 0 : D == 128 ? 2 * (part / 2) : part / 2;
+    const int from = (tok / 16) * cache_half_bytes(D) + (tok % 16) * (D / 2) + part * 16;
+    const int scales = (tok / 16) * cache_half_bytes(D) + 8 * D + (tok % 16) * (D / 16) + part * 2;
+    const uint32_t first = turn & 2 ? 0x3232 : 0x1010;
+    const int to = (part / 2) * C::kPanel + tok * 128, chunk = (4 * (part % 2)) ^ turn ^ (tok & 7);
+    uint32_t s = 0, phase = 0, half = 0;
     bool ok = true;
     while (ok && left > 0) {
       const int steps = attn_take(c, left);
       for (int i = 0; ok && i < 2 * steps; ++i, ++half) {
-        const uint32_t s = half % C::kRaw, step = half >> 1, kind = half & 1, buf = 2 * kind + (step & 1), round = step >> 1;
-        ok = wait(&raw_full[s], half / C::kRaw);
+        const uint32_t step = half >> 1, kind = half & 1, buf = 2 * kind + (step & 1), round = step >> 1;
+        ok = wait(&raw_full[s], phase);
         if (ok && round > 0) ok = wait(&kv_empty[buf], round - 1);
         if (!ok) break;
         const uint8_t* src = raw + s * C::kHalf;
-        uint8_t* dst = (kind ? v_smem : k_smem) + (step & 1) * C::kKv;
-        const uint32_t wrong = kind ? 0 : bad_blocks[s];
+        uint8_t* dst = (kind ? v_smem : k_smem) + (step & 1) * C::kKv + to;
+        const uint32_t wrong = kind ? 0 : bad_blocks[s] >> (tok / 16);
 #pragma unroll
-        for (int x = 0; x < kUnits / kDecThreads; ++x) {
-          const int unit = tid + x * kDecThreads, tok = unit / kParts, part = unit % kParts;
-          const uint8_t* block = src + (tok / 16) * cache_half_bytes(D);
-          uint4 w = *reinterpret_cast<const uint4*>(block + (tok % 16) * (D / 2) + part * 16);
-          uint32_t sb = *reinterpret_cast<const uint16_t*>(block + 8 * D + (tok % 16) * (D / 16) + part * 2);
-          if (wrong >> (tok / 16) & 1u) sb = 0x7f7fu;
+        for (int x = 0; x < kTok / kApart; ++x) {
+          const uint8_t* block = src + x * (kApart / 16) * cache_half_bytes(D);
+          uint2 a = *reinterpret_cast<const uint2*>(block + from + (turn & 2 ? 8 : 0));
+          uint2 b = *reinterpret_cast<const uint2*>(block + from + (turn & 2 ? 0 : 8));
+          uint32_t sb = *reinterpret_cast<const uint16_t*>(block + scales);
+          if (wrong >> (x * (kApart / 16)) & 1u) sb = 0x7f7fu;
           uint32_t s2;
           asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s2) : "h"((uint16_t)sb));
           if (kind) asm("min.f16x2 %0, %0, %1;" : "+r"(s2) : "r"(0x5f005f00u));  // (a value's NaN scale counts as 448)
-          uint32_t s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
-          // the chunks in an order that puts a quarter warp's on banks of their own
-          const int turn = D == 64 ? 0 : D == 128 ? 2 * (part / 2) : part / 2;
-          if (turn & 2) {
-            uint32_t t = w.x;
-            w.x = w.z, w.z = t, t = w.y, w.y = w.w, w.w = t, t = s0, s0 = s1, s1 = t;
-          }
-          if (turn & 1) {
-            uint32_t t = w.x;
-            w.x = w.y, w.y = t, t = w.z, w.z = w.w, w.w = t;
-          }
-          uint8_t* row = dst + (part / 2) * C::kPanel + tok * 128;
-          const int chunk = (4 * (part % 2)) ^ turn ^ (tok & 7);
-          *reinterpret_cast<uint4*>(row + ((chunk ^ 0) << 4)) = e2m1x8_scaled_f16(w.x, s0);
-          *reinterpret_cast<uint4*>(row + ((chunk ^ 1) << 4)) = e2m1x8_scaled_f16(w.y, s0);
-          *reinterpret_cast<uint4*>(row + ((chunk ^ 2) << 4)) = e2m1x8_scaled_f16(w.z, s1);
-          *reinterpret_cast<uint4*>(row + ((chunk ^ 3) << 4)) = e2m1x8_scaled_f16(w.w, s1);
+          const uint32_t s0 = __byte_perm(s2, s2, first), s1 = __byte_perm(s2, s2, first ^ 0x2222);
+          if (turn & 1) a = make_uint2(a.y, a.x), b = make_uint2(b.y, b.x);
+          uint8_t* row = dst + x * kApart * 128;
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 0) << 4)) = e2m1x8_scaled_f16(a.x, s0);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 1) << 4)) = e2m1x8_scaled_f16(a.y, s0);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 2) << 4)) = e2m1x8_scaled_f16(b.x, s1);
+          *reinterpret_cast<uint4*>(row + ((chunk ^ 3) << 4)) = e2m1x8_scaled_f16(b.y, s1);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -396,6 +397,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           mbar_arrive(&raw_empty[s]);
           mbar_arrive(&kv_full[buf]);
         }
+        if (++s == C::kRaw) s = 0, phase ^= 1;
       }
       left -= steps;
       if (ok && left > 0) c.next(p);

@@ -117,7 +117,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
 
   const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
   const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);  // blocks of a page
-  int round = 0;  // copies of this warp so far: stage round % S, phase round / S
+  // the stages that the next copy fills and the next pair is read from, and the phase of that
+  int fill = 0, stage = 0;
+  uint32_t phase = 0;
   bool alive = true;
 
   while (u < u_end) {
@@ -133,34 +135,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     const int first = span.first + from + member, end_pair = span.first + to;
     const int count = alive && first < end_pair ? (end_pair - first + team - 1) / team : 0;
     const int32_t* table = p.a.tables + (int64_t)r * p.a.table_row;
-    int page_even = 0, page_odd = 0;  // of 32 pairs' blocks: lane i's those of pair first + (i + 32 k) team
-    unsigned bad_blocks = 0;          // of the copies in flight: two bits per stage
+    // of 32 pairs at a time, a lane each: where it lies, the page of its odd
+    // block (pages of one block), and which blocks' pages there are not
+    const uint8_t* src = cache;
+    int odd = 0;
+    unsigned bad_even = 0, bad_odd = 0;
+    unsigned bad_blocks = 0;  // of the copies in flight: two bits per stage
     auto load = [&](int i) {
       if ((i & 31) == 0) {
         const int b = 2 * (first + (i + lane) * team);
-        page_even = b < end_block ? table[b >> blocks_log] : 0;
-        page_odd = blocks_log == 0 && b + 1 < end_block ? table[b + 1] : page_even;
+        int even = b < end_block ? table[b >> blocks_log] : 0;
+        odd = blocks_log == 0 && b + 1 < end_block ? table[b + 1] : even;
+        const bool bad0 = (unsigned)even >= (unsigned)p.a.pages, bad1 = (unsigned)odd >= (unsigned)p.a.pages;
+        bad_even = __ballot_sync(0xffffffffu, bad0), bad_odd = __ballot_sync(0xffffffffu, bad1);
+        even = bad0 ? 0 : even, odd = bad1 ? 0 : odd;
+        src = cache + ((((int64_t)even * p.a.Hkv + head) << blocks_log) + (b & ((1 << blocks_log) - 1))) * cache_block_bytes(D);
       }
-      const int pair = first + i * team, stage = (round + i) % S;
-      const int even = __shfl_sync(0xffffffffu, page_even, i & 31), odd = __shfl_sync(0xffffffffu, page_odd, i & 31);
-      const bool bad0 = (unsigned)even >= (unsigned)p.a.pages, bad1 = (unsigned)odd >= (unsigned)p.a.pages;
-      bad_blocks = (bad_blocks & ~(3u << (2 * stage))) | (((bad0 ? 1u : 0u) | (bad1 ? 2u : 0u)) << (2 * stage));
-      if (lane == 0) {
-        uint8_t* dst = ring + stage * C::kStageBytes;
-        const int64_t heads = p.a.Hkv;
-        const int in_page = (2 * pair) & ((1 << blocks_log) - 1);
-        const uint8_t* src = cache + ((((bad0 ? 0 : (int64_t)even) * heads + head) << blocks_log) + in_page) * cache_block_bytes(D);
-        const int blocks = min(end_block - 2 * pair, 2);
-        mbar_arrive_expect_tx(&full[stage], blocks * cache_block_bytes(D));
+      if ((bad_even | bad_odd | bad_blocks) != 0)
+        bad_blocks = (bad_blocks & ~(3u << (2 * fill))) |
+                     (((bad_even >> (i & 31) & 1u) | (bad_odd >> (i & 31) & 1u) << 1) << (2 * fill));
+      if (lane == (i & 31)) {
+        uint8_t* dst = ring + fill * C::kStageBytes;
+        const int blocks = min(end_block - 2 * (first + i * team), 2);
+        mbar_arrive_expect_tx(&full[fill], blocks * cache_block_bytes(D));
         if (blocks_log > 0) {  // the two lie together
-          bulk_load(dst, src, blocks * cache_block_bytes(D), &full[stage]);
+          bulk_load(dst, src, blocks * cache_block_bytes(D), &full[fill]);
         } else {
-          bulk_load(dst, src, cache_block_bytes(D), &full[stage]);
+          bulk_load(dst, src, cache_block_bytes(D), &full[fill]);
           if (blocks == 2)
-            bulk_load(dst + cache_block_bytes(D), cache + ((bad1 ? 0 : (int64_t)odd) * heads + head) * cache_block_bytes(D),
-                      cache_block_bytes(D), &full[stage]);
+            bulk_load(dst + cache_block_bytes(D), cache + ((int64_t)odd * p.a.Hkv + head) * cache_block_bytes(D),
+                      cache_block_bytes(D), &full[fill]);
         }
       }
+      fill = fill + 1 == S ? 0 : fill + 1;
     };
     int loaded = 0;
     for (; loaded < min(S - 1, count); ++loaded) load(loaded);
@@ -224,8 +231,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
 
     for (int i = 0; i < count; ++i) {
       if (loaded < count) load(loaded++);  // (into the stage of pair i - 1)
-      const int stage = (round + i) % S;
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], ((round + i) / S) & 1, &g_attention_status, kWaitCode))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, &g_attention_status, kWaitCode))) {
         alive = false;
         break;
       }
@@ -402,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         }
       }
       __syncwarp();  // the pair is read: its stage may be loaded anew
+      if (++stage == S) stage = 0, phase ^= 1;
     }
-    round += count;
 
     // the warps' sums, joined
 #pragma unroll

@@ -18,11 +18,11 @@
 // banks.  q is scaled by a power of two per row into FP16's range.
 //
 // Bound by the cache's bytes (0.56 of a byte a value, each read once for a
-// group of up to 16 rows) and by the 650 or so instructions that a warp takes
+// group of up to 16 rows) and by the 600 or so instructions that a warp takes
 // for 32 tokens of 128 columns, which take as long: of 64 requests' 440 MB the
-// copies alone take 76 us, the arithmetic alone 76, both 97 (4.5 TB/s), and
-// the join of the shared items 8 (the counters: 57% of the issue slots, half
-// of the ALU's, 52% of the memory's time).  Six of ten instructions turn
+// copies alone take 76 us, the whole call 100 (4.4 TB/s), 8 of them the join of
+// shared items (the counters: 57% of the issue slots, half of the ALU's, 52%
+// of the memory's time).  Six of ten instructions turn
 // codes into FP16 and scale them, which FP16's products need and the values'
 // 8-bit forms would not carry exactly.
 #include "attention_work.cuh"
@@ -109,16 +109,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
   pdl_wait();
   pdl_launch_dependents();
 
-  AttnCursor<kRows, kPair, kWholePairs> c;
+  // each warp's place in its stretch (in shared memory: registers are worth more to the loop)
+  __shared__ AttnCursor<kRows, kPair, kWholePairs> cursors[kWarps];
+  AttnCursor<kRows, kPair, kWholePairs>& c = cursors[warp];
   int64_t u, u_end;
   int team;
-  if (!attn_stretch<kRows, kPair, kThreads, kWarps, kTeamSpan>(p, c, u, u_end, team)) return;
+  {
+    AttnCursor<kRows, kPair, kWholePairs> start;
+    if (!attn_stretch<kRows, kPair, kThreads, kWarps, kTeamSpan>(p, start, u, u_end, team)) return;
+    if (lane == 0) c = start;
+    __syncwarp();
+  }
   const int member = team == 1 ? 0 : warp, worker = team == 1 ? (int)blockIdx.x * kWarps + warp : (int)blockIdx.x;
 
   const uint8_t* cache = static_cast<const uint8_t*>(p.a.cache);
   const int blocks_log = 31 - __clz(p.a.page_size / kCacheBlock);  // blocks of a page
-  // the stages that the next copy fills and the next pair is read from, and the phase of that
-  int fill = 0, stage = 0;
+  int stage = 0;  // that the next pair is read from, and its phase
   uint32_t phase = 0;
   bool alive = true;
 
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     int odd = 0;
     unsigned bad_even = 0, bad_odd = 0;
     unsigned bad_blocks = 0;  // of the copies in flight: two bits per stage
-    auto load = [&](int i) {
+    auto load = [&](int i, int fill) {
       if ((i & 31) == 0) {
         const int b = 2 * (first + (i + lane) * team);
         int even = b < end_block ? table[b >> blocks_log] : 0;
@@ -167,10 +173,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
                       cache_block_bytes(D), &full[fill]);
         }
       }
-      fill = fill + 1 == S ? 0 : fill + 1;
     };
-    int loaded = 0;
-    for (; loaded < min(S - 1, count); ++loaded) load(loaded);
+    for (int i = 0; i < min(S - 1, count); ++i) load(i, stage + i < S ? stage + i : stage + i - S);
 
     // q, in the operand's order, and the rows' factors
     uint32_t qf[NT][kSteps][2];
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     }
 
     for (int i = 0; i < count; ++i) {
-      if (loaded < count) load(loaded++);  // (into the stage of pair i - 1)
+      if (i + S - 1 < count) load(i + S - 1, stage == 0 ? S - 1 : stage - 1);  // (the stage of pair i - 1)
       if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, &g_attention_status, kWaitCode))) {
         alive = false;
         break;
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
           if (p.a.lse && g == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;
         }
       __syncwarp();
-      if (u < u_end) c.next(p);
+      if (u < u_end) attn_next(p, c);
       continue;
     }
     float* sums = reinterpret_cast<float*>(ring);
@@ -504,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     }
     fence_proxy_async_smem();  // the sums lie where the next copies go
     __syncthreads();
-    if (u < u_end) c.next(p);
+    if (u < u_end) attn_next(p, c);
   }
 }
 
@@ -531,7 +535,7 @@ template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
   // Rows that an average request has to a key head.  Up to 8 fill one product
   // of 8 columns and up to 16 two (16 requests of 16384 tokens, some four
-  // queries of four heads each: 98 us; on tiles of 128 rows, whose decoding
+  // queries of four heads each: 96 us; on tiles of 128 rows, whose decoding
   // warps bring 2.9 TB/s, 180).
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
   if (rows > 16) return launch_attention_tc(p, (int)rows, sms, st);

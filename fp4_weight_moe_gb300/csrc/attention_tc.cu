@@ -26,7 +26,8 @@
 // products (1090), of which two tiles hide one another's in part: the tensor
 // cores are busy 47% of the time (chunks of 2048 tokens behind 8192, 32 query
 // heads, D = 128: 586 us, 1.06 PFLOP/s).  With one tile by the decode warps,
-// 900 cycles for half a step (35 rows of five requests of 100000 tokens 257 us).
+// 900 cycles for half a step, and by issue (35 rows of five requests of 100000
+// tokens 250 us).
 //
 // The maximum follows the scores only when they outgrow it by 2^8 (p stays
 // within FP16, sums and divisor are taken against the same m), so that the
@@ -209,7 +210,10 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   {
     int64_t u, u_end;
     int team;
-    if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, c, u, u_end, team)) return;
+    AttnCursor<C::kRows, kTok, 2> start;
+    if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, start, u, u_end, team)) return;
+    if (lane == 0) c = start;
+    __syncwarp();
     left = (int)(u_end - u);
   }
 
@@ -262,7 +266,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           if (!ok) break;
         }
         left -= steps;
-        if (left > 0) c.next(p);
+        if (left > 0) attn_next(p, c);
       }
     } else if (warp == C::kMmaWarp) {
       const uint32_t idesc_s = idesc_f16(128, kTok), idesc_o = idesc_f16(128, D) | (1u << 16);
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         }
         ++item;
         left -= steps;
-        if (ok && left > 0) c.next(p);
+        if (ok && left > 0) attn_next(p, c);
       }
     }
   } else if (warp >= C::kSoftWarps) {
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         if (++s == C::kRaw) s = 0, phase ^= 1;
       }
       left -= steps;
-      if (ok && left > 0) c.next(p);
+      if (ok && left > 0) attn_next(p, c);
     }
   } else {
     regs_inc<C::kSoftRegs>();
@@ -669,7 +673,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       if (kSides == 2) rows_sync<kSides>(id);  // (the next queries go over both sides' place)
       ++item;
       left -= steps;
-      if (left > 0) c.next(p);
+      if (left > 0) attn_next(p, c);
     }
   }
   tc_fence_before();

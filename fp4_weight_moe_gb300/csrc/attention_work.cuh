@@ -321,6 +321,14 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
   return true;
 }
 
+// The next item of a cursor in shared memory, which is a warp's own.
+template <int kRows, int kUnit, int kWhole>
+__device__ __forceinline__ void attn_next(const AttnArgs& p, AttnCursor<kRows, kUnit, kWhole>& c) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) c.next(p);
+  __syncwarp();
+}
+
 // The units of the cursor's item that are this worker's, of a stretch of `left`.
 template <int kRows, int kUnit, int kWhole>
 __device__ __forceinline__ int attn_take(const AttnCursor<kRows, kUnit, kWhole>& c, int64_t left) {

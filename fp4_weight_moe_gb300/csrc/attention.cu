@@ -22,9 +22,9 @@
 // for 32 tokens of 128 columns, which take as long: of 64 requests' 440 MB the
 // copies alone take 76 us, the whole call 100 (4.4 TB/s), 8 of them the join of
 // shared items (the counters: 57% of the issue slots, half of the ALU's, 52%
-// of the memory's time).  Six of ten instructions turn
-// codes into FP16 and scale them, which FP16's products need and the values'
-// 8-bit forms would not carry exactly.
+// of the memory's time).  Half of the instructions turn codes into FP16 and
+// scale them: products of 8-bit operands would not carry a code times its
+// scale exactly.
 #include "attention_work.cuh"
 #include "host.cuh"
 #include "tcgen05.cuh"
@@ -141,9 +141,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     const int first = span.first + from + member, end_pair = span.first + to;
     const int count = alive && first < end_pair ? (end_pair - first + team - 1) / team : 0;
     const int32_t* table = p.a.tables + (int64_t)r * p.a.table_row;
-    // of 32 pairs at a time, a lane each: where it lies, the page of its odd
-    // block (pages of one block), and which blocks' pages there are not
-    const uint8_t* src = cache;
+    // of 32 pairs at a time, a lane each: which block of the cache it is (memory
+    // holds fewer than 2^32), the page of its odd block (pages of one block), and
+    // which blocks' pages there are not
+    uint32_t at_block = 0;
     int odd = 0;
     unsigned bad_even = 0, bad_odd = 0;
     unsigned bad_blocks = 0;  // of the copies in flight: two bits per stage
@@ -155,13 +156,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         const bool bad0 = (unsigned)even >= (unsigned)p.a.pages, bad1 = (unsigned)odd >= (unsigned)p.a.pages;
         bad_even = __ballot_sync(0xffffffffu, bad0), bad_odd = __ballot_sync(0xffffffffu, bad1);
         even = bad0 ? 0 : even, odd = bad1 ? 0 : odd;
-        src = cache + ((((int64_t)even * p.a.Hkv + head) << blocks_log) + (b & ((1 << blocks_log) - 1))) * cache_block_bytes(D);
+        at_block = (((uint32_t)even * p.a.Hkv + head) << blocks_log) + (b & ((1 << blocks_log) - 1));
       }
       if ((bad_even | bad_odd | bad_blocks) != 0)
         bad_blocks = (bad_blocks & ~(3u << (2 * fill))) |
                      (((bad_even >> (i & 31) & 1u) | (bad_odd >> (i & 31) & 1u) << 1) << (2 * fill));
       if (lane == (i & 31)) {
         uint8_t* dst = ring + fill * C::kStageBytes;
+        const uint8_t* src = cache + (int64_t)at_block * cache_block_bytes(D);
         const int blocks = min(end_block - 2 * (first + i * team), 2);
         mbar_arrive_expect_tx(&full[fill], blocks * cache_block_bytes(D));
         if (blocks_log > 0) {  // the two lie together
@@ -236,6 +238,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
     for (int i = 0; i < count; ++i) {
       if (i + S - 1 < count) load(i + S - 1, stage == 0 ? S - 1 : stage - 1);  // (the stage of pair i - 1)
       if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase, &g_attention_status, kWaitCode))) {
+        // (the other copies on their way end before the CTA does)
+        for (int x = i + 1; x < min(i + S, count); ++x) {
+          if (++stage == S) stage = 0, phase ^= 1;
+          mbar_wait(&full[stage], phase, &g_attention_status, kWaitCode);
+        }
         alive = false;
         break;
       }

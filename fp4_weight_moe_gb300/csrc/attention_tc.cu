@@ -25,7 +25,7 @@
 // tokens: 640 instructions a warp, between waits on tensor memory) and its two
 // products (1090), of which two tiles hide one another's in part: the tensor
 // cores are busy 47% of the time (chunks of 2048 tokens behind 8192, 32 query
-// heads, D = 128: 586 us, 1.06 PFLOP/s).  With one tile by the decode warps,
+// heads, D = 128: 578 us, 1.07 PFLOP/s).  With one tile by the decode warps,
 // 900 cycles for half a step, and by issue (35 rows of five requests of 100000
 // tokens 250 us).
 //
@@ -268,6 +268,8 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         left -= steps;
         if (left > 0) attn_next(p, c);
       }
+      // (whoever gave up: the copies on their way end before the CTA does)
+      for (uint32_t h = half > C::kRaw ? half - C::kRaw : 0; h < half; ++h) wait(&raw_full[h % C::kRaw], h / C::kRaw);
     } else if (warp == C::kMmaWarp) {
       const uint32_t idesc_s = idesc_f16(128, kTok), idesc_o = idesc_f16(128, D) | (1u << 16);
       uint32_t step = 0;         // over all items

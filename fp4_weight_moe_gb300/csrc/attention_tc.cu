@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   uint64_t* p_full = s_full + 2;    // [2] probabilities are
   uint64_t* pv_done = p_full + 2;   // [2] sums of a tile are
   uint64_t* q_full = pv_done + 2;   // [2] a tile's queries are there, and its sums read
-  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(q_full + 2);  // [kRaw]
+  uint64_t* item_done = q_full + 2;  // all sums of an item are (with one tile)
+  uint32_t* bad_blocks = reinterpret_cast<uint32_t*>(item_done + 1);  // [kRaw]
   uint32_t* tmem_slot = bad_blocks + C::kRaw;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -193,6 +194,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       mbar_init(&pv_done[i], 1);
       mbar_init(&q_full[i], 4 * C::kSides);
     }
+    mbar_init(item_done, 1);
     fence_mbar_init();
   }
   pdl_wait();
@@ -336,6 +338,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
             if (ok) ok = wait(&kv_full[2 + (step & 1)], step >> 1);
             if (!ok) break;
             sums(0, step, buffer, i == 0);
+            if (i + 1 == steps) mma_commit_warp(item_done);
             mma_commit_warp(&kv_empty[2 + (step & 1)]);
             if (i + 2 < steps) {
               const uint32_t at = step + 2;
@@ -597,13 +600,14 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           break;
         }
       }
-      // (the last scores come before the last two sums where buffers alternate,
-      // and a wait for a phase is met by the one two before it: both, in order)
-      if (kTiles == 1 && steps > 1 && ok) ok = wait(&pv_done[n], step - 2);
+      // (With one tile the last scores come before the last two sums.  Of those
+      // neither can be waited for by its phase: a wait for the last is met by the
+      // one two before it, and one for the last but one is not met once the last
+      // is done too.  So an item has a barrier of its own.)
       if (kSides == 1) {
         if (!ok || !wait(&pv_done[n], step - 1)) break;
       } else {
-        if (ok) ok = wait(&pv_done[n], step - 1);
+        if (ok) ok = wait(item_done, item);
         told[side_of][tile_row] = l.x + l.y;
         if (rows_any<kSides>(id, !ok)) break;
       }

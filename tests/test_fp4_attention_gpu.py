@@ -120,6 +120,22 @@ def test_growing_scores(D, new):
     check_lse(lse, want[1], want[3])
 
 
+@pytest.mark.parametrize("D", DIMS)
+@pytest.mark.parametrize("new", [[5] * 16, [8, 3, 6, 7] * 4, [31] * 16])
+def test_many_items_to_a_worker_again_and_again(D, new):
+    """Every item's end is waited for, however late a warp comes to it: no wait gives up in many calls."""
+    m = _m()
+    b = Batch([1500 + 37 * i for i in range(16)], D, 2, 32, 13)
+    q = queries(sum(new), 8, D, 14)
+    args = (q.cuda(), b.cache.cuda(), b.tables.cuda(), ints(b.lengths), ints(sums(new)))
+    outs = [m.fp4_attention(*args) for _ in range(60)]
+    assert m.fp4_attention_status() == 0
+    want = b.want(q, sums(new), 1 / math.sqrt(D), 0, None, 1.0, 1.0)
+    check(outs[0], want[0], want[2])
+    for out in outs[1:]:
+        assert torch.equal(out, outs[0])
+
+
 def test_empty_batches():
     m = _m()
     cache = m.alloc_fp4_cache(2, 16, 2, 64)

@@ -21,8 +21,9 @@ constexpr int kStepThreads = 1024;
 // Pages that a lane takes for its request by itself (512 requests of two pages
 // each, a warp to one after the other: 14 us of the step's 15).
 constexpr int kFew = 4;
-// Tokens that the one CTA places itself.
-constexpr int kStepTokens = 4 * kStepThreads;
+// Tokens that the one CTA places itself (64 tokens 3.4 us, with a second launch
+// 4.8; 512 requests of up to 2 tokens 6.4 and 7.8, of up to 8 9.4 and 8.4).
+constexpr int kStepTokens = 2 * kStepThreads;
 
 struct Sums {
   int fresh, back, need;

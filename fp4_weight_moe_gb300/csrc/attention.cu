@@ -3,7 +3,8 @@
 //
 //   x_j = scale k_scale q . k_j,  out = v_scale sum_j e^(x_j - m) v_j / sum_j e^(x_j - m)
 //
-// in one pass over the cache with a running maximum m (in units of log 2).
+// in one pass over the cache, against an m that follows the maximum (in units
+// of log 2; kBelow, attention_work.cuh).
 //
 // Every warp streams blocks of 16 tokens of its own (keys and values of a head
 // lie together: one bulk copy of 18 D bytes each) through a ring in shared
@@ -325,14 +326,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
               if (!(j <= pos && (p.a.window == 0 || j > pos - p.a.window))) s[b][n][e] = -INFINITY;
             }
       }
-      // the maximum follows when a score outgrows it by 2^8
+      // m follows when a score outgrows it by 2^kMost
       float top[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c2 = 0; c2 < 2; ++c2) {
           top[n][c2] = fmaxf(fmaxf(s[0][n][c2], s[0][n][c2 + 2]), fmaxf(s[1][n][c2], s[1][n][c2 + 2]));
-          grows = grows || top[n][c2] > m[n][c2] + 8.f;
+          grows = grows || top[n][c2] > m[n][c2] + kMost;
         }
       if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
           for (int c2 = 0; c2 < 2; ++c2) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) top[n][c2] = fmaxf(top[n][c2], __shfl_xor_sync(0xffffffffu, top[n][c2], x));
-            const float next = fmaxf(m[n][c2], top[n][c2]);
+            const float next = fmaxf(m[n][c2], top[n][c2] - kBelow);
             const float by = next == -INFINITY ? 1.f : exp2_approx(m[n][c2] - next);
             m[n][c2] = next;
             minus[n][c2] = next == -INFINITY ? 0.f : -next;

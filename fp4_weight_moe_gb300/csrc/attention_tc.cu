@@ -6,7 +6,7 @@
 //   softmax warps  (four or eight per tile of rows) own a row, or half of its
 //                  columns, per thread: they bring q to shared memory as FP16,
 //                  scaled by a power of two per row; read a step's scores from
-//                  tensor memory, take the running maximum, and put p =
+//                  tensor memory, follow their maximum, and put p =
 //                  2^(x - m) back over them in FP16, the second product's A
 //                  operand; at the end they read the sums and write the rows;
 //   decode warps   turn the cache's codes into FP16 (exact: at most six
@@ -29,9 +29,9 @@
 // 900 cycles for half a step, and by issue (35 rows of five requests of 100000
 // tokens 250 us).
 //
-// The maximum follows the scores only when they outgrow it by 2^8 (p stays
-// within FP16, sums and divisor are taken against the same m), so that the
-// sums in tensor memory are hardly ever rescaled.
+// m follows the scores only when they outgrow it by 2^kMost, to 2^kBelow below
+// them (p stays within FP16, sums and divisor are taken against the same m), so
+// that the sums in tensor memory are hardly ever rescaled.
 #include "attention_work.cuh"
 #include "gemm_f16w4.cuh"
 #include "gemm_fp8.cuh"
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           float top = max3(fmaxf(tops[0], tops[1]), tops[2], tops[3]) * fac;
           // (m -inf: as soon as there is a key; and behind it both have read their scores, over which p goes)
           if (kSides == 2) tc_fence_before();
-          bool grows = top > m + 8.f;
+          bool grows = top > m + kMost;
           const bool any = rows_any<kSides>(id, grows);
           if (kSides == 2) tc_fence_after();
           if (!any || pass > 0) break;
@@ -563,10 +563,10 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
             told[side_of][tile_row] = top;
             rows_sync<kSides>(id);
             top = fmaxf(told[0][tile_row], told[1][tile_row]);
-            grows = top > m + 8.f;
+            grows = top > m + kMost;
           }
-          const float by = grows ? exp2_approx(m - top) : 1.f;
-          if (grows) m = top;
+          const float next = grows ? top - kBelow : m, by = grows ? exp2_approx(m - next) : 1.f;
+          m = next;
           l.x *= by;
           l.y *= by;
           if (i > 0) {

@@ -337,6 +337,15 @@ __device__ __forceinline__ int attn_take(const AttnCursor<kRows, kUnit, kWhole>&
 
 // ---------------------------------------------------------------- pieces of the kernels
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A row's probabilities are 2^(x - m) in FP16 (x in units of log 2).  m moves
+// when a score outgrows it by kMost, to kBelow below that score: they stay
+// within FP16's 65504, and the largest is at least 2^kBelow, so that what FP16
+// rounds below its normal range is off by 2^-25 beside that, 2^-32 of the
+// largest.  (Against the largest itself, the many weak keys beside a strong one
+// of zero value lost a quarter of their weight at 18 units of e below it.)  m
+// lags by up to kMost - kBelow: with 8 chunks of 2048 tokens behind 8192 take
+// 583 us, with 4, which moves the sums more often, 745.
+constexpr float kBelow = 7.f, kMost = 15.f;
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

@@ -856,8 +856,9 @@ MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, 
  * page_size are not looked for.
  * Queries, 4-bit keys and values enter the products exactly (q in FP16
  * scaled by a power of two per row: exact to 2^-39 of the row's largest),
- * the probabilities in FP16; sums, maxima and divisors are FP32.  Results are
- * deterministic for given inputs and device.
+ * the probabilities in FP16, each off by 2^-11 of itself or, if that is more,
+ * by 2^-32 of the row's largest; sums, maxima and divisors are FP32.  Results
+ * are deterministic for given inputs and device.
  * q and out: bf16 [T][Hq][D], 16-byte aligned, strides multiples of 8
  * elements (MOE_FP4_EINVAL); Hq % Hkv == 0, Hq / Hkv <= 64, R <= 65536,
  * table_width * page_size <= 2^31 - 1024, T * Hq < 2^31

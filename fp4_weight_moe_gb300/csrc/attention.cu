@@ -304,8 +304,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
         }
       }
 
-      // scores in units of log 2, masked
-      const bool whole = tok0 >= all_lo && tok0 + kPair - 1 <= pos_first;
+      // scores in units of log 2, masked (the item's last pair may be the table's
+      // end, of which the request has tokens behind: looked for in the mask
+      // only, as the loop's registers are full)
+      const bool whole = tok0 >= all_lo && tok0 + kPair - 1 <= pos_first && (i + 1 < count || to < span.units);
       const unsigned bad = (bad_blocks >> (2 * stage)) & 3u;
       bool grows = false;
 #pragma unroll
@@ -323,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
             for (int e = 0; e < 4; ++e) {
               const int j = tok0 + kCacheBlock * b + row_token(g + 8 * (e >> 1)), pos = last[n][e & 1];
               if (bad >> b & 1u) s[b][n][e] = NAN;
-              if (!(j <= pos && (p.a.window == 0 || j > pos - p.a.window))) s[b][n][e] = -INFINITY;
+              // (a table ends at a block's end)
+              if (tok0 + kCacheBlock * b >= p.capacity || !(j <= pos && (p.a.window == 0 || j > pos - p.a.window)))
+                s[b][n][e] = -INFINITY;
             }
       }
       // m follows when a score outgrows it by 2^kMost

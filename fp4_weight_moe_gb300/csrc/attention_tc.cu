@@ -479,14 +479,14 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         if (lane == 0) mbar_arrive(&q_full[n]);
       }
       int pos, lowest;          // the row's position, the first token that it sees
-      int whole_lo, whole_hi;   // tokens that every row of the tile sees
+      int whole_lo, whole_hi;   // tokens that every row of the tile sees (none past the table, as in the masks)
       {
         const int rows = c.rows(p), base_pos = c.q.length - c.q.n;
         pos = tile_row < rows ? base_pos + attn_row(p, tile_rows, tile_row).query : -1;
         lowest = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
         const int pos_last = base_pos + attn_row(p, tile_rows, min(128 * n + 128, rows) - 1).query;
         whole_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
-        whole_hi = base_pos + attn_row(p, tile_rows, 128 * n).query;
+        whole_hi = min(base_pos + attn_row(p, tile_rows, 128 * n).query, p.capacity - 1);
       }
 
       const int warp_rows = c.rows(p);
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
         if (tok0 < whole_lo || tok0 + kTok - 1 > whole_hi) {
           // masked where they are, so that the loop below has no test for it
           // (as predicates there, they took as many instructions as the rest)
-          const int hi = pos - tok0 - col0, lo = lowest - tok0 - col0;
+          const int hi = min(pos, p.capacity - 1) - tok0 - col0, lo = lowest - tok0 - col0;
 #pragma unroll 1
           for (int x = 0; x < C::kCols; x += 16) {
             uint32_t s[16];

@@ -365,9 +365,10 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// The power of two that brings a row's largest |q| to [2^14, 2^15), and its inverse.
+// The power of two that brings a row's largest |q| to [2^14, 2^15) (one below
+// 2^-112 less far, as the power is an FP32 number), and its inverse.
 __device__ __forceinline__ float row_scale(float top, float& back) {
-  const int e = min(max((int)((__float_as_uint(top) >> 23) & 0xff) - 127 - 14, -100), 100);
+  const int e = max((int)((__float_as_uint(top) >> 23) & 0xff) - 127 - 14, -126);
   back = __uint_as_float((uint32_t)(127 + e) << 23);
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }

@@ -855,7 +855,8 @@ MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, 
  * number outside [0, pages) reads as NaN keys.  Tokens past table_width *
  * page_size are not looked for.
  * Queries, 4-bit keys and values enter the products exactly (q in FP16
- * scaled by a power of two per row: exact to 2^-39 of the row's largest),
+ * scaled by a power of two per row: exact to 2^-39 of the row's largest, or
+ * to 2^-151 where that is below 2^-112),
  * the probabilities in FP16, each off by 2^-11 of itself or, if that is more,
  * by 2^-32 of the row's largest; sums, maxima and divisors are FP32.  Results
  * are deterministic for given inputs and device.

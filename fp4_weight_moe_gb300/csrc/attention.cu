@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
           const AttnRows rr = attn_row(p, tile_rows, row);
           const int token = q.row0 + rr.query, hq = head * p.group + rr.head;
           float lse;
-          const float inv = attn_finish(p, hq, m[n][c2], l[n][c2], lse);
+          const float inv = attn_finish(p, hq, base_pos + rr.query, m[n][c2], l[n][c2], lse);
           __nv_bfloat16* dst = attn_out(p, token, hq) + g * (D / 8);
 #pragma unroll
           for (int j = 0; j < kSteps; j += 4)
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attention_rows_ke
       const AttnRows rr = attn_row(p, tile_rows, row);
       const int token = q.row0 + rr.query, hq = head * p.group + rr.head;
       float lse;
-      const float inv = attn_finish(p, hq, top, sum, lse);
+      const float inv = attn_finish(p, hq, base_pos + rr.query, top, sum, lse);
       *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
           make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
       if (p.a.lse && d == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;

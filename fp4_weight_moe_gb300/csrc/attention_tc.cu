@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           const AttnRows rr = attn_row(p, tile_rows, tile_row);
           const int hq = c.head * p.group + rr.head;
           float lse;
-          inv = attn_finish(p, hq, m, sum, lse);
+          inv = attn_finish(p, hq, pos, m, sum, lse);
           if (p.a.lse && side_of == 0) p.a.lse[(int64_t)(c.q.row0 + rr.query) * p.a.Hq + hq] = lse;
         } else if (side_of == 0) {
           *reinterpret_cast<float2*>(attn_stats<D, C::kRows>(p, part, tile_row)) = make_float2(m, sum);

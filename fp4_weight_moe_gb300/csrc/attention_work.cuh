@@ -27,7 +27,7 @@ struct AttnLine {
   int more, workers, grain_log;
 };
 struct AttnPlace {  // where a worker's stretch begins
-  int row0, tile, head, rows, from, units;
+  int row0, first, tile, head, rows, from, units;  // first: position of the request's first query
 };
 
 struct AttnArgs {
@@ -313,7 +313,7 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
   cursor.start(p, found[i], found_rest[i]);
   const bool passes = cursor.from > 0 && cursor.span.units <= kWhole;  // (an item that a worker before has whole)
   if (team == 1 && kTeams > 1 ? lane == 0 : threadIdx.x == 0)
-    p.places[w] = {cursor.q.row0, cursor.tile, cursor.head, cursor.rows(p), passes ? 0 : cursor.from, cursor.span.units};
+    p.places[w] = {cursor.q.row0, cursor.q.length - cursor.q.n, cursor.tile, cursor.head, cursor.rows(p), passes ? 0 : cursor.from, cursor.span.units};
   if (passes) {
     u += cursor.span.units - cursor.from;
     if (u < u_end) cursor.next(p);
@@ -373,12 +373,17 @@ __device__ __forceinline__ float row_scale(float top, float& back) {
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
+// Whether a query at this position sees a key.
+__device__ __forceinline__ bool attn_sees(const AttnArgs& p, int pos) {
+  return pos >= 0 && (p.a.window == 0 || pos - p.a.window < p.capacity - 1);
+}
+
 // A row's last step: from its maximum (units of log 2) and divisor, with the
-// sink's term, the factor of its sums, and its lse.
-__device__ __forceinline__ float attn_finish(const AttnArgs& p, int head, float top, float sum, float& lse) {
-  if (top == -INFINITY && sum == 0.f) {  // no key
+// sink's term, the factor of its sums, and its lse.  pos: its query's position.
+__device__ __forceinline__ float attn_finish(const AttnArgs& p, int head, int pos, float top, float sum, float& lse) {
+  if (top == -INFINITY && sum == 0.f) {  // no key, or scores of -inf: 0 / 0 without a sink
     lse = p.a.sinks ? p.a.sinks[head] : -INFINITY;
-    return 0.f;
+    return lse == -INFINITY && attn_sees(p, pos) ? NAN : 0.f;
   }
   float by = 1.f;
   if (p.a.sinks) {
@@ -498,7 +503,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& p, const AttnPlace& at
     const AttnRows r = attn_row(p, attn_rows(p, at.tile * kRows), row0 + row);
     const int token = at.row0 + r.query, hq = at.head * p.group + r.head;
     float lse;
-    const float inv = attn_finish(p, hq, tops[row], sums[row], lse);
+    const float inv = attn_finish(p, hq, at.first + r.query, tops[row], sums[row], lse);
     *reinterpret_cast<uint2*>(attn_out(p, token, hq) + d) =
         make_uint2(pack_bf16x2(acc[y].x * inv, acc[y].y * inv), pack_bf16x2(acc[y].z * inv, acc[y].w * inv));
     if (p.a.lse && d == 0) p.a.lse[(int64_t)token * p.a.Hq + hq] = lse;

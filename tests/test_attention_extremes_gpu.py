@@ -39,3 +39,36 @@ def test_queries_near_the_ends_of_bf16(D, new, power):
     exact = want(b, q, [0, new], scale)
     check(out, exact[0], exact[2], power)
     check_lse(lse, exact[1], exact[3], power)
+
+
+def all_keys_negative(b, r, h, column):
+    """Key head h's codes of a column of request r: all -1 (code 10) under the scales that are there, none of them 0."""
+    for page in b.tables[r, :-(-b.lengths[r] // b.page_size)].tolist():
+        for block in b.cache[page, h, :, 0]:
+            codes = block[:8 * b.D].view(16, b.D // 2)
+            codes[:, column // 2] = (codes[:, column // 2] & (0x0f if column % 2 else 0xf0)) | (0xa0 if column % 2 else 0x0a)
+            scales = block[8 * b.D:].view(16, b.D // 16)
+            scales[:, column // 16] = 0x38  # (1)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,length", [(1, 1), (1, 200), (3, 90), (10, 90), (40, 300), (1, 9000), (10, 9000), (40, 9000)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_scores_of_minus_infinity(D, new, length, sinks):
+    """A query whose scores are all -inf sees keys: 0 / 0, or, with a sink, 0; beside one that sees none."""
+    m = _m()
+    column = 37
+    b = Batch([length, 1], D, 2, 16, 2)
+    all_keys_negative(b, 0, 1, column)
+    q = torch.randn(new + 2, 8, D, generator=torch.Generator().manual_seed(3)).to(BF16)
+    q[:new, 6, column] = math.inf
+    s = torch.randn(8, generator=torch.Generator().manual_seed(4)) if sinks else None
+    out, lse = m.fp4_attention(q.cuda(), b.cache.cuda(), b.tables.cuda(), ints([length, 1]), ints([0, new, new + 2]),
+                               return_lse=True, sinks=None if s is None else s.cuda())
+    out, lse = out.float().cpu(), lse.cpu()
+    assert torch.equal(lse[:new, 6], torch.full((new,), float(s[6]) if sinks else -math.inf))
+    assert (out[:new, 6] == 0).all() if sinks else out[:new, 6].isnan().all()
+    others = torch.ones(new + 2, 8, dtype=torch.bool)
+    others[:new, 6] = False
+    assert out[others].isfinite().all()
+    assert (out[new] == 0).all() and torch.equal(lse[new], s if sinks else torch.full((8,), -math.inf))

@@ -388,6 +388,10 @@ __device__ __forceinline__ float attn_finish(const AttnArgs& p, int head, int po
   float by = 1.f;
   if (p.a.sinks) {
     const float sink = p.a.sinks[head] * kLog2e, next = fmaxf(top, sink);
+    if (sink == INFINITY && top < sink && sum == sum) {  // (all of the weight, and inf - inf below)
+      lse = p.a.sinks[head];
+      return 0.f;
+    }
     if (next != -INFINITY) {
       by = top == -INFINITY ? 1.f : exp2_approx(top - next);  // (-inf: none but NaN scores)
       sum = sum * by + exp2_approx(sink - next);

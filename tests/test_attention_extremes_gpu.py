@@ -72,3 +72,25 @@ def test_scores_of_minus_infinity(D, new, length, sinks):
     others[:new, 6] = False
     assert out[others].isfinite().all()
     assert (out[new] == 0).all() and torch.equal(lse[new], s if sinks else torch.full((8,), -math.inf))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,length", [(1, 100), (3, 90), (10, 90), (40, 300), (1, 9000), (40, 9000)])
+def test_sinks_without_end(D, new, length):
+    """A sink of inf takes all of the weight; one of -inf none."""
+    m = _m()
+    b = Batch([length], D, 2, 16, 2)
+    q = torch.randn(new, 8, D, generator=torch.Generator().manual_seed(3)).to(BF16)
+    args = (q.cuda(), b.cache.cuda(), b.tables.cuda(), ints([length]), ints([0, new]))
+    s = torch.tensor([math.inf, -math.inf, 0.0, math.inf] * 2, device="cuda")
+    out, lse = m.fp4_attention(*args, sinks=s, return_lse=True)
+    plain, plain_lse = m.fp4_attention(*args, return_lse=True)
+    assert (out[:, [0, 3, 4, 7]] == 0).all() and (lse[:, [0, 3, 4, 7]] == math.inf).all()
+    assert torch.equal(out[:, [1, 5]], plain[:, [1, 5]]) and torch.equal(lse[:, [1, 5]], plain_lse[:, [1, 5]])
+    s[0] = 3e38  # (in units of log 2 past FP32)
+    out, lse = m.fp4_attention(*args, sinks=s, return_lse=True)
+    assert (out[:, 0] == 0).all() and (lse[:, 0] == s[0]).all()
+    bad = q.clone()
+    bad[0, 0, 3] = math.nan
+    out, lse = m.fp4_attention(bad.cuda(), *args[1:], sinks=s, return_lse=True)
+    assert out[0, 0].isnan().all() and lse[0, 0].isnan() and (out[:, 3] == 0).all()

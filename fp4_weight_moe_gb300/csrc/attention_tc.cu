@@ -207,6 +207,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   // first half), their scores' largest, their divisors
   __shared__ float told[2][C::kRows];
   __shared__ uint32_t dead[4 * kTiles];  // a wait of a row's gave up
+  __shared__ float far_fac[32 * C::kSoftWarps];  // of threads whose scores are large: their factor
   if (threadIdx.x < 4 * kTiles) dead[threadIdx.x] = 0;  // (seen behind the barrier below)
   int left;  // units of the stretch that are left
   {
@@ -514,13 +515,14 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           // masked where they are, so that the loop below has no test for it
           // (as predicates there, they took as many instructions as the rest)
           const int hi = min(pos, p.capacity - 1) - tok0 - col0, lo = lowest - tok0 - col0;
+          const float by = whole_lo == INT_MAX ? far_fac[threadIdx.x] : 1.f;
 #pragma unroll 1
           for (int x = 0; x < C::kCols; x += 16) {
             uint32_t s[16];
             tmem_ld16(s_tmem + x, s);
 #pragma unroll
             for (int y = 0; y < 16; ++y)
-              if (x + y > hi || x + y < lo) s[y] = 0xff800000u;
+              s[y] = x + y > hi || x + y < lo ? 0xff800000u : __float_as_uint(__fmul_rn(__uint_as_float(s[y]), by));
             tmem_st16(s_tmem + x, s);
           }
           tmem_wait_st();
@@ -569,6 +571,23 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
           m = next;
           l.x *= by;
           l.y *= by;
+          // Where a unit of m, a rounded product, is no small number, the others
+          // have to be rounded before m is taken away, too (fused, the largest's
+          // distance would be anything): from here on they are, where they lie.
+          if (__any_sync(0xffffffffu, fabsf(m) > 0x1p20f && m != -INFINITY) && whole_lo != INT_MAX) {
+#pragma unroll 1
+            for (int x = 0; x < C::kCols; x += 16) {
+              uint32_t s[16];
+              tmem_ld16(s_tmem + x, s);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) s[y] = __float_as_uint(__fmul_rn(__uint_as_float(s[y]), fac));
+              tmem_st16(s_tmem + x, s);
+            }
+            tmem_wait_st();
+            far_fac[threadIdx.x] = fac;
+            fac = 1.f;
+            whole_lo = INT_MAX;
+          }
           if (i > 0) {
             if (!wait(&pv_done[n], step - 1)) {
               ok = kSides == 2;

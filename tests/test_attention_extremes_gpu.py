@@ -94,3 +94,31 @@ def test_sinks_without_end(D, new, length):
     bad[0, 0, 3] = math.nan
     out, lse = m.fp4_attention(bad.cuda(), *args[1:], sinks=s, return_lse=True)
     assert out[0, 0].isnan().all() and lse[0, 0].isnan() and (out[:, 3] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 3, 10, 40])
+@pytest.mark.parametrize("scale", [1e4, -1e6, 1e8, 1e15, 1e30])
+def test_scores_far_apart(D, new, scale):
+    """Scores so large that one key has all of the weight, and that a unit of FP32 at theirs is many powers of two."""
+    m = _m()
+    L = 500
+    b = Batch([L], D, 2, 16, 3)
+    q = torch.randn(new, 8, D, generator=torch.Generator().manual_seed(4)).to(BF16)
+    out, lse = m.fp4_attention(q.cuda(), b.cache.cuda(), b.tables.cuda(), ints([L]), ints([0, new]), scale=scale,
+                               return_lse=True)
+    out, lse = out.double().cpu(), lse.double().cpu()
+    sees = torch.arange(L) <= torch.arange(new)[:, None] + (L - new)
+    clear = 0
+    for h in range(8):
+        k, v = b.k[0][:, h // 4], b.v[0][:, h // 4]
+        x = (q[:, h].double() @ k.T * scale).masked_fill(~sees, -math.inf)
+        off = 2.0 ** -18 * float(((q[:, h].double().abs() @ k.abs().T) * abs(scale)).max())
+        top = x.topk(2, 1)
+        # (where the second lies below by more than both may be off by, and by 20 besides: e^-20 of its value)
+        first = top.values[:, 0] - top.values[:, 1] > 2 * off + 20
+        want = v[top.indices[:, 0]]
+        assert ((out[:, h] - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -20 * v.abs().max())[first].all()
+        assert ((lse[:, h] - top.values[:, 0]).abs() <= off + 2.0 ** -20 * top.values[:, 0].abs())[first].all()
+        clear += int(first.sum())
+    assert clear >= 4 * new

@@ -484,9 +484,9 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
       {
         const int rows = c.rows(p), base_pos = c.q.length - c.q.n;
         pos = tile_row < rows ? base_pos + attn_row(p, tile_rows, tile_row).query : -1;
-        lowest = p.a.window > 0 ? max(pos - p.a.window + 1, 0) : 0;
+        lowest = p.a.window > 0 ? max(max(pos, 0) - p.a.window + 1, 0) : 0;
         const int pos_last = base_pos + attn_row(p, tile_rows, min(128 * n + 128, rows) - 1).query;
-        whole_lo = p.a.window > 0 ? max(pos_last - p.a.window + 1, 0) : 0;
+        whole_lo = p.a.window > 0 ? max(max(pos_last, 0) - p.a.window + 1, 0) : 0;
         whole_hi = min(base_pos + attn_row(p, tile_rows, 128 * n).query, p.capacity - 1);
       }
 

@@ -44,8 +44,14 @@ constexpr int kPair = 2 * kCacheBlock;  // tokens that a warp takes in one go: t
 // 128 requests: 16.4 us; with the four warps of a CTA to an item 24.4).
 constexpr int kTeamSpan = 64;
 // Items of at most so many pairs are one worker's: a warp takes 0.6 us a pair by
-// itself, a part and its join about 4 us.
+// itself, a part and its join about 4 us (64 / 8 heads of 64, windows of 128:
+// 16.3 us, with 3 pairs 22.1; 32 / 8 heads of 128, 64 requests of 300 tokens:
+// 21.7 us, with 12 pairs 25.7, though 256 of them take 46 and 31).
 constexpr int kWholePairs = 6;
+// Pairs that are worth a worker, where there are workers to spare (32 / 8 heads
+// of 128: 64 requests of 300 tokens 21.7 us, with 1 pair 23.5, with 8 26.2; one
+// request of 300 13.4, 10.4, 16.8; one of 1000 12.6, 11.9, 15.5).
+constexpr int kLeastPairs = 4;
 constexpr uint32_t kWaitCode = 1u;
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -534,7 +540,7 @@ cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int grid = max_ctas(sms, D, NT);
   p.workers = grid * kWarps;
-  p.least = 4;
+  p.least = kLeastPairs;
   e = launch_dependent_smem(attention_rows_kernel<D, NT>, (unsigned)grid, kThreads, C::kSmem, st, p);
   if (e != cudaSuccess) return e;
   // few items: many parts to each, joined by more CTAs (one request of 4096
@@ -546,10 +552,20 @@ cudaError_t launch_rows(AttnArgs p, int sms, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_dim(const AttnArgs& p, int sms, cudaStream_t st) {
-  // Rows that an average request has to a key head.  Up to 8 fill one product
-  // of 8 columns and up to 16 two (16 requests of 16384 tokens, some four
-  // queries of four heads each: 96 us; on tiles of 128 rows, whose decoding
-  // warps bring 2.9 TB/s, 180).
+  // Rows that an average request has to a key head: up to 8 fill one product of
+  // 8 columns, up to 16 two, more go to tiles of 128.  16 requests of 16384
+  // tokens, 8 key heads of 128, us:
+  //   rows                      4     8    12    16    20    32    48    64
+  //   one product, again       65    66   113   113
+  //   two products, again      85    86    87    88   156   157   223   291
+  //   tiles                   174   175   175   176   176   176   180   181
+  // (From 17 to 32 rows tiles take a tenth longer at these sizes, 81 for 67 with
+  // 64 requests of 1000 tokens, 157 for 102 with heads of 64.)  It is
+  // one kernel for a call, by the mean over all requests and with rows of q
+  // behind the last sequence: requests of other kinds in a batch are served by
+  // the wrong one (63 single tokens behind 8192 and a chunk of 2048, 32 / 8
+  // heads: 643 us, 112 and 236 apart; 255 and a chunk of 512: 842, 406 and 91;
+  // 64 single tokens 113, padded to 256 rows 155).
   const int64_t rows = p.a.R > 0 ? (int64_t)p.a.T * p.group / p.a.R : 0;
   if (rows > 16) return launch_attention_tc(p, (int)rows, sms, st);
   return rows > 8 ? launch_rows<D, 2>(p, sms, st) : launch_rows<D, 1>(p, sms, st);

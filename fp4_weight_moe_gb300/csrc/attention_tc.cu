@@ -25,9 +25,12 @@
 // tokens: 640 instructions a warp, between waits on tensor memory) and its two
 // products (1090), of which two tiles hide one another's in part: the tensor
 // cores are busy 47% of the time (chunks of 2048 tokens behind 8192, 32 query
-// heads, D = 128: 578 us, 1.07 PFLOP/s).  With one tile by the decode warps,
-// 900 cycles for half a step, and by issue (35 rows of five requests of 100000
-// tokens 250 us).
+// heads, D = 128: 580 us, 1.07 PFLOP/s).  With one tile by what a step hands
+// over from one to the next, whatever number of its rows is real: 16 requests of
+// 16384 tokens (32 / 8 heads of 128, 302 MB) take 176 us with 20 rows and 186
+// with 128, 3400 cycles a step.  Left out, the decoding (141 us), the softmax
+// (158), the copies (168), all three (120) show that none of them is the bound:
+// the last is the products, 590 cycles each, and their signals, in turn.
 //
 // m follows the scores only when they outgrow it by 2^kMost, to 2^kBelow below
 // them (p stays within FP16, sums and divisor are taken against the same m), so
@@ -39,6 +42,13 @@
 namespace moe_fp4 {
 
 namespace {
+
+// Items of at most so many steps are one worker's (40 rows, 32 / 8 heads of 128:
+// 64 requests of 200 tokens 42.1 us, with 1 step 45.2; 8 requests of 1000 24.0,
+// with 8 steps 25.3; in between 64 of 300 tokens would take 47 with 4, not 56),
+// and steps that are worth a worker (8 requests of 1000 tokens 24.0 us, with 1
+// step 28.8, with 8 24.8; one of 16384 38.7, 38.7, 29.2).
+constexpr int kWholeSteps = 2, kLeastSteps = 4;
 
 template <int D, int kTiles_>
 struct TcCfg {
@@ -52,7 +62,7 @@ struct TcCfg {
   static constexpr uint32_t kHalf = kBlocks * cache_half_bytes(D);
   static constexpr int kRaw = D == 64 || (D == 128 && kTiles == 1) ? 6 : 3;  // half steps in flight
   // A row's threads: two with one tile, which has no other tile's products to
-  // hide its softmax (35 rows of five requests of 100000 tokens 273 us with
+  // hide its softmax (35 rows of five requests of up to 100000 tokens 273 us with
   // one, 257 with two); two tiles have, and twice the warps take more
   // instructions (chunks of 2048 tokens 586 us with one, 611 with two).
   static constexpr int kSides = kTiles == 1 ? 2 : 1;
@@ -201,8 +211,8 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   pdl_launch_dependents();
   // each warp's place in its CTA's stretch (in shared memory: its registers
   // are worth more to the loops between items)
-  __shared__ AttnCursor<C::kRows, kTok, 2> cursors[C::kThreads / 32];
-  AttnCursor<C::kRows, kTok, 2>& c = cursors[warp];
+  __shared__ AttnCursor<C::kRows, kTok, kWholeSteps> cursors[C::kThreads / 32];
+  AttnCursor<C::kRows, kTok, kWholeSteps>& c = cursors[warp];
   // what the threads of a row tell each other: its queries' factor (in the
   // first half), their scores' largest, their divisors
   __shared__ float told[2][C::kRows];
@@ -213,7 +223,7 @@ __global__ void __launch_bounds__(TcCfg<D, kTiles>::kThreads, 1) attention_tc_ke
   {
     int64_t u, u_end;
     int team;
-    AttnCursor<C::kRows, kTok, 2> start;
+    AttnCursor<C::kRows, kTok, kWholeSteps> start;
     if (!attn_stretch<C::kRows, kTok, C::kThreads, 1, 0>(p, start, u, u_end, team)) return;
     if (lane == 0) c = start;
     __syncwarp();
@@ -717,15 +727,16 @@ cudaError_t launch_tiles(AttnArgs p, int sms, cudaStream_t st) {
   e = attention_status_address(&err);
   if (e != cudaSuccess) return e;
   p.workers = sms;
-  p.least = 4;
+  p.least = kLeastSteps;
   e = launch_dependent_smem(attention_tc_kernel<D, kTiles>, (unsigned)sms, C::kThreads, C::kSmem, st, p, static_cast<uint32_t*>(err));
   if (e != cudaSuccess) return e;
   return launch_attention_join<D, C::kRows, 8>(p, sms, st);
 }
 
 // Tiles of rows side by side: two, but where D = 256 leaves room for the sums
-// of one, and where an average request has rows for one (35 rows of five
-// requests of 100000 tokens: on two 316 us, on one 273, two threads to a row 250).
+// of one, and where an average request has rows for one (16 requests of 16384
+// tokens, 32 / 8 heads of 128: 128 rows 186 us on one, 230 on two; 160 rows 336
+// and 244; 2 requests of 4096, 256 rows: 37.5 and 31.4).
 constexpr int most_tiles(int D) { return D <= 128 ? 2 : 1; }
 
 template <int D>

@@ -217,7 +217,9 @@ __device__ __forceinline__ AttnBlind attn_blind(const AttnArgs& p, const AttnReq
 // Every CTA finds the line's length and its worker's stretch [u, u_end) of
 // it, or each of its warps' own (then `team` is 1; CTA 0 writes the line
 // down); false where it has none.  Items that average fewer units than
-// kTeamSpan go to warps (kTeams warps of a CTA can be workers).
+// kTeamSpan go to warps (kTeams warps of a CTA can be workers).  A request's
+// tiles are gone through by one thread, in every CTA: of a prompt of 131072
+// tokens under a window of 128 (64 / 8 heads) that is some 8% of 3.2 ms.
 template <int kRows, int kUnit, int kThreads, int kTeams, int kTeamSpan, int kWhole>
 __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows, kUnit, kWhole>& cursor, int64_t& u,
                                              int64_t& u_end, int& team) {
@@ -541,6 +543,10 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(AttnArgs p
   }
 }
 
+// Its CTAs, 4 and 8 an SM: with a quarter of them five queries of 16 requests
+// of 16384 tokens take 102 us instead of 97, chunks of 2048 behind 8192 599
+// instead of 580; with twice as many one request of 4096 13.2 instead of 12.2
+// (and those 16 requests 93).
 template <int D, int kRows, int kJoin>
 cudaError_t launch_attention_join(const AttnArgs& p, int sms, cudaStream_t st) {
   const int grid = min(p.workers * (kRows / kJoin), (kRows > 16 ? 8 : 4) * sms);

@@ -805,7 +805,9 @@ MOE_FP4_API int moe_fp4_cache_step(const moe_fp4_cache_step_args *args, void *st
  * Arithmetic is FP32 with one rounding to bf16; the keys on their way to the
  * cache carry twice that, so that what is quantised is the FP32 number next
  * to the formula's (of offset + w, rounded to FP32) and its codes do not
- * depend on the order of sums.
+ * depend on the order of sums; for mean(x^2) + eps in [2^-80, 2^100] (past
+ * FP32's range a sum of squares is inf and y 0, without eps below it 0 and y
+ * inf or NaN).
  * w_q, w_k [D] bf16, or f32 (weights_f32).  positions int32 or int64
  * (positions_i64), slots int64.  rot % 16 == 0, rot <= D
  * (MOE_FP4_EUNSUPPORTED).  16-byte aligned arrays, strides that are
@@ -864,8 +866,12 @@ MOE_FP4_API int moe_fp4_cache_read(const void *cache, int pages, int page_size, 
  * elements (MOE_FP4_EINVAL); Hq % Hkv == 0, Hq / Hkv <= 64, R <= 65536,
  * table_width * page_size <= 2^31 - 1024, T * Hq < 2^31
  * (MOE_FP4_EUNSUPPORTED).  workspace: moe_fp4_attention_workspace_bytes
- * bytes, 256-byte aligned, no initialisation needed; calls that may run at
- * the same time need workspaces of their own.
+ * bytes (20 to 41 MB, which today follow from D and the current device alone),
+ * 256-byte aligned, no initialisation needed; calls that may run at the same
+ * time need workspaces of their own.
+ * The kernel is chosen for a call, by T * Hq / Hkv / R: single tokens beside a
+ * prompt's chunk, or with many rows of q behind offsets[R], take up to three
+ * times as long as in calls of their own.
  */
 typedef struct moe_fp4_attention_args {
   const void *q;

@@ -107,3 +107,19 @@ def test_not_finite_of_many_tokens():
     m.qk_norm_rope(k[:, :1], k, None, None, *(x.cuda() for x in w), v=v, cache=cache, slots=slots)
     rk, _ = m.fp4_cache_read(cache, slots)
     assert torch.equal(rk.isnan().all(-1).cpu(), bad) and torch.equal(rk.isnan().any(-1).cpu(), bad)
+
+
+@pytest.mark.parametrize("power", [-39, -20, 20, 46])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_stored_keys_far_from_one(D, power):
+    """The norm takes a key's size away, without eps too: within the range that is stated, to the last code."""
+    m = _m()
+    T, Hkv = 500, 3
+    q, k, v, wq, wk = inputs(T, 2, Hkv, D, 9 + D)
+    k = (k.double() * 2.0 ** power).to(BF16)
+    table, pos = m.rotary_table(600, D, device="cpu"), torch.arange(T, dtype=torch.int32)
+    cache, slots = m.alloc_fp4_cache(T // 16 + 1, 16, Hkv, D), torch.arange(T)
+    m.qk_norm_rope(q, k, pos.cuda(), table.cuda(), wq.to(BF16).cuda(), wk.to(BF16).cuda(), eps=0.0, v=v, cache=cache,
+                   slots=slots.cuda())
+    kf = formula(k.cpu(), wk.to(BF16), table[:T], 0.0, 0.0, False)[0].float()
+    assert torch.equal(stored(cache.cpu(), slots, D)[0], dequantise(*quantise(kf)))

@@ -237,7 +237,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
     Returns ``(q', k')`` in bfloat16.  With a ``cache`` (``alloc_fp4_cache``),
     ``v [T, kv_heads, D]`` and ``slots [T]`` (int64; -1: not stored), k' and v
     go there in 4 bits instead, divided by ``k_scale`` and ``v_scale``, and
-    k' is None."""
+    k' is None.  (Keys without a weight are computed twice on their way there:
+    8192 tokens of 32 and 8 heads of 128 in 58 us, with one in 46.)"""
     if stream is not None:
         with _on(stream, q):
             return qk_norm_rope(q, k, positions, rotary, q_weight, k_weight, eps, weight_offset, interleaved, v, cache,
@@ -324,7 +325,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: Optional[torch.Ten
 # -------------------------------------------------------------------- attention
 def alloc_fp4_attention_workspace(R_max: int, heads: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
     """A workspace for ``fp4_attention(..., workspace=...)`` of up to R_max
-    requests."""
+    requests: 20 (head_dim 64) to 41 MB, however many they are."""
     n = _capi.moe_fp4_attention_workspace_bytes(R_max, heads, kv_heads, head_dim)
     if n == 0:
         raise _capi.MoeFp4Error("moe_fp4_attention_workspace_bytes", _capi.MOE_FP4_EUNSUPPORTED)
@@ -378,7 +379,11 @@ def fp4_attention(q: torch.Tensor, cache: torch.Tensor, tables: torch.Tensor, le
     divisor, float32 ``[T, heads]``.  Queries that see no key, and rows of q
     behind the last sequence, get 0 (and sinks[h] or -inf; behind the last
     sequence -inf).  ``workspace`` (alloc_fp4_attention_workspace) is scratch;
-    without one the call takes it from torch's allocator."""
+    without one the call takes it, 20 to 41 MB, from torch's allocator.
+
+    One kernel serves a call, chosen by its mean number of rows (T * heads /
+    kv_heads / R): single tokens beside a prompt's chunk, or padded by many
+    rows of q, run up to three times as long as in calls of their own."""
     if stream is not None:
         with _on(stream, q):
             return fp4_attention(q, cache, tables, lengths, offsets, scale, window, sinks, k_scale, v_scale, out,

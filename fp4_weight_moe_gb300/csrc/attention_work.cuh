@@ -315,7 +315,8 @@ __device__ __forceinline__ bool attn_stretch(const AttnArgs& p, AttnCursor<kRows
   cursor.start(p, found[i], found_rest[i]);
   const bool passes = cursor.from > 0 && cursor.span.units <= kWhole;  // (an item that a worker before has whole)
   if (team == 1 && kTeams > 1 ? lane == 0 : threadIdx.x == 0)
-    p.places[w] = {cursor.q.row0, cursor.q.length - cursor.q.n, cursor.tile, cursor.head, cursor.rows(p), passes ? 0 : cursor.from, cursor.span.units};
+    p.places[w] = {cursor.q.row0, cursor.q.length - cursor.q.n, cursor.tile, cursor.head, cursor.rows(p),
+                   passes ? 0 : cursor.from, cursor.span.units};
   if (passes) {
     u += cursor.span.units - cursor.from;
     if (u < u_end) cursor.next(p);
